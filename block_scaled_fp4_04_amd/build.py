@@ -15,8 +15,10 @@ LIB = os.path.join(PKG, "libnvfp4.so")
 SOURCES = [os.path.join(CSRC, "nvfp4_api.cpp"), os.path.join(CSRC, "nvfp4_plan.cpp"),
            os.path.join(CSRC, "nvfp4_sequence.cpp"), os.path.join(CSRC, "nvfp4_kernels.hip"), os.path.join(CSRC, "nvfp4_grouped.hip"),
            os.path.join(CSRC, "nvfp4_quantize.hip"), os.path.join(CSRC, "nvfp4_probe.hip"),
-           os.path.join(CSRC, "nvfp4_noalloc.hip")]
-# what the kernels and their launches are built from
+           os.path.join(CSRC, "nvfp4_noalloc.hip"), os.path.join(CSRC, "nvfp4_mx_api.cpp"),
+           os.path.join(CSRC, "nvfp4_mx_quantize.hip"), os.path.join(CSRC, "nvfp4_mx_gemm.hip"),
+           os.path.join(CSRC, "nvfp4_moe.hip")]
+# what the kernels that a plan table times, and their launches, are built from
 KERNEL_FILES = [os.path.join(CSRC, f) for f in ("nvfp4_kernels.hip", "nvfp4_grouped.hip",
                                                 "nvfp4_quantize.hip", "nvfp4_internal.h",
                                                 "nvfp4_device.h", "nvfp4_quant_device.h")]

@@ -131,6 +131,12 @@ int get_workspace(int device, void* stream, const Job& job, WorkspacePtrs* out) 
     return NVFP4_OK;
 }
 
+}  // namespace
+
+// ---- jobs ---------------------------------------------------------------------
+
+namespace nvfp4 {
+
 // Runs a prepared job eagerly on `stream` with that stream's workspace.
 int run_job(const Job& job, void* stream) {
     int device = 0;
@@ -144,12 +150,6 @@ int run_job(const Job& job, void* stream) {
     const hipError_t e = launch_job(job, device, ws, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
-
-}  // namespace
-
-// ---- jobs ---------------------------------------------------------------------
-
-namespace nvfp4 {
 
 int current_device(int* device) {
     if (hipGetDevice(device) != hipSuccess) return NVFP4_ERR_HIP;
@@ -369,6 +369,7 @@ int prepare_gemm_quantized(const void* x, int x_type, int64_t ldx, const void* b
 
 hipError_t launch_job(const Job& job, int device, const WorkspacePtrs& ws, hipStream_t s) {
     if (job.empty) return hipSuccess;
+    if (job.launch) return job.launch(job, s);
     if (job.kind == JOB_GEMV_QUANT) return launch_gemv_quant(job.gemvq, s);
     if (job.kind == JOB_GROUPED) return launch_grouped(job.grouped, s);
     if (job.kind == JOB_GROUPED_TILE) return launch_grouped_tile(job.gemm, s);

@@ -7,7 +7,10 @@
 #include <stdint.h>
 
 #include "nvfp4_internal.h"
+#include "nvfp4_mx_internal.h"
 #include "nvfp4_plan.h"
+
+struct nvfp4_sequence;
 
 namespace nvfp4 {
 
@@ -17,7 +20,8 @@ enum JobKind {
     JOB_QUANTIZE = 2,
     JOB_GROUPED_TILE = 3,
     JOB_GEMV_QUANT = 4,
-    JOB_GROUPED_WSPLIT = 5
+    JOB_GROUPED_WSPLIT = 5,
+    JOB_LAUNCH = 6  // launched by Job::launch
 };
 
 struct Job {
@@ -30,6 +34,12 @@ struct Job {
     GroupedArgs grouped{};       // JOB_GROUPED, JOB_GROUPED_WSPLIT
     QuantArgs quant{};           // JOB_QUANTIZE
     GemvQuantArgs gemvq{};       // JOB_GEMV_QUANT
+    // The MXFP4 operators and the expert routing: what launches the job (no
+    // workspace), and its arguments; null for the kinds above.
+    hipError_t (*launch)(const Job&, hipStream_t) = nullptr;
+    MxQuantArgs mx_quant{};
+    MxGemmArgs mx_gemm{};
+    MoeArgs moe{};
     bool empty = false;          // nothing to launch (a grouped GEMM with no rows)
 };
 
@@ -62,5 +72,12 @@ struct WorkspacePtrs {
 // Enqueues a prepared job on `stream`, with the split-K workspace given
 // (null pointers when the job needs none).
 hipError_t launch_job(const Job& job, int device, const WorkspacePtrs& ws, hipStream_t stream);
+
+// Runs a prepared job eagerly on `stream` with that stream's workspace.
+int run_job(const Job& job, void* stream);
+
+// Appends a prepared job to a sequence (status: of its preparation, returned
+// if it is an error).
+int sequence_add(nvfp4_sequence* seq, int status, const Job& job);
 
 }  // namespace nvfp4

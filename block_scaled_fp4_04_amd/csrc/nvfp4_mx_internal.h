@@ -1,0 +1,85 @@
+// nvfp4_mx_internal.h -- launch arguments shared by the host library and the gfx950
+// kernels of the MXFP4 operators (include/nvfp4_mx.h) and of the expert
+// routing (include/nvfp4_moe.h); not part of the public ABI.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace nvfp4 {
+
+// Packed MXFP4 geometry (include/nvfp4_mx.h, "Packed layout").
+constexpr int kMxBlock = 32;     // elements that share a scale
+constexpr int kMxStep = 128;     // elements of a row per step (one MFMA deep)
+constexpr int kMxRows = 16;      // rows of a row block
+constexpr int kMxFrag = 1024;    // code bytes of 16 rows x one step
+constexpr int kMxScaleFrag = 256;  // scale bytes of 16 rows x four steps
+
+inline int64_t mx_round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+inline int64_t mx_steps(int64_t K) { return mx_round_up(K, kMxStep) / kMxStep; }
+inline int64_t mx_row_blocks(int64_t rows) { return mx_round_up(rows, kMxRows) / kMxRows; }
+
+// Quantisation (x -> codes, scales) or its inverse (codes, scales -> x).
+struct MxQuantArgs {
+    void* x;               // groups x rows x K values (fp32, or bfloat16 if bf16)
+    bool bf16;
+    uint8_t* codes;        // groups x [RB][C][4][16][16]
+    uint8_t* scales;       // groups x [RB][Q][4][16][4]
+    int64_t group_stride;  // elements between groups of x
+    int64_t ld;            // elements between rows of x
+    int64_t groups;
+    int rows, K;
+    int RB, C;             // row blocks of a group, steps
+};
+hipError_t launch_mx_quantize(const MxQuantArgs& a, hipStream_t stream);
+hipError_t launch_mx_dequantize(const MxQuantArgs& a, hipStream_t stream);
+
+// Product C = alpha * A . B^T, single (groups = 0) or grouped.
+struct MxGemmArgs {
+    const uint8_t* a_codes;    // packed A, or null
+    const uint8_t* a_scales;
+    const void* x;             // A as fp32 / bfloat16 rows (a_codes null), row stride ldx elements
+    int64_t ldx;
+    const uint8_t* b_codes;    // packed B (groups of them)
+    const uint8_t* b_scales;
+    const int32_t* offsets;    // [groups + 1] row offsets (device), or null
+    const int32_t* a_rows;     // [M] row of A of each output row (device), or null: the row itself
+    void* out;                 // M x N, fp32 or bfloat16
+    float alpha;
+    int M, N, K;               // output rows, output columns, depth
+    int A_rows;                // logical rows of A
+    int RBa, RBb;              // row blocks of A, of one B
+    int C;                     // steps
+    int groups;
+    bool x_bf16, out_bf16;
+};
+// Rows of A up to which the one-launch product from activations runs.
+constexpr int kMxQuantRows = 64;
+hipError_t launch_mx_gemm(const MxGemmArgs& a, hipStream_t stream);
+// Whether the grid of the kernel that the sizes choose stays within the
+// runtime's limit on work-items.
+bool mx_gemm_fits(const MxGemmArgs& a);
+
+// Expert routing.
+constexpr int kMoeMaxExperts = 2048;
+struct MoeArgs {
+    const void* ids;         // tokens x topk expert numbers (int32, or int64 if wide)
+    bool wide;
+    bool bf16;               // element type of the rows: bfloat16, else fp32
+    int64_t tokens;
+    int topk, experts;
+    int64_t hidden, ld_in;   // row length, row stride of the input in token order
+    int32_t* row_offsets;    // [experts + 1]
+    int32_t* slots;          // [tokens][topk]
+    int32_t* row_tokens;     // [tokens * topk]
+    const void* x;           // gather: token rows; combine: expert-order rows
+    const void* y;           // combine_grad: expert-order rows
+    const float* weights;    // [tokens][topk], or null: ones
+    void* out;               // gather, combine: result; combine_grad: dy
+    float* dweights;         // combine_grad
+};
+hipError_t launch_moe_sort(const MoeArgs& a, hipStream_t stream);
+hipError_t launch_moe_gather(const MoeArgs& a, hipStream_t stream);
+hipError_t launch_moe_combine(const MoeArgs& a, hipStream_t stream);
+hipError_t launch_moe_combine_grad(const MoeArgs& a, hipStream_t stream);
+
+}  // namespace nvfp4

@@ -74,6 +74,20 @@ int capture(nvfp4_sequence* seq) {
 
 }  // namespace
 
+namespace nvfp4 {
+
+int sequence_add(nvfp4_sequence* seq, int status, const Job& job) {
+    if (!seq) return NVFP4_ERR_INVALID_VALUE;
+    if (seq->finalized) return NVFP4_ERR_STATE;
+    try {
+        return add_job(seq, status, job);
+    } catch (const std::bad_alloc&) {
+        return NVFP4_ERR_ALLOC;
+    }
+}
+
+}  // namespace nvfp4
+
 extern "C" {
 
 int nvfp4_sequence_create(nvfp4_sequence_t* seq) {

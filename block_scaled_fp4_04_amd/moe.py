@@ -1,0 +1,191 @@
+"""Python binding of expert routing (``include/nvfp4_moe.h``): a router's
+choices sorted by expert, token rows laid out in that order for a grouped
+product, added up again under the router's weights, and the gradients.
+Argument marshalling only.
+
+    route = moe_sort(expert_ids, experts)
+    y = mx_grouped_gemm(mx_quantize(x), w, route.row_offsets, rows=route.tokens)
+    out = moe_combine(y, route, weights)
+
+or, for a product that reads its rows in order (``grouped_gemm``), with
+``moe_gather(x, route)`` in front of it.
+"""
+from __future__ import annotations
+
+import ctypes
+from dataclasses import dataclass
+
+from . import _i64, _vp, lib
+from .mx import _device_of, _rows_2d, _run
+
+INDEX_I32 = 0   # types of expert numbers (nvfp4_moe.h)
+INDEX_I64 = 1
+MOE_MAX_EXPERTS = 2048
+
+MOE_EXPORTS = ["nvfp4_moe_sort", "nvfp4_moe_gather", "nvfp4_moe_combine",
+               "nvfp4_moe_combine_grad", "nvfp4_sequence_add_moe_sort",
+               "nvfp4_sequence_add_moe_gather", "nvfp4_sequence_add_moe_combine"]
+
+_int = ctypes.c_int
+_SORT = [_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp]
+_GATHER = [_vp, _int, _i64, _i64, _i64, _i64, _vp, _vp]
+_COMBINE = [_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp]
+_GRAD = [_vp, _i64, _vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _vp]
+_bound = None
+
+
+def moe_lib() -> ctypes.CDLL:
+    """The library with the argument types of its routing functions set."""
+    global _bound
+    L = lib()
+    if _bound is not L:
+        for name, types in (("nvfp4_moe_sort", _SORT + [_vp]), ("nvfp4_moe_gather", _GATHER + [_vp]),
+                            ("nvfp4_moe_combine", _COMBINE + [_vp]),
+                            ("nvfp4_moe_combine_grad", _GRAD + [_vp]),
+                            ("nvfp4_sequence_add_moe_sort", [_vp] + _SORT),
+                            ("nvfp4_sequence_add_moe_gather", [_vp] + _GATHER),
+                            ("nvfp4_sequence_add_moe_combine", [_vp] + _COMBINE)):
+            f = getattr(L, name)
+            f.restype, f.argtypes = _int, types
+        _bound = L
+    return L
+
+
+@dataclass
+class MoeRoute:
+    """A router's choices sorted by expert (int32 device tensors):
+    ``row_offsets`` [experts + 1] where each expert's rows begin, ``slots``
+    [tokens, topk] the row of each choice (-1: dropped) and ``tokens``
+    [tokens * topk] the token of each row (-1 behind the last one)."""
+    row_offsets: "object"
+    slots: "object"
+    tokens: "object"
+    experts: int
+
+    def check(self) -> None:
+        import torch
+        n = self.slots.numel()
+        for what, t, ok in (("row_offsets", self.row_offsets, self.row_offsets.numel() == self.experts + 1),
+                            ("slots", self.slots, self.slots.dim() == 2),
+                            ("tokens", self.tokens, self.tokens.numel() == n)):
+            if t.dtype != torch.int32 or not t.is_contiguous() or not ok:
+                raise ValueError(f"route.{what} must be a contiguous int32 tensor of its shape")
+
+
+def _sort_args(ids, experts, out):
+    import torch
+    if ids.dim() != 2 or ids.dtype not in (torch.int32, torch.int64) or not ids.is_contiguous():
+        raise ValueError("expert_ids must be a contiguous [tokens, topk] int32 or int64 tensor")
+    T, k = ids.shape
+    if out is None:
+        both = torch.empty(2 * T * k + experts + 1, dtype=torch.int32, device=ids.device)
+        out = MoeRoute(both[2 * T * k:], both[:T * k].view(T, k), both[T * k:2 * T * k], experts)
+    else:
+        out.check()
+        if out.experts != experts or tuple(out.slots.shape) != (T, k):
+            raise ValueError("out has the wrong shape")
+    return out, (ids.data_ptr(), INDEX_I64 if ids.dtype is torch.int64 else INDEX_I32, T, k,
+                 experts, out.row_offsets.data_ptr(), out.slots.data_ptr(), out.tokens.data_ptr())
+
+
+def moe_sort(expert_ids, experts: int, out: MoeRoute | None = None, stream=None) -> MoeRoute:
+    """Sort a router's choices, ``expert_ids`` [tokens, topk] (int32 or int64
+    device tensor; numbers outside [0, experts) are dropped choices), by
+    expert, those of one expert by token (nvfp4_moe_sort).  At most
+    MOE_MAX_EXPERTS experts."""
+    out, args = _sort_args(expert_ids, experts, out)
+    _run(moe_lib().nvfp4_moe_sort, "nvfp4_moe_sort", args,
+         _device_of(expert_ids, out.row_offsets, out.slots, out.tokens), stream)
+    return out
+
+
+def _weights(weights, route):
+    import torch
+    if weights is None:
+        return None
+    if (weights.dtype != torch.float32 or weights.shape != route.slots.shape
+            or not weights.is_contiguous()):
+        raise ValueError(f"weights must be a contiguous float32 tensor of shape {tuple(route.slots.shape)}")
+    return weights.data_ptr()
+
+
+def _like(t, name: str, rows: int, hidden: int, dtype, device):
+    """`t` made, or checked to be a contiguous rows x hidden tensor of `dtype`."""
+    import torch
+    if t is None:
+        return torch.empty((rows, hidden), dtype=dtype, device=device)
+    if tuple(t.shape) != (rows, hidden) or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape ({rows}, {hidden})")
+    return t
+
+
+def _gather_args(x, route, out):
+    kind = _rows_2d(x)
+    route.check()
+    T, k = route.slots.shape
+    if x.shape[0] != T:
+        raise ValueError(f"x has {x.shape[0]} rows, the route {T} tokens")
+    out = _like(out, "out", T * k, x.shape[1], x.dtype, x.device)
+    return out, (x.data_ptr(), kind, T, k, x.shape[1], x.stride(0), route.slots.data_ptr(),
+                 out.data_ptr())
+
+
+def moe_gather(x, route: MoeRoute, out=None, stream=None):
+    """The rows of x (tokens x hidden, rows may be strided) in the experts'
+    order, one for each kept choice (nvfp4_moe_gather): [tokens * topk,
+    hidden].  Rows that no choice owns (behind row_offsets[-1]) are left as
+    they were in ``out``."""
+    out, args = _gather_args(x, route, out)
+    _run(moe_lib().nvfp4_moe_gather, "nvfp4_moe_gather", args,
+         _device_of(x, route.row_offsets, route.slots, route.tokens, out), stream)
+    return out
+
+
+def _combine_args(y, route, weights, out):
+    kind = _rows_2d(y, "y")
+    route.check()
+    T, k = route.slots.shape
+    y = _like(y, "y", T * k, y.shape[1], y.dtype, y.device)
+    w = _weights(weights, route)
+    out = _like(out, "out", T, y.shape[1], y.dtype, y.device)
+    return out, (y.data_ptr(), kind, T, k, y.shape[1], route.slots.data_ptr(), w, out.data_ptr())
+
+
+def moe_combine(y, route: MoeRoute, weights=None, out=None, stream=None):
+    """out[t] = sum over token t's kept choices of weights[t, j] * y[row of the
+    choice] (nvfp4_moe_combine), summed in fp32 in the order of j: [tokens,
+    hidden].  ``weights``: float32 [tokens, topk]; None for ones."""
+    out, args = _combine_args(y, route, weights, out)
+    _run(moe_lib().nvfp4_moe_combine, "nvfp4_moe_combine", args,
+         _device_of(y, route.row_offsets, route.slots, route.tokens, weights, out), stream)
+    return out
+
+
+def moe_gather_grad(dout, route: MoeRoute, out=None, stream=None):
+    """The gradient of moe_gather: each token's row is the sum of the
+    gradients ``dout`` [tokens * topk, hidden] of its kept choices' rows."""
+    return moe_combine(dout, route, None, out, stream)
+
+
+def moe_combine_grad(dout, y, route: MoeRoute, weights=None, dy=None, dweights=None, stream=None):
+    """The gradients (dy, dweights) of moe_combine(y, route, weights) for its
+    output's gradient ``dout`` [tokens, hidden] (rows may be strided)
+    (nvfp4_moe_combine_grad).  Rows of dy that no choice owns are left as they
+    were; dweights of dropped choices are zero.  ``dy`` may be y itself."""
+    import torch
+    kind = _rows_2d(dout, "dout")
+    route.check()
+    T, k = route.slots.shape
+    if dout.shape[0] != T:
+        raise ValueError(f"dout has {dout.shape[0]} rows, the route {T} tokens")
+    H = dout.shape[1]
+    y = _like(y, "y", T * k, H, dout.dtype, dout.device)
+    w = _weights(weights, route)
+    dy = _like(dy, "dy", T * k, H, dout.dtype, dout.device)
+    dweights = _like(dweights, "dweights", T, k, torch.float32, dout.device)
+    args = (dout.data_ptr(), dout.stride(0), y.data_ptr(), kind, T, k, H, route.slots.data_ptr(), w,
+            dy.data_ptr(), dweights.data_ptr())
+    _run(moe_lib().nvfp4_moe_combine_grad, "nvfp4_moe_combine_grad", args,
+         _device_of(dout, y, route.row_offsets, route.slots, route.tokens, weights, dy, dweights),
+         stream)
+    return dy, dweights

@@ -1,0 +1,345 @@
+"""MXFP4 operators on the GPU against the 64-bit references of mx_ref.py.
+
+Quantisation is held to every byte of the packed buffers; products to the
+bound of mx_ref.gemm_bound (fp32 sums, one rounding of the output)."""
+from __future__ import annotations
+
+import sys
+
+import numpy as np
+import pytest
+
+import mx_ref
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # collected on CPU hosts, skipped there
+    pytest.skip("no GPU", allow_module_level=True)
+
+import block_scaled_fp4_04_amd as nv  # noqa: E402
+
+DEV = "cuda"
+DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
+EPS = {t: torch.finfo(t).eps for t in DT.values()}
+
+
+def say(msg: str) -> None:
+    print(f"[gpu] {msg}", flush=True)
+    sys.stdout.flush()
+
+
+def rng(*key):
+    return np.random.Generator(np.random.PCG64(list(key)))
+
+
+def host(t):
+    return t.to(torch.float32).cpu().numpy()
+
+
+def equal_bytes(q, x):
+    """The packed operand equals the packed reference of the fp32 rows x."""
+    pc, ps = nv.mx_pack(*mx_ref.quantize(x))
+    gc, gs = q.codes.cpu().numpy(), q.scales.cpu().numpy()
+    assert np.array_equal(gs, ps), f"{np.count_nonzero(gs != ps)} scale bytes differ"
+    assert np.array_equal(gc, pc), f"{np.count_nonzero(gc != pc)} code bytes differ"
+
+
+# ---- quantisation ------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("rows,K,sigma", [(1, 32, 1.0), (16, 128, 1.0), (17, 160, 1e-3), (33, 544, 30.0),
+                                          (100, 6112, 1.0), (5, 8192, 0.02)])
+def test_quantize(rows, K, sigma, dtype):
+    say(f"quantize {rows}x{K} {dtype}")
+    x = torch.from_numpy((rng(rows, K).standard_normal((rows, K)) * sigma).astype(np.float32)).to(DT[dtype])
+    equal_bytes(nv.mx_quantize(x.to(DEV)), host(x))
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_quantize_every_exponent_and_value(dtype):
+    """All finite bfloat16 values beside block maxima of every exponent."""
+    bits = np.arange(65536, dtype=np.uint32) << 16
+    v = bits.view(np.float32)
+    v = v[np.isfinite(v)]
+    x = np.zeros((v.size // 32 * 8, 32), np.float32)
+    for i in range(8):  # eight shifts of the value list against itself: blocks of mixed exponents
+        x[i::8] = np.roll(v, 37 * i)[:v.size // 32 * 32].reshape(32, -1).T if i % 2 else \
+            np.roll(v, 11 * i)[:v.size // 32 * 32].reshape(-1, 32)
+    equal_bytes(nv.mx_quantize(torch.from_numpy(x).to(DT[dtype]).to(DEV)), x)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_quantize_edge_blocks(dtype):
+    big, tiny = 3.3895313892515355e38, 2.0 ** -133   # largest bfloat16, smallest bfloat16 subnormal
+    rows = [np.zeros(32), -np.zeros(32), np.full(32, big), np.full(32, -tiny), np.full(32, 2.0 ** -126),
+            np.array([7.0, 5.0, -5.0, 3.5, 2.5, 1.75, 1.25, 0.75, 0.25, -0.25, 6.0, 7.96875] + [0.5] * 20),
+            np.array([np.nan] + [1.0] * 31), np.array([1.0] * 31 + [np.inf]), np.array([-np.inf] + [0.0] * 31),
+            np.array([big] + [1e-30] * 31), np.array([2.0 ** -125, 2.0 ** -127] * 16)]
+    x = np.array(rows, np.float32)
+    equal_bytes(nv.mx_quantize(torch.from_numpy(x).to(DT[dtype]).to(DEV)), x)
+
+
+def test_quantize_strided_rows_and_groups():
+    g = rng(3)
+    wide = np.full((3, 20, 200), np.nan, np.float32)      # the gaps must not be read
+    wide[:, :18, :160] = g.standard_normal((3, 18, 160))
+    for dtype in DT.values():
+        t = torch.from_numpy(wide).to(dtype).to(DEV)
+        equal_bytes(nv.mx_quantize(t[1, :18, :160]), host(t[1, :18, :160]))
+        q = nv.mx_quantize(t[:, :18, :160])
+        assert (q.groups, q.rows, q.K) == (3, 18, 160)
+        cb, sb = nv.mx_packed_size(18, 160)
+        for i in range(3):
+            one = nv.MxOperand(q.codes[i * cb:(i + 1) * cb], q.scales[i * sb:(i + 1) * sb], 18, 160)
+            equal_bytes(one, host(t[i, :18, :160]))
+
+
+def test_quantize_refuses_misaligned_rows():
+    x = torch.zeros(4, 64 + 4, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(nv.Nvfp4Error) as e:
+        nv.mx_quantize(x[:, :64])                          # rows every 136 bytes
+    assert e.value.status == nv.ERR_INVALID_VALUE
+    with pytest.raises(nv.Nvfp4Error) as e:
+        nv.mx_quantize(torch.zeros(4 * 64 + 4, dtype=torch.bfloat16, device=DEV)[4:].view(4, 64))
+    assert e.value.status == nv.ERR_MISALIGNED
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_dequantize_every_scale_and_code(dtype):
+    codes = np.tile((np.arange(16, dtype=np.uint8) | np.arange(16, dtype=np.uint8)[::-1] << 4)[None], (256, 1))
+    scales = np.arange(256, dtype=np.uint8)[:, None]
+    got = nv.mx_dequantize(nv.mx_to_device(codes, scales), DT[dtype])
+    want = torch.from_numpy(mx_ref.values(codes, scales)).to(torch.float32).to(DT[dtype])  # exact but for 2^129
+    assert torch.equal(torch.isnan(got.cpu()), torch.isnan(want))
+    assert torch.equal(torch.nan_to_num(got.cpu()), torch.nan_to_num(want))
+
+
+def test_dequantize_strided_and_empty():
+    g = rng(4)
+    codes, scales = mx_ref.random_operand(g, 2 * 19, 96)
+    w = nv.mx_groups_to_device(codes.reshape(2, 19, 48), scales.reshape(2, 19, 3))
+    out = torch.full((2, 19, 104), 7.0, device=DEV)
+    nv.mx_dequantize(w, out=out[:, :, :96])
+    want = mx_ref.values(codes, scales).reshape(2, 19, 96)
+    assert np.array_equal(host(out[:, :, :96]), want.astype(np.float32))
+    assert (out[:, :, 96:] == 7).all()
+    q = nv.mx_quantize(torch.zeros(0, 64, device=DEV))
+    assert q.rows == 0 and nv.mx_dequantize(q).shape == (0, 64)
+
+
+# ---- product -----------------------------------------------------------------
+
+SHAPES = [(1, 1, 32), (1, 768, 6144), (2, 17, 128), (16, 256, 6144), (17, 33, 544), (40, 100, 2080),
+          (64, 64, 512), (65, 64, 128), (100, 130, 6112), (130, 200, 640), (257, 260, 1024),
+          (300, 1000, 384), (512, 768, 512)]
+
+
+def operands(seed, M, N, K):
+    g = rng(seed, M, N, K)
+    a, b = mx_ref.random_operand(g, M, K), mx_ref.random_operand(g, N, K)
+    return a, b, mx_ref.values(*a), mx_ref.values(*b)
+
+
+def check(got, va, vb, alpha):
+    want = alpha * (va @ vb.T)
+    off = np.abs(host(got).astype(np.float64) - want)
+    bound = mx_ref.gemm_bound(va, vb, alpha, EPS[got.dtype])
+    worst = float((off / bound).max())
+    say(f"worst error / bound {worst:.3f}")
+    assert worst <= 1.0
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_gemm(M, N, K, dtype):
+    say(f"gemm {M}x{N}x{K} {dtype}")
+    a, b, va, vb = operands(1, M, N, K)
+    out = torch.full((M * N + 64,), 3.0, dtype=DT[dtype], device=DEV)
+    c = out[:M * N].view(M, N)
+    nv.mx_gemm(nv.mx_to_device(*a), nv.mx_to_device(*b), -0.75, out=c)
+    check(c, va, vb, -0.75)
+    assert (out[M * N:] == 3).all()
+
+
+def test_gemm_nan_blocks_and_extreme_scales():
+    """A NaN block reaches its own row (or column) and nothing else; products
+    of the largest and smallest scales stay within fp32's rules."""
+    for M, N in ((5, 40), (70, 130), (300, 300)):
+        a, b, _, _ = operands(2, M, N, 640)
+        a[1][3, 7] = 255
+        b[1][N - 1, 2] = 255
+        c = host(nv.mx_gemm(nv.mx_to_device(*a), nv.mx_to_device(*b)))
+        nan = np.zeros((M, N), bool)
+        nan[3], nan[:, N - 1] = True, True
+        assert np.array_equal(np.isnan(c), nan)
+    codes = np.full((16, 64), 0x77, np.uint8)             # 6.0 everywhere
+    low, high = np.zeros((16, 4), np.uint8), np.full((16, 4), 254, np.uint8)
+    A, B = nv.mx_to_device(codes, low), nv.mx_to_device(codes, high)
+    assert (nv.mx_gemm(A, B, dtype=torch.float32) == 128 * 36).all()   # 2^-127 * 2^127
+    assert torch.isinf(nv.mx_gemm(B, B)).all()
+    assert (nv.mx_gemm(A, A) == 0).all()
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("M,N,K", [(1, 768, 6144), (3, 50, 160), (16, 256, 2080), (17, 64, 32), (33, 40, 6112),
+                                   (64, 128, 1056)])
+def test_gemm_quantized_is_the_two_calls(M, N, K, dtype):
+    say(f"gemm_quantized {M}x{N}x{K} {dtype}")
+    g = rng(5, M, N, K)
+    wide = np.full((M, K + 8), np.nan, np.float32)
+    wide[:, :K] = g.standard_normal((M, K)) * np.exp(2 * g.standard_normal((M, 1)))
+    x = torch.from_numpy(wide).to(DT[dtype]).to(DEV)[:, :K]
+    b = mx_ref.random_operand(g, N, K)
+    B = nv.mx_to_device(*b)
+    for out_type in DT.values():
+        two = nv.mx_gemm(nv.mx_quantize(x), B, 0.5, dtype=out_type)
+        assert torch.equal(nv.mx_gemm_quantized(x, B, 0.5, dtype=out_type), two)
+        assert torch.equal(nv.mx_linear(x, B, 0.5, dtype=out_type), two)
+    va = mx_ref.values(*mx_ref.quantize(host(x)))
+    check(two, va, mx_ref.values(*b), 0.5)
+
+
+def test_linear_many_rows_and_none():
+    g = rng(6)
+    x = torch.from_numpy(g.standard_normal((150, 416)).astype(np.float32)).to(DEV)
+    b = mx_ref.random_operand(g, 72, 416)
+    B = nv.mx_to_device(*b)
+    check(nv.mx_linear(x, B), mx_ref.values(*mx_ref.quantize(host(x))), mx_ref.values(*b), 1.0)
+    assert nv.mx_linear(x[:0], B).shape == (0, 72)
+    assert nv.mx_gemm(nv.mx_quantize(x[:0]), B).shape == (0, 72)
+    with pytest.raises(nv.Nvfp4Error) as e:
+        nv.mx_gemm_quantized(x, B)
+    assert e.value.status == nv.ERR_UNSUPPORTED
+
+
+def test_nan_row_of_activations():
+    x = torch.ones(20, 256, device=DEV)
+    x[7, 100] = float("nan")
+    x[9, 3] = float("inf")
+    B = nv.mx_quantize(torch.ones(48, 256, device=DEV))
+    for c in (nv.mx_linear(x, B), nv.mx_gemm_quantized(x, B), nv.mx_gemm(nv.mx_quantize(x), B)):
+        nan = torch.isnan(c).all(dim=1).cpu()
+        assert nan.nonzero().flatten().tolist() == [7, 9]
+        assert (c[~nan.to(DEV)] == 256).all()
+
+
+# ---- grouped product ---------------------------------------------------------
+
+
+def grouped_reference(va, vb, offsets, rows, alpha, out_eps):
+    M, N = len(rows), vb.shape[1]
+    want, bound = np.zeros((M, N)), np.zeros((M, N))
+    for g in range(vb.shape[0]):
+        r = slice(offsets[g], offsets[g + 1])
+        if r.stop > r.start:
+            want[r] = alpha * (va[rows[r]] @ vb[g].T)
+            bound[r] = mx_ref.gemm_bound(va[rows[r]], vb[g], alpha, out_eps)
+    return want, bound
+
+
+@pytest.mark.parametrize("sizes,N,K,tail", [
+    ([0, 1, 16, 17, 40], 40, 640, 0),          # empty, one row, whole and broken row blocks
+    ([3, 0, 0, 33], 16, 128, 5),                # rows behind the last group
+    ([16] * 9, 256, 2080, 0),
+    ([5, 27, 2], 73, 4128, 3),                  # odd columns
+    ([130, 64, 1, 200], 130, 544, 7),           # dozens of rows each
+    ([700, 0, 300], 264, 1152, 2),              # hundreds of rows each
+    ([0, 0, 0], 32, 64, 4),                     # nothing but a tail
+])
+@pytest.mark.parametrize("indirect", [False, True])
+def test_grouped(sizes, N, K, tail, indirect):
+    say(f"grouped {sizes} N={N} K={K} tail={tail} indirect={indirect}")
+    g = rng(sum(sizes), N, K)
+    off = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    M = int(off[-1]) + tail
+    n = 23 if indirect else M
+    a = mx_ref.random_operand(g, n, K)
+    b = mx_ref.random_operand(g, len(sizes) * N, K)
+    b = b[0].reshape(len(sizes), N, -1), b[1].reshape(len(sizes), N, -1)
+    rows = g.integers(0, n, M).astype(np.int32) if indirect else np.arange(M)
+    if indirect and tail:
+        rows[-tail:] = -1
+    A, B = nv.mx_to_device(*a), nv.mx_groups_to_device(*b)
+    r = torch.from_numpy(rows.astype(np.int32)).to(DEV) if indirect else None
+    for dtype in DT.values():
+        out = torch.full((M, N), 5.0, dtype=dtype, device=DEV)
+        nv.mx_grouped_gemm(A, B, torch.from_numpy(off).to(DEV), 0.5, rows=r, out=out)
+        want, bound = grouped_reference(mx_ref.values(*a), mx_ref.values(*b), off, rows, 0.5, EPS[dtype])
+        kept = int(off[-1])
+        assert (np.abs(host(out)[:kept] - want[:kept]) <= bound[:kept]).all()
+        assert (out[kept:] == 5).all()
+
+
+def test_grouped_malformed_tables_stay_inside():
+    """Offsets and row numbers out of range are clamped: rows may be wrong,
+    the memory behind the output is untouched."""
+    g = rng(8)
+    A, B = nv.mx_to_device(*mx_ref.random_operand(g, 40, 256)), \
+        nv.mx_groups_to_device(*(t.reshape(3, 32, -1) for t in mx_ref.random_operand(g, 96, 256)))
+    for off in ([0, 10, 5, 60], [-7, 20, 40, 1000], [50, 60, 70, 80]):
+        out = torch.full((40 * 32 + 512,), 9.0, device=DEV)
+        rows = torch.arange(-20, 60, 2, dtype=torch.int32, device=DEV)
+        nv.mx_grouped_gemm(A, B, torch.tensor(off, dtype=torch.int32, device=DEV), rows=rows,
+                           out=out[:40 * 32].view(40, 32))
+        torch.cuda.synchronize()
+        assert (out[40 * 32:] == 9).all()
+
+
+def test_grouped_without_rows():
+    B = nv.mx_quantize(torch.ones(2, 16, 64, device=DEV))
+    off = torch.zeros(3, dtype=torch.int32, device=DEV)
+    assert nv.mx_grouped_gemm(nv.mx_quantize(torch.zeros(0, 64, device=DEV)), B, off).shape == (0, 16)
+
+
+# ---- streams, graphs, sequences ------------------------------------------------
+
+
+def test_streams_and_graph_replays():
+    g = rng(9)
+    x = torch.from_numpy(g.standard_normal((48, 1056)).astype(np.float32)).to(DEV)
+    B = nv.mx_to_device(*mx_ref.random_operand(g, 96, 1056))
+    want = nv.mx_gemm(nv.mx_quantize(x), B)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    other = nv.mx_gemm(nv.mx_quantize(x, stream=s), B, stream=s)
+    s.synchronize()
+    assert torch.equal(other, want)
+    q, out = nv.mx_quantize(x), torch.empty_like(want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        nv.mx_quantize(x, out=q)
+        nv.mx_gemm(q, B, out=out)
+    for i in range(3):
+        x.copy_(torch.randn_like(x) * (i + 1))
+        want = nv.mx_gemm(nv.mx_quantize(x), B)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
+def test_sequence():
+    g = rng(10)
+    x = torch.from_numpy(g.standard_normal((24, 544)).astype(np.float32)).to(DEV).to(torch.bfloat16)
+    B = nv.mx_to_device(*mx_ref.random_operand(g, 64, 544))
+    W = nv.mx_groups_to_device(*(t.reshape(2, 32, -1) for t in mx_ref.random_operand(g, 64, 544)))
+    off = torch.tensor([0, 9, 24], dtype=torch.int32, device=DEV)
+    q = nv.mx_quantize(x)
+    c1, c2 = (torch.empty(24, 64, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    c3 = torch.empty(24, 32, device=DEV)
+    seq = nv.Sequence()
+    seq.add_mx_quantize(x, q)
+    seq.add_mx_gemm(q, B, c1, 0.5)
+    seq.add_mx_gemm_quantized(x, B, c2, 0.5)
+    seq.add_mx_grouped_gemm(q, W, off, c3)
+    seq.finalize()
+    for _ in range(3):
+        x.copy_(torch.randn_like(x))
+        want = nv.mx_gemm(nv.mx_quantize(x), B, 0.5)
+        want3 = nv.mx_grouped_gemm(nv.mx_quantize(x), W, off, dtype=torch.float32)
+        seq.launch()
+        torch.cuda.synchronize()
+        assert torch.equal(c1, want) and torch.equal(c2, want) and torch.equal(c3, want3)
+    seq.close()
