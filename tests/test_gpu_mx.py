@@ -133,7 +133,8 @@ def test_dequantize_strided_and_empty():
 
 SHAPES = [(1, 1, 32), (1, 768, 6144), (2, 17, 128), (16, 256, 6144), (17, 33, 544), (40, 100, 2080),
           (64, 64, 512), (65, 64, 128), (100, 130, 6112), (130, 200, 640), (257, 260, 1024),
-          (300, 1000, 384), (512, 768, 512)]
+          (300, 1000, 384), (512, 768, 512),
+          (1300, 1290, 672), (1285, 1283, 2080), (4010, 3304, 544), (3900, 3301, 128)]
 
 
 def operands(seed, M, N, K):
