@@ -11,9 +11,34 @@
 #include "nvfp4_mx_device.h"
 
 #include <type_traits>
+#include <utility>
 
 namespace nvfp4 {
 namespace {
+
+// dma16 / dma4 (nvfp4_device.h) with the LDS address as a uniform base plus a
+// constant: one scalar instruction a load.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+template <int BYTES, int AT>
+__device__ __forceinline__ void mx_dma(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff,
+                                       uint32_t lds) {
+    if constexpr (BYTES == 16)
+        asm volatile("s_add_u32 m0, %3, %4\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+                     :: "v"(voff), "s"(r), "s"(soff), "s"(lds), "n"(AT) : "memory", "m0", "scc");
+    else
+        asm volatile("s_add_u32 m0, %3, %4\n\tbuffer_load_dword %0, %1, %2 offen lds"
+                     :: "v"(voff), "s"(r), "s"(soff), "s"(lds), "n"(AT) : "memory", "m0", "scc");
+}
+#pragma clang diagnostic pop
+
+// f(integral_constant<int, 0>) ... f(integral_constant<int, N - 1>)
+template <typename F, int... I>
+__device__ __forceinline__ void mx_each(F&& f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void mx_each(F&& f) { mx_each(f, std::make_integer_sequence<int, N>{}); }
 
 // Four consecutive columns of C, scaled and rounded; N need not be a multiple
 // of anything.
@@ -234,27 +259,41 @@ __global__ void __launch_bounds__(256, 1) mx_tile_kernel(MxGemmArgs a, int tiles
     const __amdgpu_buffer_rsrc_t ras = make_rsrc(a.a_scales + (int64_t)tm * AF * Q * kMxScaleFrag, (uint32_t)rba * Q * kMxScaleFrag);
     const __amdgpu_buffer_rsrc_t rbs = make_rsrc(a.b_scales + (int64_t)tn * BF * Q * kMxScaleFrag, (uint32_t)rbb * Q * kMxScaleFrag);
     const uint32_t lds0 = lds_addr(lds);
-    const uint32_t v16 = lane * 16, v4 = lane * 4;
 
-    auto load_codes = [&](int c, int stage) {
-        const uint32_t cc = (uint32_t)min(c, C - 1);
+    // A wave's loads: CPW code fragments of a step (number i is fragment wave *
+    // CPW + i) and SPW of the SPS scale fragments that travel with the step (a
+    // quarter of a scale word; with fewer than four a wave repeats one).
+    // Where they come from in the operands' memory, per lane:
+    uint32_t code_at[CPW], scale_at[4][SPW];
+    bool scale_a[4][SPW];
+    int scale_f[4][SPW];
 #pragma unroll
-        for (int i = 0; i < CPW; ++i) {
-            const int f = wave * CPW + i;
-            const bool isA = f < AF;
-            dma16(isA ? rac : rbc, v16, ((uint32_t)(isA ? f : f - AF) * (uint32_t)C + cc) * kMxFrag,
-                     lds0 + (uint32_t)(stage * STAGE + f * kMxFrag));
-        }
-    };
-    // quarter s of the scale fragments of word q
-    auto load_scales = [&](int q, int s) {
-        const uint32_t qq = (uint32_t)min(q, Q - 1);
+    for (int i = 0; i < CPW; ++i) {
+        const int f = wave * CPW + i;
+        code_at[i] = (uint32_t)(f < AF ? f : f - AF) * (uint32_t)C * kMxFrag + lane * 16;
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
 #pragma unroll
         for (int i = 0; i < SPW; ++i) {
             const int f = s * SPS + (wave * SPW + i) % SPS;
-            const bool isA = f < AF;
-            dma4(isA ? ras : rbs, v4, ((uint32_t)(isA ? f : f - AF) * (uint32_t)Q + qq) * kMxScaleFrag,
-                    lds0 + (uint32_t)(NS * STAGE + (q & 1) * SCALES + f * kMxScaleFrag));
+            scale_f[s][i] = f;
+            scale_a[s][i] = f < AF;
+            scale_at[s][i] = (uint32_t)(f < AF ? f : f - AF) * (uint32_t)Q * kMxScaleFrag + lane * 4;
+        }
+    // Load number I of the step c, whose buffer is `stage`; the scales are
+    // quarter S of word q.
+    auto load = [&](auto I, auto S, int c, int stage, int q) {
+        constexpr int i = I.value;
+        if constexpr (i < CPW) {
+            const bool isA = wave * CPW + i < AF;
+            mx_dma<16, i * kMxFrag>(isA ? rac : rbc, code_at[i], (uint32_t)min(c, C - 1) * kMxFrag,
+                                    lds0 + (uint32_t)(stage * STAGE + wave * CPW * kMxFrag));
+        } else {
+            constexpr int k = i - CPW;
+            mx_dma<4, NS * STAGE>(scale_a[S.value][k] ? ras : rbs, scale_at[S.value][k],
+                                  (uint32_t)min(q, Q - 1) * kMxScaleFrag,
+                                  lds0 + (uint32_t)((q & 1) * SCALES + scale_f[S.value][k] * kMxScaleFrag));
         }
     };
 
@@ -269,78 +308,95 @@ __global__ void __launch_bounds__(256, 1) mx_tile_kernel(MxGemmArgs a, int tiles
     // A lane's place in a 32-row block of a fragment pair: row l % 32, and
     // block 2 * half + l / 32 of the step.
     const int q32 = lane & 31, kgl = lane >> 5;
-    const uint8_t* lane_codes = lds + (q32 >> 4) * kMxFrag + kgl * 256 + (q32 & 15) * 16;
-    const uint8_t* lane_scales = lds + NS * STAGE + (q32 >> 4) * kMxScaleFrag + kgl * 64 + (q32 & 15) * 4;
     const int fa = wm * (AF / 2), fb = AF + wn * (BF / 2);  // the wave's first fragments
+    const uint8_t* lane_a = lds + (q32 >> 4) * kMxFrag + kgl * 256 + (q32 & 15) * 16 + fa * kMxFrag;
+    const uint8_t* lane_b = lane_a + (fb - fa) * kMxFrag;
+    const uint8_t* lane_sa = lds + NS * STAGE + (q32 >> 4) * kMxScaleFrag + kgl * 64 + (q32 & 15) * 4 + fa * kMxScaleFrag;
+    const uint8_t* lane_sb = lane_sa + (fb - fa) * kMxScaleFrag;
 
     struct Half { mx_u4 a[MI], b[NI]; };
-    auto read_half = [&](Half& h, int stage, int half) {
-        const uint8_t* p = lane_codes + stage * STAGE + half * 512;
-#pragma unroll
-        for (int i = 0; i < MI; ++i) h.a[i] = *reinterpret_cast<const mx_u4*>(p + (fa + 2 * i) * kMxFrag);
-#pragma unroll
-        for (int j = 0; j < NI; ++j) h.b[j] = *reinterpret_cast<const mx_u4*>(p + (fb + 2 * j) * kMxFrag);
+    struct Scales { uint32_t a[MI][2], b[NI][2]; };
+    constexpr int P = MI + NI;   // 32-row blocks of a wave: LDS reads of a half
+    constexpr int MM = MI * NI;  // MFMAs of a half
+    static_assert(P <= MM, "a read behind each MFMA");
+    // LDS read number I of a half
+    auto read = [&](auto I, Half& h, int stage, int half) {
+        constexpr int i = I.value;
+        const int at = stage * STAGE + half * 512;
+        if constexpr (i < MI)
+            h.a[i] = *reinterpret_cast<const mx_u4*>(lane_a + at + 2 * i * kMxFrag);
+        else
+            h.b[i - MI] = *reinterpret_cast<const mx_u4*>(lane_b + at + 2 * (i - MI) * kMxFrag);
     };
-    struct Scales { uint32_t a[2][MI], b[2][NI]; };
-    auto read_scales = [&](Scales& s, int q) {
-        const uint8_t* p = lane_scales + (q & 1) * SCALES;
+    // the two scale words of 32-row block I
+    auto read_scale = [&](auto I, Scales& s, int q) {
+        constexpr int i = I.value;
+        const int at = (q & 1) * SCALES;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int i = 0; i < MI; ++i) s.a[h][i] = *reinterpret_cast<const uint32_t*>(p + (fa + 2 * i) * kMxScaleFrag + h * 128);
-#pragma unroll
-            for (int j = 0; j < NI; ++j) s.b[h][j] = *reinterpret_cast<const uint32_t*>(p + (fb + 2 * j) * kMxScaleFrag + h * 128);
-        }
+        for (int h = 0; h < 2; ++h)
+            if constexpr (i < MI)
+                s.a[i][h] = *reinterpret_cast<const uint32_t*>(lane_sa + at + 2 * i * kMxScaleFrag + h * 128);
+            else
+                s.b[i - MI][h] = *reinterpret_cast<const uint32_t*>(lane_sb + at + 2 * (i - MI) * kMxScaleFrag + h * 128);
+    };
+    Scales sc, sn;
+    auto mfma = [&](auto N, auto S, const Half& h, int half) {
+        constexpr int i = N.value / NI, j = N.value % NI;
+        acc[i][j] = mx_mfma32<S.value>(h.b[j], sc.b[j][half], h.a[i], sc.a[i][half], acc[i][j]);
     };
 
     // fill the ring
-#pragma unroll
-    for (int s = 0; s < 4; ++s) load_scales(0, s);
-#pragma unroll
-    for (int c = 0; c < NS; ++c) {
-        load_codes(c, c);
-        load_scales(c / 4 + 1, c & 3);
-    }
+    mx_each<4>([&](auto S) {
+        mx_each<SPW>([&](auto I) { load(std::integral_constant<int, CPW + I.value>{}, S, 0, 0, 0); });
+    });
+    mx_each<NS>([&](auto c) {
+        mx_each<L>([&](auto I) { load(I, std::integral_constant<int, c.value & 3>{}, c.value, c.value, c.value / 4 + 1); });
+    });
     wait_vmcnt<(NS - 1) * L>();  // step 0 and the first scale word
     wg_barrier();
-    Scales sc;
-    read_scales(sc, 0);
     Half h0, h1;
-    read_half(h0, 0, 0);
+    mx_each<P>([&](auto I) { read_scale(I, sc, 0); });
+    mx_each<P>([&](auto I) { read(I, h0, 0, 0); });
 
-    auto mfmas = [&](const Half& h, int half, auto S) {
-#pragma unroll
-        for (int i = 0; i < MI; ++i)
-#pragma unroll
-            for (int j = 0; j < NI; ++j)
-                acc[i][j] = mx_mfma32<S.value>(h.b[j], sc.b[half][j], h.a[i], sc.a[half][i], acc[i][j]);
-    };
+    // One step.  The order is fixed (the scheduling barriers): behind each
+    // MFMA one LDS read and its share of the loads, which issue while the
+    // MFMA runs; left to itself the compiler moves the reads to their uses
+    // and the MFMAs wait for each.
     int c = 0, stage = 0;
-    Scales sn;
     auto step = [&](auto S) {
-        read_half(h1, stage, 1);
-        mfmas(h0, 0, S);
+        constexpr int s = S.value, s_load = (s + NS) & 3;  // of the step being loaded
+        mx_each<MM>([&](auto N) {
+            mfma(N, S, h0, 0);
+            if constexpr (N.value < P) read(N, h1, stage, 1);
+            __builtin_amdgcn_sched_barrier(0);
+        });
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         wait_vmcnt<(NS - 2) * L>();
         wg_barrier();
-        load_codes(c + NS, stage);
-        load_scales((c + NS) / 4 + 1, (c + NS) & 3);
+        __builtin_amdgcn_sched_barrier(0);
+        const int freed = stage;
         stage = stage + 1 == NS ? 0 : stage + 1;
-        read_half(h0, stage, 0);
-        if (S.value == 3) read_scales(sn, c / 4 + 1);
-        mfmas(h1, 1, S);
-        if (S.value == 3) sc = sn;
+        mx_each<MM>([&](auto N) {
+            constexpr int n = N.value;
+            mfma(N, S, h1, 1);
+            if constexpr (n < P) read(N, h0, stage, 0);
+            if constexpr (s == 3 && n >= MM - P) read_scale(std::integral_constant<int, n - (MM - P)>{}, sn, c / 4 + 1);
+            mx_each<(n + 1) * L / MM - n * L / MM>([&](auto I) {
+                load(std::integral_constant<int, n * L / MM + I.value>{}, std::integral_constant<int, s_load>{},
+                     c + NS, freed, (c + NS) / 4 + 1);
+            });
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        if constexpr (s == 3) sc = sn;
         ++c;
     };
-    for (;;) {
+    // whole scale words, then the steps that are left (one loop exit: the
+    // accumulators stay where they are)
+    for (int q = C / 4; q > 0; --q) mx_each<4>(step);
+    if (C & 3) {
         step(std::integral_constant<int, 0>{});
-        if (c >= C) break;
-        step(std::integral_constant<int, 1>{});
-        if (c >= C) break;
-        step(std::integral_constant<int, 2>{});
-        if (c >= C) break;
-        step(std::integral_constant<int, 3>{});
-        if (c >= C) break;
+        if ((C & 3) > 1) step(std::integral_constant<int, 1>{});
+        if ((C & 3) > 2) step(std::integral_constant<int, 2>{});
     }
     wait_vmcnt<0>();  // the ring's last loads, before its memory is used again
     __syncthreads();
