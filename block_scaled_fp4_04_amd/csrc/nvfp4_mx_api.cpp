@@ -218,13 +218,13 @@ int nvfp4_mx_pack(const uint8_t* codes, const uint8_t* scales, int64_t rows, int
                 const int64_t row = rb * kMxRows + r;
                 const bool live = row < rows && b < blocks;
                 if (c < C) {
-                    uint8_t* d = packed_codes + (rb * C + c) * kMxFrag + kg * 256 + r * 16;
+                    uint8_t* d = packed_codes + (rb * C + c) * kMxFrag + mx_code_at((int)r, (int)kg);
                     if (live)
                         std::memcpy(d, codes + row * (K / 2) + b * 16, 16);
                     else
                         std::memset(d, 0, 16);
                 }
-                packed_scales[(rb * Q + c / 4) * kMxScaleFrag + kg * 64 + r * 4 + c % 4] =
+                packed_scales[(rb * Q + c / 4) * kMxScaleFrag + mx_scale_at((int)r, (int)kg) + c % 4] =
                     live ? scales[row * blocks + b] : 0;
             }
         }
@@ -241,9 +241,9 @@ int nvfp4_mx_unpack(const uint8_t* packed_codes, const uint8_t* packed_scales, i
         for (int64_t b = 0; b < blocks; ++b) {
             const int64_t c = b / 4, kg = b % 4;
             std::memcpy(codes + row * (K / 2) + b * 16,
-                        packed_codes + (rb * C + c) * kMxFrag + kg * 256 + r * 16, 16);
+                        packed_codes + (rb * C + c) * kMxFrag + mx_code_at((int)r, (int)kg), 16);
             scales[row * blocks + b] =
-                packed_scales[(rb * Q + c / 4) * kMxScaleFrag + kg * 64 + r * 4 + c % 4];
+                packed_scales[(rb * Q + c / 4) * kMxScaleFrag + mx_scale_at((int)r, (int)kg) + c % 4];
         }
     }
     return NVFP4_OK;

@@ -108,8 +108,8 @@ __global__ void __launch_bounds__(W * 64) mx_split_kernel(MxGemmArgs a) {
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
         const int64_t rb = min(cb0 + j, a.RBb - 1);
-        bcp[j] = bc + rb * C * kMxFrag + lane * 16;
-        bsp[j] = bs + rb * Q * kMxScaleFrag + lane * 4;
+        bcp[j] = bc + rb * C * kMxFrag + mx_code_at(r16, kg);
+        bsp[j] = bs + rb * Q * kMxScaleFrag + mx_scale_at(r16, kg);
     }
 
     for (int m0 = r0; m0 < r1; m0 += 16 * MI) {
@@ -142,11 +142,11 @@ __global__ void __launch_bounds__(W * 64) mx_split_kernel(MxGemmArgs a) {
                 if constexpr (AT == A_PACKED) {
                     const int64_t rb = arow[i] >> 4;
                     const int rr = (int)(arow[i] & 15);
-                    sa[i] = *reinterpret_cast<const uint32_t*>(a.a_scales + (rb * Q + q) * kMxScaleFrag + kg * 64 + rr * 4);
+                    sa[i] = *reinterpret_cast<const uint32_t*>(a.a_scales + (rb * Q + q) * kMxScaleFrag + mx_scale_at(rr, kg));
 #pragma unroll
                     for (int s = 0; s < 4; ++s) {
                         const int64_t c = min(4 * q + s, C - 1);
-                        wa[s][i] = *reinterpret_cast<const mx_u4*>(a.a_codes + (rb * C + c) * kMxFrag + kg * 256 + rr * 16);
+                        wa[s][i] = *reinterpret_cast<const mx_u4*>(a.a_codes + (rb * C + c) * kMxFrag + mx_code_at(rr, kg));
                     }
                 } else {
                     sa[i] = 0;
@@ -216,11 +216,12 @@ __global__ void __launch_bounds__(W * 64) mx_split_kernel(MxGemmArgs a) {
 // Rows past the operands' ends read as zeros (the buffers' range check) and
 // are not stored.  Steps past the last one load it again, unused.
 // ---------------------------------------------------------------------------
-template <int BM, int BN, int NS>
+template <int BM, int BN, int NS, int WM, bool GROUPED>
 __global__ void __launch_bounds__(256, 1) mx_tile_kernel(MxGemmArgs a, int tiles_m, int tiles_n) {
-    constexpr int MI = BM / 64, NI = BN / 64;    // 32 x 32 blocks of a wave
-    constexpr int AF = BM / 16, BF = BN / 16;    // fragments of a step
-    constexpr int CPW = (AF + BF) / 4;           // of them, a wave's loads
+    constexpr int WN = 4 / WM;                            // waves along M and N
+    constexpr int MI = BM / 32 / WM, NI = BN / 32 / WN;   // 32 x 32 blocks of a wave
+    constexpr int AF = BM / 16, BF = BN / 16;             // fragments of a step
+    constexpr int CPW = (AF + BF) / 4;                    // of them, a wave's loads
     constexpr int SPS = (AF + BF) / 4;           // scale fragments that travel with a step
     constexpr int SPW = (SPS + 3) / 4;           // of them, a wave's loads
     constexpr int L = CPW + SPW;
@@ -228,37 +229,103 @@ __global__ void __launch_bounds__(256, 1) mx_tile_kernel(MxGemmArgs a, int tiles
     constexpr int SCALES = (AF + BF) * kMxScaleFrag;  // of four steps
     // (NS <= 4: the loads of a scale word start once the word two before is read)
     static_assert((AF + BF) % 4 == 0 && NS >= 2 && NS <= 4 && (NS - 1) * L < 64, "ring");
-    static_assert(2 * (BM * (BN + 16)) <= NS * STAGE + 2 * SCALES, "the output is staged in the ring");
+    static_assert(BM * WN * (BN / WN * 2 + 16) <= NS * STAGE + 2 * SCALES, "the output is staged in the ring");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * STAGE + 2 * SCALES];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 3;
-    const int wm = wave >> 1, wn = wave & 1;
+    const int wm = wave / WN, wn = wave % WN;
     const int C = a.C, Q = (C + 3) / 4;
 
     // Consecutive workgroups go to the eight XCDs in turn: each XCD gets a
-    // contiguous range of tiles, walked in groups of 8 along M, so that the
-    // tiles that run together share their operands in its L2.
+    // contiguous range of tiles, so that the tiles that run together share
+    // their operands in its L2: walked in groups of 8 along M, or, grouped,
+    // row block by row block in the groups' order.
     int t = blockIdx.x;
     {
         const int total = tiles_m * tiles_n;
         if ((total & 7) == 0) t = (t & 7) * (total >> 3) + (t >> 3);
     }
-    constexpr int GROUP_M = 8;
-    const int in_group = GROUP_M * tiles_n;
-    const int first_m = (t / in_group) * GROUP_M;
-    const int gsize = min(tiles_m - first_m, GROUP_M);
-    const int tm = first_m + (t % in_group) % gsize, tn = (t % in_group) / gsize;
-    const int m0 = tm * BM, n0 = tn * BN;
+    int tn, m0, row_end = a.M;
+    int64_t b_first;  // first row block of this tile's B
+    if constexpr (GROUPED) {
+        // Row blocks are numbered in group order, ceil(rows / BM) to a group;
+        // the grid is an upper bound.  Each thread counts those of a run of
+        // groups, and the one whose run holds this tile's publishes it.
+        int* sch = reinterpret_cast<int*>(lds);
+        const int tid = threadIdx.x, vm = t / tiles_n;
+        tn = t % tiles_n;
+        const int per = (a.groups + 255) / 256;
+        const int g_lo = min(tid * per, a.groups), g_hi = min(g_lo + per, a.groups);
+        auto rows_of = [&](int g, int& r0, int& r1) {
+            r0 = min(max(a.offsets[g], 0), a.M);
+            r1 = min(max(a.offsets[g + 1], r0), a.M);
+        };
+        int64_t cnt = 0;  // (a malformed table may count up to groups * M rows)
+        for (int g = g_lo; g < g_hi; ++g) {
+            int r0, r1;
+            rows_of(g, r0, r1);
+            cnt += (r1 - r0 + BM - 1) / BM;
+        }
+        const int mine = (int)min(cnt, (int64_t)1 << 22);
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int y = __shfl_up(incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 63) sch[wave] = incl;
+        if (tid == 0) sch[4] = -1;
+        __syncthreads();
+        int at = vm - (incl - mine);
+        for (int w = 0; w < wave; ++w) at -= sch[w];
+        if (at >= 0 && at < mine)
+            for (int g = g_lo; g < g_hi; ++g) {
+                int r0, r1;
+                rows_of(g, r0, r1);
+                const int n = (r1 - r0 + BM - 1) / BM;
+                if (at < n) {
+                    sch[4] = g;
+                    sch[5] = r0 + at * BM;
+                    sch[6] = r1;
+                    break;
+                }
+                at -= n;
+            }
+        __syncthreads();
+        const int g = __builtin_amdgcn_readfirstlane(sch[4]);
+        if (g < 0) return;  // past the last row block: the whole workgroup leaves
+        m0 = __builtin_amdgcn_readfirstlane(sch[5]);
+        row_end = __builtin_amdgcn_readfirstlane(sch[6]);
+        b_first = (int64_t)g * a.RBb + (int64_t)tn * BF;
+        __syncthreads();  // everyone has read before the ring fills
+    } else {
+        constexpr int GROUP_M = 8;
+        const int in_group = GROUP_M * tiles_n;
+        const int first_m = (t / in_group) * GROUP_M;
+        const int gsize = min(tiles_m - first_m, GROUP_M);
+        tn = (t % in_group) / gsize;
+        m0 = (first_m + (t % in_group) % gsize) * BM;
+        b_first = (int64_t)tn * BF;
+    }
+    const int n0 = tn * BN;
 
     // The tile's part of each operand: row blocks from its first one to the
-    // operand's end or the tile's.
-    const int rba = min(AF, a.RBa - tm * AF), rbb = min(BF, a.RBb - tn * BF);
-    const __amdgpu_buffer_rsrc_t rac = make_rsrc(a.a_codes + (int64_t)tm * AF * C * kMxFrag, (uint32_t)rba * C * kMxFrag);
-    const __amdgpu_buffer_rsrc_t rbc = make_rsrc(a.b_codes + (int64_t)tn * BF * C * kMxFrag, (uint32_t)rbb * C * kMxFrag);
-    const __amdgpu_buffer_rsrc_t ras = make_rsrc(a.a_scales + (int64_t)tm * AF * Q * kMxScaleFrag, (uint32_t)rba * Q * kMxScaleFrag);
-    const __amdgpu_buffer_rsrc_t rbs = make_rsrc(a.b_scales + (int64_t)tn * BF * Q * kMxScaleFrag, (uint32_t)rbb * Q * kMxScaleFrag);
+    // operand's end or the tile's; A of a grouped product is addressed whole,
+    // row by row.
+    const int rba = GROUPED ? a.RBa : min(AF, a.RBa - m0 / 16), rbb = min(BF, a.RBb - tn * BF);
+    const int64_t a_first = GROUPED ? 0 : m0 / 16;
+    const __amdgpu_buffer_rsrc_t rac = make_rsrc(a.a_codes + a_first * C * kMxFrag, (uint32_t)rba * C * kMxFrag);
+    const __amdgpu_buffer_rsrc_t rbc = make_rsrc(a.b_codes + b_first * C * kMxFrag, (uint32_t)rbb * C * kMxFrag);
+    const __amdgpu_buffer_rsrc_t ras = make_rsrc(a.a_scales + a_first * Q * kMxScaleFrag, (uint32_t)rba * Q * kMxScaleFrag);
+    const __amdgpu_buffer_rsrc_t rbs = make_rsrc(a.b_scales + b_first * Q * kMxScaleFrag, (uint32_t)rbb * Q * kMxScaleFrag);
     const uint32_t lds0 = lds_addr(lds);
+    // Row of A that a lane brings for fragment f of the tile (grouped): a
+    // fragment's lanes fill it in order, four to a row.
+    auto a_row = [&](int f) {
+        const int r = min(m0 + f * 16 + (lane >> 2), row_end - 1);
+        return (uint32_t)(a.a_rows ? min(max(a.a_rows[r], 0), a.A_rows - 1) : r);
+    };
 
     // A wave's loads: CPW code fragments of a step (number i is fragment wave *
     // CPW + i) and SPW of the SPS scale fragments that travel with the step (a
@@ -271,6 +338,10 @@ __global__ void __launch_bounds__(256, 1) mx_tile_kernel(MxGemmArgs a, int tiles
     for (int i = 0; i < CPW; ++i) {
         const int f = wave * CPW + i;
         code_at[i] = (uint32_t)(f < AF ? f : f - AF) * (uint32_t)C * kMxFrag + lane * 16;
+        if (GROUPED && f < AF) {
+            const uint32_t r = a_row(f);
+            code_at[i] = (r >> 4) * (uint32_t)C * kMxFrag + mx_code_at(r & 15, (lane & 3) ^ (lane >> 4));
+        }
     }
 #pragma unroll
     for (int s = 0; s < 4; ++s)
@@ -280,6 +351,10 @@ __global__ void __launch_bounds__(256, 1) mx_tile_kernel(MxGemmArgs a, int tiles
             scale_f[s][i] = f;
             scale_a[s][i] = f < AF;
             scale_at[s][i] = (uint32_t)(f < AF ? f : f - AF) * (uint32_t)Q * kMxScaleFrag + lane * 4;
+            if (GROUPED && f < AF) {
+                const uint32_t r = a_row(f);
+                scale_at[s][i] = (r >> 4) * (uint32_t)Q * kMxScaleFrag + mx_scale_at(r & 15, lane & 3);
+            }
         }
     // Load number I of the step c, whose buffer is `stage`; the scales are
     // quarter S of word q.
@@ -308,10 +383,11 @@ __global__ void __launch_bounds__(256, 1) mx_tile_kernel(MxGemmArgs a, int tiles
     // A lane's place in a 32-row block of a fragment pair: row l % 32, and
     // block 2 * half + l / 32 of the step.
     const int q32 = lane & 31, kgl = lane >> 5;
-    const int fa = wm * (AF / 2), fb = AF + wn * (BF / 2);  // the wave's first fragments
-    const uint8_t* lane_a = lds + (q32 >> 4) * kMxFrag + kgl * 256 + (q32 & 15) * 16 + fa * kMxFrag;
-    const uint8_t* lane_b = lane_a + (fb - fa) * kMxFrag;
-    const uint8_t* lane_sa = lds + NS * STAGE + (q32 >> 4) * kMxScaleFrag + kgl * 64 + (q32 & 15) * 4 + fa * kMxScaleFrag;
+    const int fa = wm * (AF / WM), fb = AF + wn * (BF / WN);  // the wave's first fragments
+    const uint8_t* lane_code[2];  // of each half
+#pragma unroll
+    for (int h = 0; h < 2; ++h) lane_code[h] = lds + (q32 >> 4) * kMxFrag + mx_code_at(q32 & 15, 2 * h + kgl);
+    const uint8_t* lane_sa = lds + NS * STAGE + ((q32 >> 4) + fa) * kMxScaleFrag + mx_scale_at(q32 & 15, kgl);
     const uint8_t* lane_sb = lane_sa + (fb - fa) * kMxScaleFrag;
 
     struct Half { mx_u4 a[MI], b[NI]; };
@@ -322,11 +398,11 @@ __global__ void __launch_bounds__(256, 1) mx_tile_kernel(MxGemmArgs a, int tiles
     // LDS read number I of a half
     auto read = [&](auto I, Half& h, int stage, int half) {
         constexpr int i = I.value;
-        const int at = stage * STAGE + half * 512;
+        const uint8_t* p = lane_code[half] + stage * STAGE;
         if constexpr (i < MI)
-            h.a[i] = *reinterpret_cast<const mx_u4*>(lane_a + at + 2 * i * kMxFrag);
+            h.a[i] = *reinterpret_cast<const mx_u4*>(p + (fa + 2 * i) * kMxFrag);
         else
-            h.b[i - MI] = *reinterpret_cast<const mx_u4*>(lane_b + at + 2 * (i - MI) * kMxFrag);
+            h.b[i - MI] = *reinterpret_cast<const mx_u4*>(p + (fb + 2 * (i - MI)) * kMxFrag);
     };
     // the two scale words of 32-row block I
     auto read_scale = [&](auto I, Scales& s, int q) {
@@ -335,9 +411,9 @@ __global__ void __launch_bounds__(256, 1) mx_tile_kernel(MxGemmArgs a, int tiles
 #pragma unroll
         for (int h = 0; h < 2; ++h)
             if constexpr (i < MI)
-                s.a[i][h] = *reinterpret_cast<const uint32_t*>(lane_sa + at + 2 * i * kMxScaleFrag + h * 128);
+                s.a[i][h] = *reinterpret_cast<const uint32_t*>(lane_sa + at + 2 * i * kMxScaleFrag + h * 8);
             else
-                s.b[i - MI][h] = *reinterpret_cast<const uint32_t*>(lane_sb + at + 2 * (i - MI) * kMxScaleFrag + h * 128);
+                s.b[i - MI][h] = *reinterpret_cast<const uint32_t*>(lane_sb + at + 2 * (i - MI) * kMxScaleFrag + h * 8);
     };
     Scales sc, sn;
     auto mfma = [&](auto N, auto S, const Half& h, int half) {
@@ -403,11 +479,12 @@ __global__ void __launch_bounds__(256, 1) mx_tile_kernel(MxGemmArgs a, int tiles
 
     // Epilogue.  Block (i, j) of lane l: row 32 i + l % 32, columns 32 j +
     // 8 (v / 4) + 4 (l / 32) + v % 4.
-    const int row0 = m0 + wm * (BM / 2), col0 = n0 + wn * (BN / 2);
+    constexpr int PM = BM / WM, PN = BN / WN;  // the wave's part
+    const int row0 = m0 + wm * PM, col0 = n0 + wn * PN;
     if (a.out_bf16 && (a.N & 7) == 0) {
         // through LDS, a wave's part each, so that whole lines are stored
-        constexpr int ROW = BN + 16;  // bytes (BN / 2 columns and 16 bytes of padding)
-        uint8_t* part = lds + wave * (BM / 2) * ROW;
+        constexpr int ROW = PN * 2 + 16;  // bytes, 16 of them padding
+        uint8_t* part = lds + wave * PM * ROW;
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -420,15 +497,15 @@ __global__ void __launch_bounds__(256, 1) mx_tile_kernel(MxGemmArgs a, int tiles
                     __builtin_memcpy(__builtin_assume_aligned(part + (i * 32 + q32) * ROW + (j * 32 + 2 * v + 4 * kgl) * 2, 8), o, 8);
                 }
         __syncthreads();
-        constexpr int LPR = BN / 16;       // lanes that store a row's part
+        constexpr int LPR = PN / 8;        // lanes that store a row's part
         constexpr int RPS = 64 / LPR;      // rows a store covers
         const int r = lane / LPR, col = col0 + (lane % LPR) * 8;
 #pragma unroll 4
-        for (int k = 0; k < BM / 2; k += RPS) {
+        for (int k = 0; k < PM; k += RPS) {
             const int row = row0 + k + r;
             mx_u4 o;
             __builtin_memcpy(&o, __builtin_assume_aligned(part + (k + r) * ROW + (lane % LPR) * 16, 16), 16);
-            if (row < a.M && col < a.N)
+            if (row < row_end && col < a.N)
                 *reinterpret_cast<mx_u4*>(static_cast<uint16_t*>(a.out) + (int64_t)row * a.N + col) = o;
         }
     } else {
@@ -440,7 +517,7 @@ __global__ void __launch_bounds__(256, 1) mx_tile_kernel(MxGemmArgs a, int tiles
 #pragma unroll
                 for (int v = 0; v < 16; v += 4) {
                     const mx_f4 f = {acc[i][j][v], acc[i][j][v + 1], acc[i][j][v + 2], acc[i][j][v + 3]};
-                    if (row < a.M) mx_store4(a, row, col0 + j * 32 + 2 * v + 4 * kgl, f);
+                    if (row < row_end) mx_store4(a, row, col0 + j * 32 + 2 * v + 4 * kgl, f);
                 }
         }
     }
@@ -471,13 +548,14 @@ void run_split(Launch& l) {
     l.error = hipGetLastError();
 }
 
-template <int BM, int BN, int NS>
+template <int BM, int BN, int NS, int WM, bool GROUPED>
 void run_tile(Launch& l) {
     const MxGemmArgs& a = l.a;
-    const int64_t tiles_m = ((int64_t)a.M + BM - 1) / BM, tiles_n = ((int64_t)a.N + BN - 1) / BN;
+    // (grouped: each group adds at most one broken row block)
+    const int64_t tiles_m = ((int64_t)a.M + BM - 1) / BM + (GROUPED ? a.groups : 0), tiles_n = ((int64_t)a.N + BN - 1) / BN;
     l.items = tiles_m * tiles_n * 256;
     if (l.dry) return;
-    hipLaunchKernelGGL((mx_tile_kernel<BM, BN, NS>), dim3((unsigned)(tiles_m * tiles_n)), dim3(256), 0,
+    hipLaunchKernelGGL((mx_tile_kernel<BM, BN, NS, WM, GROUPED>), dim3((unsigned)(tiles_m * tiles_n)), dim3(256), 0,
                        l.stream, a, (int)tiles_m, (int)tiles_n);
     l.error = hipGetLastError();
 }
@@ -493,15 +571,24 @@ void choose(Launch& l) {
     const MxGemmArgs& a = l.a;
     if (a.groups > 0) {
         if (a.M / a.groups <= 32) return run_split<2, 4, 4, A_PACKED, true>(l);
+        if (a.C <= kMxTileSteps && (int64_t)a.RBa * a.C * kMxFrag < ((int64_t)1 << 31)) {
+            static const int v = getenv("MXV") ? atoi(getenv("MXV")) : 0;
+            if (v == 1) return run_tile<128, 256, 3, 2, true>(l);
+            if (v == 2) return run_tile<64, 256, 3, 1, true>(l);
+            if (v == 3) return run_tile<256, 256, 4, 2, true>(l);
+            if (v == 4) return run_tile<128, 256, 4, 2, true>(l);
+            if (v == 5) return run_tile<64, 256, 4, 1, true>(l);
+            return run_tile<128, 128, 4, 2, true>(l);
+        }
         return run_split<4, 4, 8, A_PACKED, true>(l);
     }
     if (!a.a_codes) return a.x_bf16 ? run_few_rows<A_BF16>(l) : run_few_rows<A_F32>(l);
     if (a.M <= 64) return run_few_rows<A_PACKED>(l);
     if (a.C <= kMxTileSteps) {
         const int64_t t256 = ((a.M + 255) / 256) * (int64_t)((a.N + 255) / 256);
-        if (t256 >= 192) return run_tile<256, 256, 4>(l);
+        if (t256 >= 192) return run_tile<256, 256, 4, 2, false>(l);
         const int64_t t128 = ((a.M + 127) / 128) * (int64_t)((a.N + 127) / 128);
-        if (t128 >= 100) return run_tile<128, 128, 4>(l);
+        if (t128 >= 100) return run_tile<128, 128, 4, 2, false>(l);
     }
     return run_split<4, 4, 8, A_PACKED, false>(l);
 }

@@ -14,6 +14,11 @@ constexpr int kMxRows = 16;      // rows of a row block
 constexpr int kMxFrag = 1024;    // code bytes of 16 rows x one step
 constexpr int kMxScaleFrag = 256;  // scale bytes of 16 rows x four steps
 
+// Where block b (0..3) of a step of row r (0..15) starts in a fragment, and its
+// four scale bytes in a scale fragment.
+__host__ __device__ constexpr int mx_code_at(int r, int b) { return r * 64 + ((b ^ (r >> 2)) << 4); }
+__host__ __device__ constexpr int mx_scale_at(int r, int b) { return r * 16 + b * 4; }
+
 inline int64_t mx_round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 inline int64_t mx_steps(int64_t K) { return mx_round_up(K, kMxStep) / kMxStep; }
 inline int64_t mx_row_blocks(int64_t rows) { return mx_round_up(rows, kMxRows) / kMxRows; }
@@ -22,8 +27,8 @@ inline int64_t mx_row_blocks(int64_t rows) { return mx_round_up(rows, kMxRows) /
 struct MxQuantArgs {
     void* x;               // groups x rows x K values (fp32, or bfloat16 if bf16)
     bool bf16;
-    uint8_t* codes;        // groups x [RB][C][4][16][16]
-    uint8_t* scales;       // groups x [RB][Q][4][16][4]
+    uint8_t* codes;        // groups x [RB][C][16][4][16]
+    uint8_t* scales;       // groups x [RB][Q][16][4][4]
     int64_t group_stride;  // elements between groups of x
     int64_t ld;            // elements between rows of x
     int64_t groups;

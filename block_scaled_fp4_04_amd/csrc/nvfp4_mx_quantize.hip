@@ -10,7 +10,7 @@
 // A wave makes one fragment of the packed layout, 16 rows x 128 elements:
 // lane l owns the whole block of row l % 16 at elements 32 * (l / 16), so
 // the largest magnitude needs no exchange between lanes and the lanes' 16
-// code bytes are one contiguous 1 KB store.  Bound by memory.
+// code bytes fill one contiguous 1 KB.  Bound by memory.
 #include "nvfp4_mx_device.h"
 
 #include <algorithm>
@@ -39,13 +39,13 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(MxQuantArgs a) {
         const T* p = static_cast<const T*>(a.x) + g * a.group_stride + (int64_t)row * a.ld + k;
         byte = mx_quant_load(p, w);
     }
-    reinterpret_cast<mx_u4*>(a.codes + frag * kMxFrag)[lane] = w;
+    *reinterpret_cast<mx_u4*>(a.codes + frag * kMxFrag + mx_code_at(r16, kg)) = w;
     const int Q = (a.C + 3) / 4;
-    a.scales[(grb * Q + c / 4) * kMxScaleFrag + lane * 4 + (c & 3)] = (uint8_t)byte;
+    a.scales[(grb * Q + c / 4) * kMxScaleFrag + mx_scale_at(r16, kg) + (c & 3)] = (uint8_t)byte;
     // the last step also clears the scales of the steps that fill its word
     if (c == a.C - 1)
         for (int s = (c & 3) + 1; s < 4; ++s)
-            a.scales[(grb * Q + c / 4) * kMxScaleFrag + lane * 4 + s] = 0;
+            a.scales[(grb * Q + c / 4) * kMxScaleFrag + mx_scale_at(r16, kg) + s] = 0;
 }
 
 template <typename T>
@@ -61,9 +61,9 @@ __global__ void __launch_bounds__(256) mx_dequantize_kernel(MxQuantArgs a) {
     const int row = (int)(grb % a.RB) * kMxRows + r16;
     const int k = c * kMxStep + kg * kMxBlock;
     if (row >= a.rows || k >= a.K) return;
-    const mx_u4 w = reinterpret_cast<const mx_u4*>(a.codes + frag * kMxFrag)[lane];
+    const mx_u4 w = *reinterpret_cast<const mx_u4*>(a.codes + frag * kMxFrag + mx_code_at(r16, kg));
     const int Q = (a.C + 3) / 4;
-    const uint32_t byte = a.scales[(grb * Q + c / 4) * kMxScaleFrag + lane * 4 + (c & 3)];
+    const uint32_t byte = a.scales[(grb * Q + c / 4) * kMxScaleFrag + mx_scale_at(r16, kg) + (c & 3)];
     const float s = mx_scale(byte);
     T* p = static_cast<T*>(a.x) + g * a.group_stride + (int64_t)row * a.ld + k;
     // 8 codes of a word -> 8 values (a code times a power of two is exact in

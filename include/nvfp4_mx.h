@@ -18,12 +18,17 @@
  * host or nvfp4_mx_quantize on the device).  Rows are padded to whole row
  * blocks of 16 (RB of them) and K to whole steps of 128 (C of them) with zero
  * codes and zero scale bytes (exact zeros, so results are unaffected):
- *   packed codes  [RB][C][4][16][16]   (row block, step, block of the step,
- *                                       row of the row block, 16 code bytes)
- *   packed scales [RB][ceil(C/4)][4][16][4]  (row block, four steps, block of
- *                                       a step, row, the four steps' bytes)
+ *   packed codes  [RB][C][16][4][16]   (row block, step, row of the row
+ *                                       block, place in the row's 64 bytes,
+ *                                       16 code bytes): block b (0..3) of a
+ *                                       step of row r is at place b ^ (r / 4)
+ *   packed scales [RB][ceil(C/4)][16][4][4]  (row block, four steps, row,
+ *                                       block of a step, the four steps'
+ *                                       bytes)
  * The 1024 code bytes of 16 rows x 128 elements are what one wave feeds to
- * one matrix instruction.
+ * one matrix instruction; a row's 64 of them are contiguous, so that rows can
+ * be picked one by one, and the places are such that the lanes of a wave
+ * read them from LDS without bank conflicts.
  *
  * Status codes, pointers, streams and errors as in nvfp4.h: every entry point
  * returns an nvfp4_status and never aborts, throws or prints; argument errors

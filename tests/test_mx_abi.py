@@ -49,12 +49,14 @@ def test_pack_roundtrip_and_layout(rows, K):
     q = -(-c // 4)
     wide = np.zeros((rb * 16, c * 64), np.uint8)
     wide[:rows, :K // 2] = codes
-    assert np.array_equal(pc.reshape(rb, c, 4, 16, 16),
-                          wide.reshape(rb, 16, c, 4, 16).transpose(0, 2, 3, 1, 4))
+    rows_first = wide.reshape(rb, 16, c, 4, 16).transpose(0, 2, 1, 3, 4)
+    for r in range(16):
+        for b in range(4):                     # block b of a step lies at place b ^ (r / 4)
+            assert np.array_equal(pc.reshape(rb, c, 16, 4, 16)[:, :, r, b ^ (r // 4)], rows_first[:, :, r, b])
     wide = np.zeros((rb * 16, q * 16), np.uint8)
     wide[:rows, :K // 32] = scales
-    assert np.array_equal(ps.reshape(rb, q, 4, 16, 4),
-                          wide.reshape(rb, 16, q, 4, 4).transpose(0, 2, 4, 1, 3))
+    assert np.array_equal(ps.reshape(rb, q, 16, 4, 4),
+                          wide.reshape(rb, 16, q, 4, 4).transpose(0, 2, 1, 4, 3))
 
 
 def test_pack_rejects_bad_shapes():
