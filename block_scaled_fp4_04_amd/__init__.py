@@ -660,61 +660,56 @@ class Sequence:
             self._h, x.data_ptr(), rows, K, x.stride(0), out.codes.data_ptr(),
             out.scales.data_ptr()), f"{fn}(rows={rows}, K={K})")
 
-    def _record(self, fn, name: str, args: tuple, keep: list) -> None:
+    def _record(self, fn, args: tuple, keep: list) -> None:
         self._keep += keep
-        self._check(fn(self._h, *args), name)
+        self._check(fn(self._h, *args), fn.__name__)
 
     def add_mx_quantize(self, x, out: "MxOperand") -> None:
         """Records mx_quantize(x, out) for a 2-D x."""
         if x.dim() != 2:
             raise ValueError("x must be a 2-D tensor")
         out, a = mx._quantize_args(x, out)
-        mx._device_of(x, out.codes, out.scales)
-        self._record(mx.mx_lib().nvfp4_sequence_add_mx_quantize, "nvfp4_sequence_add_mx_quantize",
-                     a[:2] + a[4:], [x, out])
+        mx._gpu_of((x, out.codes, out.scales))
+        self._record(mx.mx_lib().nvfp4_sequence_add_mx_quantize, a[:2] + a[4:], [x, out])
 
     def add_mx_gemm(self, a: "MxOperand", b: "MxOperand", out, alpha: float = 1.0) -> None:
         """Records mx_gemm(a, b, alpha, out)."""
         out, args = mx._gemm_args(a, b, alpha, out, None)
-        mx._device_of(a.codes, a.scales, b.codes, b.scales, out)
-        self._record(mx.mx_lib().nvfp4_sequence_add_mx_gemm, "nvfp4_sequence_add_mx_gemm", args,
+        mx._gpu_of((a.codes, a.scales, b.codes, b.scales, out))
+        self._record(mx.mx_lib().nvfp4_sequence_add_mx_gemm, args,
                      [a, b, out])
 
     def add_mx_gemm_quantized(self, x, b: "MxOperand", out, alpha: float = 1.0) -> None:
         """Records mx_gemm_quantized(x, b, alpha, out)."""
         out, args = mx._gemm_quantized_args(x, b, alpha, out, None)
-        mx._device_of(x, b.codes, b.scales, out)
-        self._record(mx.mx_lib().nvfp4_sequence_add_mx_gemm_quantized,
-                     "nvfp4_sequence_add_mx_gemm_quantized", args, [x, b, out])
+        mx._gpu_of((x, b.codes, b.scales, out))
+        self._record(mx.mx_lib().nvfp4_sequence_add_mx_gemm_quantized, args, [x, b, out])
 
     def add_mx_grouped_gemm(self, a: "MxOperand", b: "MxGroups", row_offsets, out,
                             alpha: float = 1.0, rows=None) -> None:
         """Records mx_grouped_gemm(a, b, row_offsets, alpha, rows, out)."""
         out, args = mx._grouped_args(a, b, row_offsets, alpha, rows, out, None)
-        mx._device_of(a.codes, a.scales, b.codes, b.scales, row_offsets, rows, out)
-        self._record(mx.mx_lib().nvfp4_sequence_add_mx_grouped_gemm,
-                     "nvfp4_sequence_add_mx_grouped_gemm", args, [a, b, row_offsets, rows, out])
+        mx._gpu_of((a.codes, a.scales, b.codes, b.scales, row_offsets, rows, out))
+        self._record(mx.mx_lib().nvfp4_sequence_add_mx_grouped_gemm, args, [a, b, row_offsets, rows, out])
 
     def add_moe_sort(self, expert_ids, out: "MoeRoute") -> None:
         """Records moe_sort(expert_ids, out.experts, out)."""
         out, args = moe._sort_args(expert_ids, out.experts, out)
-        mx._device_of(expert_ids, out.row_offsets, out.slots, out.tokens)
-        self._record(moe.moe_lib().nvfp4_sequence_add_moe_sort, "nvfp4_sequence_add_moe_sort", args,
+        mx._gpu_of((expert_ids, out.row_offsets, out.slots, out.tokens))
+        self._record(moe.moe_lib().nvfp4_sequence_add_moe_sort, args,
                      [expert_ids, out])
 
     def add_moe_gather(self, x, route: "MoeRoute", out) -> None:
         """Records moe_gather(x, route, out)."""
         out, args = moe._gather_args(x, route, out)
-        mx._device_of(x, route.slots, out)
-        self._record(moe.moe_lib().nvfp4_sequence_add_moe_gather, "nvfp4_sequence_add_moe_gather",
-                     args, [x, route, out])
+        mx._gpu_of((x, route.slots, out))
+        self._record(moe.moe_lib().nvfp4_sequence_add_moe_gather, args, [x, route, out])
 
     def add_moe_combine(self, y, route: "MoeRoute", weights, out) -> None:
         """Records moe_combine(y, route, weights, out)."""
         out, args = moe._combine_args(y, route, weights, out)
-        mx._device_of(y, route.slots, weights, out)
-        self._record(moe.moe_lib().nvfp4_sequence_add_moe_combine, "nvfp4_sequence_add_moe_combine",
-                     args, [y, route, weights, out])
+        mx._gpu_of((y, route.slots, weights, out))
+        self._record(moe.moe_lib().nvfp4_sequence_add_moe_combine, args, [y, route, weights, out])
 
     def finalize(self) -> None:
         st = lib().nvfp4_sequence_finalize(self._h)

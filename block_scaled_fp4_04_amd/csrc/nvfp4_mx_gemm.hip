@@ -241,11 +241,11 @@ __global__ void __launch_bounds__(256, 1) mx_tile_kernel(MxGemmArgs a, int tiles
     // contiguous range of tiles, so that the tiles that run together share
     // their operands in its L2: walked in groups of 8 along M, or, grouped,
     // row block by row block in the groups' order.
-    int t = blockIdx.x;
-    {
-        const int total = tiles_m * tiles_n;
-        if ((total & 7) == 0) t = (t & 7) * (total >> 3) + (t >> 3);
-    }
+    auto tile_of = [&](int total) {  // -1: none
+        const int x = blockIdx.x & 7, per = total >> 3, more = total & 7;
+        const int k = blockIdx.x >> 3;
+        return k < per + (x < more) ? x * per + min(x, more) + k : -1;
+    };
     int tn, m0, row_end = a.M;
     int64_t b_first;  // first row block of this tile's B
     if constexpr (GROUPED) {
@@ -253,8 +253,7 @@ __global__ void __launch_bounds__(256, 1) mx_tile_kernel(MxGemmArgs a, int tiles
         // the grid is an upper bound.  Each thread counts those of a run of
         // groups, and the one whose run holds this tile's publishes it.
         int* sch = reinterpret_cast<int*>(lds);
-        const int tid = threadIdx.x, vm = t / tiles_n;
-        tn = t % tiles_n;
+        const int tid = threadIdx.x;
         const int per = (a.groups + 255) / 256;
         const int g_lo = min(tid * per, a.groups), g_hi = min(g_lo + per, a.groups);
         auto rows_of = [&](int g, int& r0, int& r1) {
@@ -267,7 +266,7 @@ __global__ void __launch_bounds__(256, 1) mx_tile_kernel(MxGemmArgs a, int tiles
             rows_of(g, r0, r1);
             cnt += (r1 - r0 + BM - 1) / BM;
         }
-        const int mine = (int)min(cnt, (int64_t)1 << 22);
+        const int mine = (int)min(cnt, (int64_t)1 << 22);  // (M < 2^28: no more in a sound one)
         int incl = mine;
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
@@ -275,9 +274,12 @@ __global__ void __launch_bounds__(256, 1) mx_tile_kernel(MxGemmArgs a, int tiles
             if (lane >= o) incl += y;
         }
         if (lane == 63) sch[wave] = incl;
-        if (tid == 0) sch[4] = -1;
         __syncthreads();
-        int at = vm - (incl - mine);
+        // (the XCDs share the tiles that there are, not the grid's bound)
+        const int t = tile_of(min(sch[0] + sch[1] + sch[2] + sch[3], tiles_m) * tiles_n);
+        if (t < 0) return;  // past the last row block: the whole workgroup leaves
+        tn = t % tiles_n;
+        int at = t / tiles_n - (incl - mine);
         for (int w = 0; w < wave; ++w) at -= sch[w];
         if (at >= 0 && at < mine)
             for (int g = g_lo; g < g_hi; ++g) {
@@ -294,13 +296,13 @@ __global__ void __launch_bounds__(256, 1) mx_tile_kernel(MxGemmArgs a, int tiles
             }
         __syncthreads();
         const int g = __builtin_amdgcn_readfirstlane(sch[4]);
-        if (g < 0) return;  // past the last row block: the whole workgroup leaves
         m0 = __builtin_amdgcn_readfirstlane(sch[5]);
         row_end = __builtin_amdgcn_readfirstlane(sch[6]);
         b_first = (int64_t)g * a.RBb + (int64_t)tn * BF;
         __syncthreads();  // everyone has read before the ring fills
     } else {
         constexpr int GROUP_M = 8;
+        const int t = tile_of(tiles_m * tiles_n);
         const int in_group = GROUP_M * tiles_n;
         const int first_m = (t / in_group) * GROUP_M;
         const int gsize = min(tiles_m - first_m, GROUP_M);
@@ -570,14 +572,17 @@ void run_few_rows(Launch& l) {
 void choose(Launch& l) {
     const MxGemmArgs& a = l.a;
     if (a.groups > 0) {
-        if (a.M / a.groups <= 32) return run_split<2, 4, 4, A_PACKED, true>(l);
-        if (a.C <= kMxTileSteps && (int64_t)a.RBa * a.C * kMxFrag < ((int64_t)1 << 31)) {
+        static const int dv = getenv("MXV") ? atoi(getenv("MXV")) : 0;
+        if (dv != 2 && dv != 7 && dv != 8 && a.M / a.groups <= 32) return run_split<2, 4, 4, A_PACKED, true>(l);
+        if (a.C <= kMxTileSteps && a.M < (1 << 28) && (int64_t)a.RBa * a.C * kMxFrag < ((int64_t)1 << 31)) {
             static const int v = getenv("MXV") ? atoi(getenv("MXV")) : 0;
             if (v == 1) return run_tile<128, 256, 3, 2, true>(l);
             if (v == 2) return run_tile<64, 256, 3, 1, true>(l);
             if (v == 3) return run_tile<256, 256, 4, 2, true>(l);
             if (v == 4) return run_tile<128, 256, 4, 2, true>(l);
             if (v == 5) return run_tile<64, 256, 4, 1, true>(l);
+            if (v == 7) return run_tile<64, 256, 2, 1, true>(l);
+            if (v == 8) return run_tile<128, 128, 3, 2, true>(l);
             return run_tile<128, 128, 4, 2, true>(l);
         }
         return run_split<4, 4, 8, A_PACKED, true>(l);

@@ -16,7 +16,7 @@ import ctypes
 from dataclasses import dataclass
 
 from . import _i64, _vp, lib
-from .mx import _device_of, _rows_2d, _run
+from .mx import _on, _rows_2d, _run
 
 INDEX_I32 = 0   # types of expert numbers (nvfp4_moe.h)
 INDEX_I64 = 1
@@ -39,7 +39,8 @@ def moe_lib() -> ctypes.CDLL:
     global _bound
     L = lib()
     if _bound is not L:
-        for name, types in (("nvfp4_moe_sort", _SORT + [_vp]), ("nvfp4_moe_gather", _GATHER + [_vp]),
+        for name, types in (("nvfp4_moe_sort", _SORT + [_vp]),
+                            ("nvfp4_moe_gather", _GATHER + [_vp]),
                             ("nvfp4_moe_combine", _COMBINE + [_vp]),
                             ("nvfp4_moe_combine_grad", _GRAD + [_vp]),
                             ("nvfp4_sequence_add_moe_sort", [_vp] + _SORT),
@@ -64,10 +65,10 @@ class MoeRoute:
 
     def check(self) -> None:
         import torch
-        n = self.slots.numel()
-        for what, t, ok in (("row_offsets", self.row_offsets, self.row_offsets.numel() == self.experts + 1),
-                            ("slots", self.slots, self.slots.dim() == 2),
-                            ("tokens", self.tokens, self.tokens.numel() == n)):
+        off, slots, tokens = self.row_offsets, self.slots, self.tokens
+        for what, t, ok in (("row_offsets", off, off.numel() == self.experts + 1),
+                            ("slots", slots, slots.dim() == 2),
+                            ("tokens", tokens, tokens.numel() == slots.numel())):
             if t.dtype != torch.int32 or not t.is_contiguous() or not ok:
                 raise ValueError(f"route.{what} must be a contiguous int32 tensor of its shape")
 
@@ -78,8 +79,9 @@ def _sort_args(ids, experts, out):
         raise ValueError("expert_ids must be a contiguous [tokens, topk] int32 or int64 tensor")
     T, k = ids.shape
     if out is None:
-        both = torch.empty(2 * T * k + experts + 1, dtype=torch.int32, device=ids.device)
-        out = MoeRoute(both[2 * T * k:], both[:T * k].view(T, k), both[T * k:2 * T * k], experts)
+        tables = ids.new_empty(2 * T * k + experts + 1, dtype=torch.int32)
+        slots, tokens, off = tables.split((T * k, T * k, experts + 1))
+        out = MoeRoute(off, slots.view(T, k), tokens, experts)
     else:
         out.check()
         if out.experts != experts or tuple(out.slots.shape) != (T, k):
@@ -93,9 +95,11 @@ def moe_sort(expert_ids, experts: int, out: MoeRoute | None = None, stream=None)
     device tensor; numbers outside [0, experts) are dropped choices), by
     expert, those of one expert by token (nvfp4_moe_sort).  At most
     MOE_MAX_EXPERTS experts."""
+    if stream is not None:
+        with _on(stream):
+            return moe_sort(expert_ids, experts, out)
     out, args = _sort_args(expert_ids, experts, out)
-    _run(moe_lib().nvfp4_moe_sort, "nvfp4_moe_sort", args,
-         _device_of(expert_ids, out.row_offsets, out.slots, out.tokens), stream)
+    _run(moe_lib().nvfp4_moe_sort, args, (expert_ids, out.row_offsets, out.slots, out.tokens))
     return out
 
 
@@ -105,15 +109,16 @@ def _weights(weights, route):
         return None
     if (weights.dtype != torch.float32 or weights.shape != route.slots.shape
             or not weights.is_contiguous()):
-        raise ValueError(f"weights must be a contiguous float32 tensor of shape {tuple(route.slots.shape)}")
+        raise ValueError("weights must be a contiguous float32 tensor of shape "
+                         f"{tuple(route.slots.shape)}")
     return weights.data_ptr()
 
 
-def _like(t, name: str, rows: int, hidden: int, dtype, device):
-    """`t` made, or checked to be a contiguous rows x hidden tensor of `dtype`."""
+def _like(t, name: str, rows: int, hidden: int, dtype, like):
+    """`t` made beside `like`, or checked to be a contiguous rows x hidden tensor of `dtype`."""
     import torch
     if t is None:
-        return torch.empty((rows, hidden), dtype=dtype, device=device)
+        return like.new_empty((rows, hidden), dtype=dtype)
     if tuple(t.shape) != (rows, hidden) or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape ({rows}, {hidden})")
     return t
@@ -125,7 +130,7 @@ def _gather_args(x, route, out):
     T, k = route.slots.shape
     if x.shape[0] != T:
         raise ValueError(f"x has {x.shape[0]} rows, the route {T} tokens")
-    out = _like(out, "out", T * k, x.shape[1], x.dtype, x.device)
+    out = _like(out, "out", T * k, x.shape[1], x.dtype, x)
     return out, (x.data_ptr(), kind, T, k, x.shape[1], x.stride(0), route.slots.data_ptr(),
                  out.data_ptr())
 
@@ -135,9 +140,11 @@ def moe_gather(x, route: MoeRoute, out=None, stream=None):
     order, one for each kept choice (nvfp4_moe_gather): [tokens * topk,
     hidden].  Rows that no choice owns (behind row_offsets[-1]) are left as
     they were in ``out``."""
+    if stream is not None:
+        with _on(stream):
+            return moe_gather(x, route, out)
     out, args = _gather_args(x, route, out)
-    _run(moe_lib().nvfp4_moe_gather, "nvfp4_moe_gather", args,
-         _device_of(x, route.row_offsets, route.slots, route.tokens, out), stream)
+    _run(moe_lib().nvfp4_moe_gather, args, (x, route.slots, out))
     return out
 
 
@@ -145,9 +152,9 @@ def _combine_args(y, route, weights, out):
     kind = _rows_2d(y, "y")
     route.check()
     T, k = route.slots.shape
-    y = _like(y, "y", T * k, y.shape[1], y.dtype, y.device)
+    y = _like(y, "y", T * k, y.shape[1], y.dtype, y)
     w = _weights(weights, route)
-    out = _like(out, "out", T, y.shape[1], y.dtype, y.device)
+    out = _like(out, "out", T, y.shape[1], y.dtype, y)
     return out, (y.data_ptr(), kind, T, k, y.shape[1], route.slots.data_ptr(), w, out.data_ptr())
 
 
@@ -155,9 +162,11 @@ def moe_combine(y, route: MoeRoute, weights=None, out=None, stream=None):
     """out[t] = sum over token t's kept choices of weights[t, j] * y[row of the
     choice] (nvfp4_moe_combine), summed in fp32 in the order of j: [tokens,
     hidden].  ``weights``: float32 [tokens, topk]; None for ones."""
+    if stream is not None:
+        with _on(stream):
+            return moe_combine(y, route, weights, out)
     out, args = _combine_args(y, route, weights, out)
-    _run(moe_lib().nvfp4_moe_combine, "nvfp4_moe_combine", args,
-         _device_of(y, route.row_offsets, route.slots, route.tokens, weights, out), stream)
+    _run(moe_lib().nvfp4_moe_combine, args, (y, route.slots, weights, out))
     return out
 
 
@@ -172,6 +181,9 @@ def moe_combine_grad(dout, y, route: MoeRoute, weights=None, dy=None, dweights=N
     output's gradient ``dout`` [tokens, hidden] (rows may be strided)
     (nvfp4_moe_combine_grad).  Rows of dy that no choice owns are left as they
     were; dweights of dropped choices are zero.  ``dy`` may be y itself."""
+    if stream is not None:
+        with _on(stream):
+            return moe_combine_grad(dout, y, route, weights, dy, dweights)
     import torch
     kind = _rows_2d(dout, "dout")
     route.check()
@@ -179,13 +191,11 @@ def moe_combine_grad(dout, y, route: MoeRoute, weights=None, dy=None, dweights=N
     if dout.shape[0] != T:
         raise ValueError(f"dout has {dout.shape[0]} rows, the route {T} tokens")
     H = dout.shape[1]
-    y = _like(y, "y", T * k, H, dout.dtype, dout.device)
+    y = _like(y, "y", T * k, H, dout.dtype, dout)
     w = _weights(weights, route)
-    dy = _like(dy, "dy", T * k, H, dout.dtype, dout.device)
-    dweights = _like(dweights, "dweights", T, k, torch.float32, dout.device)
+    dy = _like(dy, "dy", T * k, H, dout.dtype, dout)
+    dweights = _like(dweights, "dweights", T, k, torch.float32, dout)
     args = (dout.data_ptr(), dout.stride(0), y.data_ptr(), kind, T, k, H, route.slots.data_ptr(), w,
             dy.data_ptr(), dweights.data_ptr())
-    _run(moe_lib().nvfp4_moe_combine_grad, "nvfp4_moe_combine_grad", args,
-         _device_of(dout, y, route.row_offsets, route.slots, route.tokens, weights, dy, dweights),
-         stream)
+    _run(moe_lib().nvfp4_moe_combine_grad, args, (dout, y, route.slots, weights, dy, dweights))
     return dy, dweights

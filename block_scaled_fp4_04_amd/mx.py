@@ -177,36 +177,40 @@ def mx_groups_to_device(codes: np.ndarray, scales: np.ndarray, device="cuda") ->
 # ---- what the calls share ---------------------------------------------------
 
 
-def _device_of(*tensors):
-    """The GPU that all the tensors (None left out) lie on."""
-    device = None
+def _gpu_of(tensors) -> int:
+    """The index of the GPU that all the tensors (None left out) lie on."""
+    gpu = tensors[0].get_device()
     for t in tensors:
-        if t is None:
-            continue
-        if device is None:
-            device = t.device
-            if device.type != "cuda":
-                raise ValueError(f"tensors must be on a GPU, not on {device}")
-        elif t.device != device:
-            raise ValueError(f"tensors must be on one device, not on {device} and {t.device}")
-    return device
+        if t is not None and t.get_device() != gpu:
+            raise ValueError(f"tensors must be on one device, not on {tensors[0].device} and {t.device}")
+    if gpu < 0:
+        raise ValueError(f"tensors must be on a GPU, not on {tensors[0].device}")
+    return gpu
 
 
-def _run(fn, name: str, args: tuple, device, stream) -> None:
-    """Calls the C function on `device`, on `stream` or that device's current
-    one."""
+def _on(stream):
+    """The context of a stream (a torch stream or a raw handle): what a call
+    allocates in it belongs to that stream."""
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    handle = int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
-    if device.index == torch.cuda.current_device():
-        st = fn(*args, handle)
+    if not hasattr(stream, "cuda_stream"):
+        stream = (torch.cuda.ExternalStream(int(stream)) if int(stream)
+                  else torch.cuda.default_stream())
+    return torch.cuda.stream(stream)
+
+
+def _run(fn, args: tuple, tensors: tuple) -> None:
+    """Calls the C function on the GPU where the tensors lie, on its current
+    stream."""
+    import torch
+    gpu = _gpu_of(tensors)
+    if gpu == torch._C._cuda_getDevice():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(gpu))
     else:
-        with torch.cuda.device(device):
-            st = fn(*args, handle)
+        with torch.cuda.device(gpu):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(gpu))
     if st:
         sizes = ", ".join(str(a) for a in args if isinstance(a, int) and 0 <= a < 1 << 31)
-        raise Nvfp4Error(st, f"{name}({sizes})")
+        raise Nvfp4Error(st, f"{fn.__name__}({sizes})")
 
 
 def _type_of(dtype, what: str) -> int:
@@ -218,11 +222,11 @@ def _type_of(dtype, what: str) -> int:
     raise ValueError(f"{what} must be float32 or bfloat16, not {dtype}")
 
 
-def _out(out, dtype, M: int, N: int, device):
-    """The output tensor (made, or the given one checked) and its type code."""
-    import torch
+def _out(out, dtype, M: int, N: int, like):
+    """The output tensor (made beside `like`, or the given one checked) and its
+    type code."""
     if out is None:
-        out = torch.empty((M, N), dtype=dtype, device=device)
+        out = like.new_empty((M, N), dtype=dtype)
     elif tuple(out.shape) != (M, N) or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous tensor of shape ({M}, {N})")
     return out, _type_of(out.dtype, "out")
@@ -248,8 +252,8 @@ def _quantize_args(x, out):
         if K < MX_BLOCK or K % MX_BLOCK:
             raise ValueError(f"K must be a positive multiple of {MX_BLOCK}, not {K}")
         cb, sb = _packed(rows, K)
-        codes = torch.empty(cb * groups, dtype=torch.uint8, device=x.device)
-        scales = torch.empty(sb * groups, dtype=torch.uint8, device=x.device)
+        codes = x.new_empty(cb * groups, dtype=torch.uint8)
+        scales = x.new_empty(sb * groups, dtype=torch.uint8)
         out = (MxGroups(codes, scales, groups, rows, K) if x.dim() == 3
                else MxOperand(codes, scales, rows, K))
     else:
@@ -266,15 +270,20 @@ def mx_quantize(x, out=None, stream=None):
     (groups x rows x K, the weights of a layer of experts) MxGroups; or fills
     ``out``.  K is a multiple of 32; rows and groups may be strided (by whole
     16 bytes)."""
+    if stream is not None:
+        with _on(stream):
+            return mx_quantize(x, out)
     out, args = _quantize_args(x, out)
-    _run(mx_lib().nvfp4_mx_quantize, "nvfp4_mx_quantize", args,
-         _device_of(x, out.codes, out.scales), stream)
+    _run(mx_lib().nvfp4_mx_quantize, args, (x, out.codes, out.scales))
     return out
 
 
 def mx_dequantize(a, dtype=None, out=None, stream=None):
     """The values of an MxOperand (rows x K) or MxGroups (groups x rows x K)
     as bfloat16 (default) or float32, exact in both (nvfp4_mx_dequantize)."""
+    if stream is not None:
+        with _on(stream):
+            return mx_dequantize(a, dtype, out)
     import torch
     groups = getattr(a, "groups", None)
     shape = (a.rows, a.K) if groups is None else (groups, a.rows, a.K)
@@ -286,8 +295,7 @@ def mx_dequantize(a, dtype=None, out=None, stream=None):
     args = (a.codes.data_ptr(), a.scales.data_ptr(), 1 if groups is None else groups, a.rows, a.K,
             out.data_ptr(), _type_of(out.dtype, "out"), 0 if groups is None else out.stride(0),
             out.stride(-2))
-    _run(mx_lib().nvfp4_mx_dequantize, "nvfp4_mx_dequantize", args,
-         _device_of(a.codes, a.scales, out), stream)
+    _run(mx_lib().nvfp4_mx_dequantize, args, (a.codes, a.scales, out))
     return out
 
 
@@ -296,7 +304,7 @@ def _gemm_args(a, b, alpha, out, dtype):
         raise ValueError(f"K dimension mismatch: A has K={a.K}, B has K={b.K}")
     a.check("a")
     b.check("b")
-    out, kind = _out(out, dtype, a.rows, b.rows, a.codes.device)
+    out, kind = _out(out, dtype, a.rows, b.rows, a.codes)
     return out, (a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(), b.scales.data_ptr(),
                  float(alpha), out.data_ptr(), kind, a.rows, b.rows, a.K)
 
@@ -304,10 +312,12 @@ def _gemm_args(a, b, alpha, out, dtype):
 def mx_gemm(a: MxOperand, b: MxOperand, alpha: float = 1.0, out=None, dtype=None, stream=None):
     """C = alpha * (A . B^T) of packed MXFP4 operands (nvfp4_mx_gemm): M x N,
     bfloat16 unless ``dtype`` or ``out`` says float32."""
+    if stream is not None:
+        with _on(stream):
+            return mx_gemm(a, b, alpha, out, dtype)
     import torch
     out, args = _gemm_args(a, b, alpha, out, dtype or torch.bfloat16)
-    _run(mx_lib().nvfp4_mx_gemm, "nvfp4_mx_gemm", args,
-         _device_of(a.codes, a.scales, b.codes, b.scales, out), stream)
+    _run(mx_lib().nvfp4_mx_gemm, args, (a.codes, a.scales, b.codes, b.scales, out))
     return out
 
 
@@ -317,7 +327,7 @@ def _gemm_quantized_args(x, b, alpha, out, dtype):
     if K != b.K:
         raise ValueError(f"K dimension mismatch: x has K={K}, B has K={b.K}")
     b.check("b")
-    out, out_kind = _out(out, dtype, M, b.rows, x.device)
+    out, out_kind = _out(out, dtype, M, b.rows, x)
     return out, (x.data_ptr(), kind, x.stride(0), b.codes.data_ptr(), b.scales.data_ptr(),
                  float(alpha), out.data_ptr(), out_kind, M, b.rows, K)
 
@@ -326,10 +336,12 @@ def mx_gemm_quantized(x, b: MxOperand, alpha: float = 1.0, out=None, dtype=None,
     """mx_gemm(mx_quantize(x), b, alpha) in one launch, bit for bit
     (nvfp4_mx_gemm_quantized): x holds up to MX_QUANT_ROWS rows of fp32 or
     bfloat16 activations."""
+    if stream is not None:
+        with _on(stream):
+            return mx_gemm_quantized(x, b, alpha, out, dtype)
     import torch
     out, args = _gemm_quantized_args(x, b, alpha, out, dtype or torch.bfloat16)
-    _run(mx_lib().nvfp4_mx_gemm_quantized, "nvfp4_mx_gemm_quantized", args,
-         _device_of(x, b.codes, b.scales, out), stream)
+    _run(mx_lib().nvfp4_mx_gemm_quantized, args, (x, b.codes, b.scales, out))
     return out
 
 
@@ -337,9 +349,12 @@ def mx_linear(x, b: MxOperand, alpha: float = 1.0, out=None, dtype=None, stream=
     """C = alpha * (quantise(x) . B^T) for plain activations x (rows x K,
     fp32 or bfloat16): one launch where mx_gemm_quantized is the faster form
     (few rows), else mx_quantize and mx_gemm.  Both give the same bits."""
+    if stream is not None:
+        with _on(stream):
+            return mx_linear(x, b, alpha, out, dtype)
     if x.dim() == 2 and x.shape[0] <= _one_launch_rows(x, b):
-        return mx_gemm_quantized(x, b, alpha, out, dtype, stream)
-    return mx_gemm(mx_quantize(x, stream=stream), b, alpha, out, dtype, stream)
+        return mx_gemm_quantized(x, b, alpha, out, dtype)
+    return mx_gemm(mx_quantize(x), b, alpha, out, dtype)
 
 
 def _one_launch_rows(x, b) -> int:
@@ -354,12 +369,13 @@ def _grouped_args(a, b, row_offsets, alpha, rows, out, dtype):
     if (row_offsets.dtype != torch.int32 or row_offsets.numel() != b.groups + 1
             or not row_offsets.is_contiguous()):
         raise ValueError(f"row_offsets must be a contiguous int32 tensor of {b.groups + 1} entries")
-    if rows is not None and (rows.dtype != torch.int32 or rows.dim() != 1 or not rows.is_contiguous()):
+    if rows is not None and (rows.dtype != torch.int32 or rows.dim() != 1
+                             or not rows.is_contiguous()):
         raise ValueError("rows must be a contiguous 1-D int32 tensor")
     a.check("a")
     b.check("b")
     M = a.rows if rows is None else rows.numel()
-    out, kind = _out(out, dtype, M, b.rows, a.codes.device)
+    out, kind = _out(out, dtype, M, b.rows, a.codes)
     return out, (a.codes.data_ptr(), a.scales.data_ptr(), a.rows,
                  None if rows is None else rows.data_ptr(), b.codes.data_ptr(),
                  b.scales.data_ptr(), row_offsets.data_ptr(), b.groups, float(alpha),
@@ -373,8 +389,11 @@ def mx_grouped_gemm(a: MxOperand, b: MxGroups, row_offsets, alpha: float = 1.0, 
     operand.  Row r of C takes row rows[r] of A (``MoeRoute.tokens``: the
     activations are quantised once per token and never copied), or row r
     without ``rows``.  Rows behind the last group are left as they were."""
+    if stream is not None:
+        with _on(stream):
+            return mx_grouped_gemm(a, b, row_offsets, alpha, rows, out, dtype)
     import torch
     out, args = _grouped_args(a, b, row_offsets, alpha, rows, out, dtype or torch.bfloat16)
-    _run(mx_lib().nvfp4_mx_grouped_gemm, "nvfp4_mx_grouped_gemm", args,
-         _device_of(a.codes, a.scales, b.codes, b.scales, row_offsets, rows, out), stream)
+    _run(mx_lib().nvfp4_mx_grouped_gemm, args,
+         (a.codes, a.scales, b.codes, b.scales, row_offsets, rows, out))
     return out
