@@ -206,8 +206,8 @@ __global__ void __launch_bounds__(W * 64) mx_split_kernel(MxGemmArgs a) {
 //
 // The fragments of the packed layout (16 rows x one step, 1 KB) go from
 // memory to LDS as they are (direct-to-LDS loads, 16 bytes a lane) into a
-// ring of NS steps; a quarter of the next scale word's fragments travels with
-// each step.  A lane then reads its 16 code bytes with one LDS read, 16 lanes
+// ring of NS steps, and the scale words, four steps at a time, to a buffer of
+// their own.  A lane then reads its 16 code bytes with one LDS read, 16 lanes
 // side by side.  Operands of a 64-element half step are read while the MFMAs
 // of the half before run.  One barrier a step, in its middle: every wave has
 // then read all of the step's buffer, which takes the loads of step + NS, and
@@ -217,20 +217,19 @@ __global__ void __launch_bounds__(W * 64) mx_split_kernel(MxGemmArgs a) {
 // are not stored.  Steps past the last one load it again, unused.
 // ---------------------------------------------------------------------------
 template <int BM, int BN, int NS, int WM, bool GROUPED>
-__global__ void __launch_bounds__(256, 1) mx_tile_kernel(MxGemmArgs a, int tiles_m, int tiles_n) {
+__global__ void __launch_bounds__(256, BM * BN > 128 * 256 ? 1 : 2) mx_tile_kernel(MxGemmArgs a, int tiles_m, int tiles_n) {
     constexpr int WN = 4 / WM;                            // waves along M and N
     constexpr int MI = BM / 32 / WM, NI = BN / 32 / WN;   // 32 x 32 blocks of a wave
     constexpr int AF = BM / 16, BF = BN / 16;             // fragments of a step
     constexpr int CPW = (AF + BF) / 4;                    // of them, a wave's loads
-    constexpr int SPS = (AF + BF) / 4;           // scale fragments that travel with a step
-    constexpr int SPW = (SPS + 3) / 4;           // of them, a wave's loads
-    constexpr int L = CPW + SPW;
+    constexpr int SPW = CPW;                              // a wave's scale loads, every fourth step
     constexpr int STAGE = (AF + BF) * kMxFrag;
-    constexpr int SCALES = (AF + BF) * kMxScaleFrag;  // of four steps
-    // (NS <= 4: the loads of a scale word start once the word two before is read)
-    static_assert((AF + BF) % 4 == 0 && NS >= 2 && NS <= 4 && (NS - 1) * L < 64, "ring");
-    static_assert(BM * WN * (BN / WN * 2 + 16) <= NS * STAGE + 2 * SCALES, "the output is staged in the ring");
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * STAGE + 2 * SCALES];
+    constexpr int SCALES = (AF + BF) * kMxScaleFrag;      // of four steps
+    // (NS <= 4: the next scale word's loads, issued in the middle of a word's
+    // first step, have landed in the middle of its last one)
+    static_assert((AF + BF) % 4 == 0 && NS >= 2 && NS <= 4 && NS * CPW + SPW < 64, "ring");
+    static_assert(BM * WN * (BN / WN * 2 + 16) <= NS * STAGE + SCALES, "the output is staged in the ring");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * STAGE + SCALES];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 3;
@@ -329,49 +328,32 @@ __global__ void __launch_bounds__(256, 1) mx_tile_kernel(MxGemmArgs a, int tiles
         return (uint32_t)(a.a_rows ? min(max(a.a_rows[r], 0), a.A_rows - 1) : r);
     };
 
-    // A wave's loads: CPW code fragments of a step (number i is fragment wave *
-    // CPW + i) and SPW of the SPS scale fragments that travel with the step (a
-    // quarter of a scale word; with fewer than four a wave repeats one).
-    // Where they come from in the operands' memory, per lane:
-    uint32_t code_at[CPW], scale_at[4][SPW];
-    bool scale_a[4][SPW];
-    int scale_f[4][SPW];
+    // A wave's loads: number i is fragment wave * CPW + i of a step's codes, or
+    // of a scale word.  Where they come from in the operands' memory, per lane:
+    uint32_t code_at[CPW], scale_at[SPW];
 #pragma unroll
     for (int i = 0; i < CPW; ++i) {
         const int f = wave * CPW + i;
-        code_at[i] = (uint32_t)(f < AF ? f : f - AF) * (uint32_t)C * kMxFrag + lane * 16;
+        const uint32_t k = (uint32_t)(f < AF ? f : f - AF);
+        code_at[i] = k * (uint32_t)C * kMxFrag + lane * 16;
+        scale_at[i] = k * (uint32_t)Q * kMxScaleFrag + lane * 4;
         if (GROUPED && f < AF) {
             const uint32_t r = a_row(f);
             code_at[i] = (r >> 4) * (uint32_t)C * kMxFrag + mx_code_at(r & 15, (lane & 3) ^ (lane >> 4));
+            scale_at[i] = (r >> 4) * (uint32_t)Q * kMxScaleFrag + mx_scale_at(r & 15, lane & 3);
         }
     }
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-#pragma unroll
-        for (int i = 0; i < SPW; ++i) {
-            const int f = s * SPS + (wave * SPW + i) % SPS;
-            scale_f[s][i] = f;
-            scale_a[s][i] = f < AF;
-            scale_at[s][i] = (uint32_t)(f < AF ? f : f - AF) * (uint32_t)Q * kMxScaleFrag + lane * 4;
-            if (GROUPED && f < AF) {
-                const uint32_t r = a_row(f);
-                scale_at[s][i] = (r >> 4) * (uint32_t)Q * kMxScaleFrag + mx_scale_at(r & 15, lane & 3);
-            }
-        }
-    // Load number I of the step c, whose buffer is `stage`; the scales are
-    // quarter S of word q.
-    auto load = [&](auto I, auto S, int c, int stage, int q) {
+    // Load number I of step c into buffer `stage`, and of scale word q.
+    auto load_code = [&](auto I, int c, int stage) {
         constexpr int i = I.value;
-        if constexpr (i < CPW) {
-            const bool isA = wave * CPW + i < AF;
-            mx_dma<16, i * kMxFrag>(isA ? rac : rbc, code_at[i], (uint32_t)min(c, C - 1) * kMxFrag,
-                                    lds0 + (uint32_t)(stage * STAGE + wave * CPW * kMxFrag));
-        } else {
-            constexpr int k = i - CPW;
-            mx_dma<4, NS * STAGE>(scale_a[S.value][k] ? ras : rbs, scale_at[S.value][k],
-                                  (uint32_t)min(q, Q - 1) * kMxScaleFrag,
-                                  lds0 + (uint32_t)((q & 1) * SCALES + scale_f[S.value][k] * kMxScaleFrag));
-        }
+        mx_dma<16, i * kMxFrag>(wave * CPW + i < AF ? rac : rbc, code_at[i], (uint32_t)min(c, C - 1) * kMxFrag,
+                                lds0 + (uint32_t)(stage * STAGE + wave * CPW * kMxFrag));
+    };
+    auto load_scale = [&](auto I, int q) {
+        constexpr int i = I.value;
+        mx_dma<4, NS * STAGE + i * kMxScaleFrag>(wave * CPW + i < AF ? ras : rbs, scale_at[i],
+                                                 (uint32_t)min(q, Q - 1) * kMxScaleFrag,
+                                                 lds0 + (uint32_t)(wave * CPW * kMxScaleFrag));
     };
 
     mx_f16 acc[MI][NI];
@@ -407,15 +389,14 @@ __global__ void __launch_bounds__(256, 1) mx_tile_kernel(MxGemmArgs a, int tiles
             h.b[i - MI] = *reinterpret_cast<const mx_u4*>(p + (fb + 2 * (i - MI)) * kMxFrag);
     };
     // the two scale words of 32-row block I
-    auto read_scale = [&](auto I, Scales& s, int q) {
+    auto read_scale = [&](auto I, Scales& s) {
         constexpr int i = I.value;
-        const int at = (q & 1) * SCALES;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
             if constexpr (i < MI)
-                s.a[i][h] = *reinterpret_cast<const uint32_t*>(lane_sa + at + 2 * i * kMxScaleFrag + h * 8);
+                s.a[i][h] = *reinterpret_cast<const uint32_t*>(lane_sa + 2 * i * kMxScaleFrag + h * 8);
             else
-                s.b[i - MI][h] = *reinterpret_cast<const uint32_t*>(lane_sb + at + 2 * (i - MI) * kMxScaleFrag + h * 8);
+                s.b[i - MI][h] = *reinterpret_cast<const uint32_t*>(lane_sb + 2 * (i - MI) * kMxScaleFrag + h * 8);
     };
     Scales sc, sn;
     auto mfma = [&](auto N, auto S, const Half& h, int half) {
@@ -424,16 +405,12 @@ __global__ void __launch_bounds__(256, 1) mx_tile_kernel(MxGemmArgs a, int tiles
     };
 
     // fill the ring
-    mx_each<4>([&](auto S) {
-        mx_each<SPW>([&](auto I) { load(std::integral_constant<int, CPW + I.value>{}, S, 0, 0, 0); });
-    });
-    mx_each<NS>([&](auto c) {
-        mx_each<L>([&](auto I) { load(I, std::integral_constant<int, c.value & 3>{}, c.value, c.value, c.value / 4 + 1); });
-    });
-    wait_vmcnt<(NS - 1) * L>();  // step 0 and the first scale word
+    mx_each<SPW>([&](auto I) { load_scale(I, 0); });
+    mx_each<NS>([&](auto c) { mx_each<CPW>([&](auto I) { load_code(I, c.value, c.value); }); });
+    wait_vmcnt<(NS - 1) * CPW>();  // step 0 and the first scale word
     wg_barrier();
     Half h0, h1;
-    mx_each<P>([&](auto I) { read_scale(I, sc, 0); });
+    mx_each<P>([&](auto I) { read_scale(I, sc); });
     mx_each<P>([&](auto I) { read(I, h0, 0, 0); });
 
     // One step.  The order is fixed (the scheduling barriers): behind each
@@ -442,14 +419,16 @@ __global__ void __launch_bounds__(256, 1) mx_tile_kernel(MxGemmArgs a, int tiles
     // and the MFMAs wait for each.
     int c = 0, stage = 0;
     auto step = [&](auto S) {
-        constexpr int s = S.value, s_load = (s + NS) & 3;  // of the step being loaded
+        constexpr int s = S.value;
         mx_each<MM>([&](auto N) {
             mfma(N, S, h0, 0);
             if constexpr (N.value < P) read(N, h1, stage, 1);
             __builtin_amdgcn_sched_barrier(0);
         });
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        wait_vmcnt<(NS - 2) * L>();
+        // step c + 1 has landed: what may be in flight was issued in the last
+        // NS - 2 steps (the scales in a word's first one)
+        wait_vmcnt<(NS - 2) * CPW + (s > 0 && s <= NS - 2 ? SPW : 0)>();
         wg_barrier();
         __builtin_amdgcn_sched_barrier(0);
         const int freed = stage;
@@ -458,10 +437,11 @@ __global__ void __launch_bounds__(256, 1) mx_tile_kernel(MxGemmArgs a, int tiles
             constexpr int n = N.value;
             mfma(N, S, h1, 1);
             if constexpr (n < P) read(N, h0, stage, 0);
-            if constexpr (s == 3 && n >= MM - P) read_scale(std::integral_constant<int, n - (MM - P)>{}, sn, c / 4 + 1);
-            mx_each<(n + 1) * L / MM - n * L / MM>([&](auto I) {
-                load(std::integral_constant<int, n * L / MM + I.value>{}, std::integral_constant<int, s_load>{},
-                     c + NS, freed, (c + NS) / 4 + 1);
+            if constexpr (s == 3 && n >= MM - P) read_scale(std::integral_constant<int, n - (MM - P)>{}, sn);
+            mx_each<(n + 1) * CPW / MM - n * CPW / MM>([&](auto I) {
+                constexpr int i = n * CPW / MM + I.value;
+                load_code(std::integral_constant<int, i>{}, c + NS, freed);
+                if constexpr (s == 0) load_scale(std::integral_constant<int, i>{}, c / 4 + 1);
             });
             __builtin_amdgcn_sched_barrier(0);
         });
