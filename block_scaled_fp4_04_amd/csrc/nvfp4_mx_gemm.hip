@@ -216,8 +216,8 @@ __global__ void __launch_bounds__(W * 64) mx_split_kernel(MxGemmArgs a) {
 // Rows past the operands' ends read as zeros (the buffers' range check) and
 // are not stored.  Steps past the last one load it again, unused.
 // ---------------------------------------------------------------------------
-template <int BM, int BN, int NS, int WM, bool GROUPED>
-__global__ void __launch_bounds__(256, BM * BN > 128 * 256 ? 1 : 2) mx_tile_kernel(MxGemmArgs a, int tiles_m, int tiles_n) {
+template <int BM, int BN, int NS, int WM, int KS, bool GROUPED>
+__global__ void __launch_bounds__(KS * 256, KS > 1 || BM * BN > 128 * 256 ? KS : 2) mx_tile_kernel(MxGemmArgs a, int tiles_m, int tiles_n) {
     constexpr int WN = 4 / WM;                            // waves along M and N
     constexpr int MI = BM / 32 / WM, NI = BN / 32 / WN;   // 32 x 32 blocks of a wave
     constexpr int AF = BM / 16, BF = BN / 16;             // fragments of a step
@@ -228,11 +228,15 @@ __global__ void __launch_bounds__(256, BM * BN > 128 * 256 ? 1 : 2) mx_tile_kern
     // (NS <= 4: the next scale word's loads, issued in the middle of a word's
     // first step, have landed in the middle of its last one)
     static_assert((AF + BF) % 4 == 0 && NS >= 2 && NS <= 4 && NS * CPW + SPW < 64, "ring");
-    static_assert(BM * WN * (BN / WN * 2 + 16) <= NS * STAGE + SCALES, "the output is staged in the ring");
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * STAGE + SCALES];
+    constexpr int RING = NS * STAGE + SCALES;
+    static_assert(BM * WN * (BN / WN * 2 + 16) <= RING, "the output is staged in the first ring");
+    static_assert((KS - 1) * BM * BN * 4 <= KS * RING, "and partial tiles in all");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds_all[KS * RING];
 
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 3;
+    const int wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = wave_all & 3, team = KS > 1 ? wave_all >> 2 : 0;
+    uint8_t* lds = lds_all + team * RING;
     const int wm = wave / WN, wn = wave % WN;
     const int C = a.C, Q = (C + 3) / 4;
 
@@ -251,10 +255,11 @@ __global__ void __launch_bounds__(256, BM * BN > 128 * 256 ? 1 : 2) mx_tile_kern
         // Row blocks are numbered in group order, ceil(rows / BM) to a group;
         // the grid is an upper bound.  Each thread counts those of a run of
         // groups, and the one whose run holds this tile's publishes it.
-        int* sch = reinterpret_cast<int*>(lds);
+        constexpr int NW = 4 * KS;
+        int* sch = reinterpret_cast<int*>(lds_all);
         const int tid = threadIdx.x;
-        const int per = (a.groups + 255) / 256;
-        const int g_lo = min(tid * per, a.groups), g_hi = min(g_lo + per, a.groups);
+        const int per = (a.groups + NW * 64 - 1) / (NW * 64);
+        const int g_lo = (int)min((int64_t)tid * per, (int64_t)a.groups), g_hi = min(g_lo + per, a.groups);
         auto rows_of = [&](int g, int& r0, int& r1) {
             r0 = min(max(a.offsets[g], 0), a.M);
             r1 = min(max(a.offsets[g + 1], r0), a.M);
@@ -272,31 +277,33 @@ __global__ void __launch_bounds__(256, BM * BN > 128 * 256 ? 1 : 2) mx_tile_kern
             const int y = __shfl_up(incl, o);
             if (lane >= o) incl += y;
         }
-        if (lane == 63) sch[wave] = incl;
+        if (lane == 63) sch[wave_all] = incl;
         __syncthreads();
         // (the XCDs share the tiles that there are, not the grid's bound)
-        const int t = tile_of(min(sch[0] + sch[1] + sch[2] + sch[3], tiles_m) * tiles_n);
+        int64_t sum = 0;
+        for (int w = 0; w < NW; ++w) sum += sch[w];
+        const int t = tile_of((int)min(sum, (int64_t)tiles_m) * tiles_n);
         if (t < 0) return;  // past the last row block: the whole workgroup leaves
         tn = t % tiles_n;
-        int at = t / tiles_n - (incl - mine);
-        for (int w = 0; w < wave; ++w) at -= sch[w];
+        int64_t at = t / tiles_n - (incl - mine);
+        for (int w = 0; w < wave_all; ++w) at -= sch[w];
         if (at >= 0 && at < mine)
             for (int g = g_lo; g < g_hi; ++g) {
                 int r0, r1;
                 rows_of(g, r0, r1);
                 const int n = (r1 - r0 + BM - 1) / BM;
                 if (at < n) {
-                    sch[4] = g;
-                    sch[5] = r0 + at * BM;
-                    sch[6] = r1;
+                    sch[NW] = g;
+                    sch[NW + 1] = r0 + (int)at * BM;
+                    sch[NW + 2] = r1;
                     break;
                 }
                 at -= n;
             }
         __syncthreads();
-        const int g = __builtin_amdgcn_readfirstlane(sch[4]);
-        m0 = __builtin_amdgcn_readfirstlane(sch[5]);
-        row_end = __builtin_amdgcn_readfirstlane(sch[6]);
+        const int g = __builtin_amdgcn_readfirstlane(sch[NW]);
+        m0 = __builtin_amdgcn_readfirstlane(sch[NW + 1]);
+        row_end = __builtin_amdgcn_readfirstlane(sch[NW + 2]);
         b_first = (int64_t)g * a.RBb + (int64_t)tn * BF;
         __syncthreads();  // everyone has read before the ring fills
     } else {
@@ -343,16 +350,21 @@ __global__ void __launch_bounds__(256, BM * BN > 128 * 256 ? 1 : 2) mx_tile_kern
             scale_at[i] = (r >> 4) * (uint32_t)Q * kMxScaleFrag + mx_scale_at(r & 15, lane & 3);
         }
     }
-    // Load number I of step c into buffer `stage`, and of scale word q.
+    // The team's steps, c0 .. c0 + steps - 1: whole scale words, shared evenly.
+    const int q0 = KS > 1 ? (int)((int64_t)Q * team / KS) : 0;
+    const int c0 = 4 * q0;
+    const int steps = KS > 1 ? min(4 * (int)((int64_t)Q * (team + 1) / KS), C) - c0 : C;
+    // Load number I of the team's step c into buffer `stage`, and of its scale
+    // word q.
     auto load_code = [&](auto I, int c, int stage) {
         constexpr int i = I.value;
-        mx_dma<16, i * kMxFrag>(wave * CPW + i < AF ? rac : rbc, code_at[i], (uint32_t)min(c, C - 1) * kMxFrag,
+        mx_dma<16, i * kMxFrag>(wave * CPW + i < AF ? rac : rbc, code_at[i], (uint32_t)min(c0 + c, C - 1) * kMxFrag,
                                 lds0 + (uint32_t)(stage * STAGE + wave * CPW * kMxFrag));
     };
     auto load_scale = [&](auto I, int q) {
         constexpr int i = I.value;
         mx_dma<4, NS * STAGE + i * kMxScaleFrag>(wave * CPW + i < AF ? ras : rbs, scale_at[i],
-                                                 (uint32_t)min(q, Q - 1) * kMxScaleFrag,
+                                                 (uint32_t)min(q0 + q, Q - 1) * kMxScaleFrag,
                                                  lds0 + (uint32_t)(wave * CPW * kMxScaleFrag));
     };
 
@@ -378,7 +390,8 @@ __global__ void __launch_bounds__(256, BM * BN > 128 * 256 ? 1 : 2) mx_tile_kern
     struct Scales { uint32_t a[MI][2], b[NI][2]; };
     constexpr int P = MI + NI;   // 32-row blocks of a wave: LDS reads of a half
     constexpr int MM = MI * NI;  // MFMAs of a half
-    static_assert(P <= MM, "a read behind each MFMA");
+    // the MFMA of a half behind which LDS read i is issued
+    constexpr auto slot_of = [](int i) { return P <= MM ? i : i * MM / P; };
     // LDS read number I of a half
     auto read = [&](auto I, Half& h, int stage, int half) {
         constexpr int i = I.value;
@@ -422,7 +435,7 @@ __global__ void __launch_bounds__(256, BM * BN > 128 * 256 ? 1 : 2) mx_tile_kern
         constexpr int s = S.value;
         mx_each<MM>([&](auto N) {
             mfma(N, S, h0, 0);
-            if constexpr (N.value < P) read(N, h1, stage, 1);
+            mx_each<P>([&](auto I) { if constexpr (slot_of(I.value) == N.value) read(I, h1, stage, 1); });
             __builtin_amdgcn_sched_barrier(0);
         });
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -436,8 +449,10 @@ __global__ void __launch_bounds__(256, BM * BN > 128 * 256 ? 1 : 2) mx_tile_kern
         mx_each<MM>([&](auto N) {
             constexpr int n = N.value;
             mfma(N, S, h1, 1);
-            if constexpr (n < P) read(N, h0, stage, 0);
-            if constexpr (s == 3 && n >= MM - P) read_scale(std::integral_constant<int, n - (MM - P)>{}, sn);
+            mx_each<P>([&](auto I) {
+                if constexpr (slot_of(I.value) == n) read(I, h0, stage, 0);
+                if constexpr (s == 3 && MM - 1 - slot_of(I.value) == n) read_scale(I, sn);
+            });
             mx_each<(n + 1) * CPW / MM - n * CPW / MM>([&](auto I) {
                 constexpr int i = n * CPW / MM + I.value;
                 load_code(std::integral_constant<int, i>{}, c + NS, freed);
@@ -450,14 +465,40 @@ __global__ void __launch_bounds__(256, BM * BN > 128 * 256 ? 1 : 2) mx_tile_kern
     };
     // whole scale words, then the steps that are left (one loop exit: the
     // accumulators stay where they are)
-    for (int q = C / 4; q > 0; --q) mx_each<4>(step);
-    if (C & 3) {
+    for (int q = steps / 4; q > 0; --q) mx_each<4>(step);
+    if (steps & 3) {
         step(std::integral_constant<int, 0>{});
-        if ((C & 3) > 1) step(std::integral_constant<int, 1>{});
-        if ((C & 3) > 2) step(std::integral_constant<int, 2>{});
+        if ((steps & 3) > 1) step(std::integral_constant<int, 1>{});
+        if ((steps & 3) > 2) step(std::integral_constant<int, 2>{});
     }
+    // a team with fewer steps than another meets it at the barriers that are left
+    if constexpr (KS > 1)
+        for (int k = 4 * ((Q + KS - 1) / KS) - steps; k > 0; --k) wg_barrier();
     wait_vmcnt<0>();  // the ring's last loads, before its memory is used again
     __syncthreads();
+
+    // The teams' sums, added in their order: each but the first leaves its own
+    // in LDS.
+    if constexpr (KS > 1) {
+        mx_f4* part = reinterpret_cast<mx_f4*>(lds_all) + wave * (MM * 256) + lane;
+        if (team > 0)
+            mx_each<MM * 4>([&](auto K) {
+                constexpr int k = K.value, m = k / 4, v = k % 4 * 4;
+                const mx_f16& x = acc[m / NI][m % NI];
+                part[(team - 1) * (4 * MM * 256) + k * 64] = mx_f4{x[v], x[v + 1], x[v + 2], x[v + 3]};
+            });
+        __syncthreads();
+        if (team == 0)
+            mx_each<MM * 4>([&](auto K) {
+                constexpr int k = K.value, m = k / 4, v = k % 4 * 4;
+                mx_f16& x = acc[m / NI][m % NI];
+                for (int t = 0; t < KS - 1; ++t) {
+                    const mx_f4 y = part[t * (4 * MM * 256) + k * 64];
+                    x[v] += y[0]; x[v + 1] += y[1]; x[v + 2] += y[2]; x[v + 3] += y[3];
+                }
+            });
+        __syncthreads();
+    }
 
     // Epilogue.  Block (i, j) of lane l: row 32 i + l % 32, columns 32 j +
     // 8 (v / 4) + 4 (l / 32) + v % 4.
@@ -466,19 +507,22 @@ __global__ void __launch_bounds__(256, BM * BN > 128 * 256 ? 1 : 2) mx_tile_kern
     if (a.out_bf16 && (a.N & 7) == 0) {
         // through LDS, a wave's part each, so that whole lines are stored
         constexpr int ROW = PN * 2 + 16;  // bytes, 16 of them padding
-        uint8_t* part = lds + wave * PM * ROW;
+        uint8_t* part = lds_all + wave * PM * ROW;
+        if (KS == 1 || team == 0) {
 #pragma unroll
-        for (int i = 0; i < MI; ++i)
+            for (int i = 0; i < MI; ++i)
 #pragma unroll
-            for (int j = 0; j < NI; ++j)
+                for (int j = 0; j < NI; ++j)
 #pragma unroll
-                for (int v = 0; v < 16; v += 4) {
-                    uint32_t o[2];
-                    o[0] = mx_to_bf16(a.alpha * acc[i][j][v]) | (uint32_t)mx_to_bf16(a.alpha * acc[i][j][v + 1]) << 16;
-                    o[1] = mx_to_bf16(a.alpha * acc[i][j][v + 2]) | (uint32_t)mx_to_bf16(a.alpha * acc[i][j][v + 3]) << 16;
-                    __builtin_memcpy(__builtin_assume_aligned(part + (i * 32 + q32) * ROW + (j * 32 + 2 * v + 4 * kgl) * 2, 8), o, 8);
-                }
+                    for (int v = 0; v < 16; v += 4) {
+                        uint32_t o[2];
+                        o[0] = mx_to_bf16(a.alpha * acc[i][j][v]) | (uint32_t)mx_to_bf16(a.alpha * acc[i][j][v + 1]) << 16;
+                        o[1] = mx_to_bf16(a.alpha * acc[i][j][v + 2]) | (uint32_t)mx_to_bf16(a.alpha * acc[i][j][v + 3]) << 16;
+                        __builtin_memcpy(__builtin_assume_aligned(part + (i * 32 + q32) * ROW + (j * 32 + 2 * v + 4 * kgl) * 2, 8), o, 8);
+                    }
+        }
         __syncthreads();
+        if (KS > 1 && team > 0) return;
         constexpr int LPR = PN / 8;        // lanes that store a row's part
         constexpr int RPS = 64 / LPR;      // rows a store covers
         const int r = lane / LPR, col = col0 + (lane % LPR) * 8;
@@ -490,7 +534,7 @@ __global__ void __launch_bounds__(256, BM * BN > 128 * 256 ? 1 : 2) mx_tile_kern
             if (row < row_end && col < a.N)
                 *reinterpret_cast<mx_u4*>(static_cast<uint16_t*>(a.out) + (int64_t)row * a.N + col) = o;
         }
-    } else {
+    } else if (KS == 1 || team == 0) {
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
             const int row = row0 + i * 32 + q32;
@@ -530,14 +574,14 @@ void run_split(Launch& l) {
     l.error = hipGetLastError();
 }
 
-template <int BM, int BN, int NS, int WM, bool GROUPED>
+template <int BM, int BN, int NS, int WM, int KS, bool GROUPED>
 void run_tile(Launch& l) {
     const MxGemmArgs& a = l.a;
     // (grouped: each group adds at most one broken row block)
     const int64_t tiles_m = ((int64_t)a.M + BM - 1) / BM + (GROUPED ? a.groups : 0), tiles_n = ((int64_t)a.N + BN - 1) / BN;
-    l.items = tiles_m * tiles_n * 256;
+    l.items = tiles_m * tiles_n * KS * 256;
     if (l.dry) return;
-    hipLaunchKernelGGL((mx_tile_kernel<BM, BN, NS, WM, GROUPED>), dim3((unsigned)(tiles_m * tiles_n)), dim3(256), 0,
+    hipLaunchKernelGGL((mx_tile_kernel<BM, BN, NS, WM, KS, GROUPED>), dim3((unsigned)(tiles_m * tiles_n)), dim3(KS * 256), 0,
                        l.stream, a, (int)tiles_m, (int)tiles_n);
     l.error = hipGetLastError();
 }
@@ -552,29 +596,33 @@ void run_few_rows(Launch& l) {
 void choose(Launch& l) {
     const MxGemmArgs& a = l.a;
     if (a.groups > 0) {
-        static const int dv = getenv("MXV") ? atoi(getenv("MXV")) : 0;
-        if (dv != 2 && dv != 7 && dv != 8 && a.M / a.groups <= 32) return run_split<2, 4, 4, A_PACKED, true>(l);
-        if (a.C <= kMxTileSteps && a.M < (1 << 28) && (int64_t)a.RBa * a.C * kMxFrag < ((int64_t)1 << 31)) {
-            static const int v = getenv("MXV") ? atoi(getenv("MXV")) : 0;
-            if (v == 1) return run_tile<128, 256, 3, 2, true>(l);
-            if (v == 2) return run_tile<64, 256, 3, 1, true>(l);
-            if (v == 3) return run_tile<256, 256, 4, 2, true>(l);
-            if (v == 4) return run_tile<128, 256, 4, 2, true>(l);
-            if (v == 5) return run_tile<64, 256, 4, 1, true>(l);
-            if (v == 7) return run_tile<64, 256, 2, 1, true>(l);
-            if (v == 8) return run_tile<128, 128, 3, 2, true>(l);
-            return run_tile<128, 128, 4, 2, true>(l);
-        }
-        return run_split<4, 4, 8, A_PACKED, true>(l);
+        const char* e = getenv("MXV"); const int v = e ? atoi(e) : 0;
+        if (v == 10) return run_split<2, 4, 4, A_PACKED, true>(l);
+        if (v == 11) return run_split<4, 4, 8, A_PACKED, true>(l);
+        if (v == 12) return run_split<1, 4, 8, A_PACKED, true>(l);
+        if (v == 13) return run_split<2, 2, 8, A_PACKED, true>(l);
+        if (v == 14) return run_split<2, 4, 8, A_PACKED, true>(l);
+        if (v == 1) return run_tile<128, 256, 3, 2, 1, true>(l);
+        if (v == 2) return run_tile<64, 256, 3, 1, 1, true>(l);
+        if (v == 20) return run_tile<64, 64, 4, 2, 4, true>(l);
+        if (v == 21) return run_tile<64, 64, 4, 2, 2, true>(l);
+        if (v == 22) return run_tile<64, 128, 4, 2, 2, true>(l);
+        if (v == 3) return run_tile<256, 256, 4, 2, 1, true>(l);
+        if (v == 8) return run_tile<128, 128, 3, 2, 1, true>(l);
+        return run_tile<128, 128, 4, 2, 1, true>(l);
     }
     if (!a.a_codes) return a.x_bf16 ? run_few_rows<A_BF16>(l) : run_few_rows<A_F32>(l);
     if (a.M <= 64) return run_few_rows<A_PACKED>(l);
-    if (a.C <= kMxTileSteps) {
-        const int64_t t256 = ((a.M + 255) / 256) * (int64_t)((a.N + 255) / 256);
-        if (t256 >= 192) return run_tile<256, 256, 4, 2, false>(l);
-        const int64_t t128 = ((a.M + 127) / 128) * (int64_t)((a.N + 127) / 128);
-        if (t128 >= 100) return run_tile<128, 128, 4, 2, false>(l);
-    }
+    const char* e = getenv("MXV"); const int v = e ? atoi(e) : 0;
+    if (v == 1) return run_tile<128, 256, 3, 2, 1, false>(l);
+    if (v == 2) return run_tile<64, 256, 3, 1, 1, false>(l);
+    if (v == 3) return run_tile<256, 256, 4, 2, 1, false>(l);
+    if (v == 4) return run_tile<128, 128, 4, 2, 1, false>(l);
+    if (v == 5) return run_tile<128, 128, 4, 2, 2, false>(l);
+    if (v == 20) return run_tile<64, 64, 4, 2, 4, false>(l);
+    if (v == 21) return run_tile<64, 64, 4, 2, 2, false>(l);
+    if (v == 22) return run_tile<64, 128, 4, 2, 2, false>(l);
+    if (v == 24) return run_tile<64, 128, 3, 2, 4, false>(l);
     return run_split<4, 4, 8, A_PACKED, false>(l);
 }
 
