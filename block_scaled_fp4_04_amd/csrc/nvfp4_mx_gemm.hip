@@ -10,6 +10,7 @@
 #include "nvfp4_device.h"
 #include "nvfp4_mx_device.h"
 
+#include <algorithm>
 #include <type_traits>
 #include <utility>
 
@@ -67,133 +68,143 @@ __device__ __forceinline__ void mx_store4(const MxGemmArgs& a, int row, int col,
 }
 
 // ---------------------------------------------------------------------------
-// Split kernel: the waves of a workgroup share one output tile of 16 MI x
-// 16 NI and split its K range, four steps (one scale word) at a time.  Each
-// wave loads its operands straight into registers; the wave tiles are added
+// Skinny kernel, for few rows of A: a workgroup takes 16 columns of C (one row
+// block of B) and its 16 waves split K a scale word (four steps) at a time.
+// Each wave copies its 4 KB of B straight to a part of LDS of its own and
+// reads its operands from there (in the packed layout a wave's rows are 64
+// bytes apart: loaded straight to registers they cost the address unit twice
+// the time, 3.7 against 3.2 us at 1 x 768 x 6144); the waves' sums are added
 // in LDS in wave order, so results do not depend on timing.
 //
-// A operand of v_mfma_scale_f32_16x16x128: B's rows; B operand: A's rows; so
-// lane l ends up with row l % 16 of A and four consecutive columns of C.
+// First operand of v_mfma_scale_f32_16x16x128_f8f6f4: B's rows; second: A's
+// rows; so lane l ends up with row l % 16 of A and four consecutive columns.
 //
-// GROUPED: group g owns rows offsets[g] .. offsets[g+1]-1 of C; a workgroup
-// takes one column tile of one group and walks its rows.  Offsets are
-// clamped to [0, M] and row numbers to A's rows, so a malformed table gives
-// wrong rows but no access outside the buffers.
+// A_F32, A_BF16: the wave quantises its piece of the activations itself, four
+// rows of sixteen blocks at a time, a block to a lane, and hands the codes
+// to the lanes that multiply them through LDS.  (With a lane quantising the
+// four blocks that it multiplies, one row cost as much as sixteen: 5.0 us
+// at 1 x 768 x 6144, where packed operands take 3.7.)
+//
+// GROUPED (operands past the tile kernel's 32-bit offsets): group g owns rows
+// offsets[g] .. offsets[g+1]-1 of C; a workgroup takes one row block of one
+// group's B and walks the group's rows.  Offsets are clamped to [0, M] and row
+// numbers to A's rows, so a malformed table gives wrong rows but no access
+// outside the buffers.
 // ---------------------------------------------------------------------------
 enum { A_PACKED = 0, A_F32 = 1, A_BF16 = 2 };
 
-template <int MI, int NI, int W, int AT, bool GROUPED>
-__global__ void __launch_bounds__(W * 64) mx_split_kernel(MxGemmArgs a) {
-    __shared__ mx_f4 red[W][MI * NI][64];
+// Orders a wave's LDS accesses among its lanes.
+__device__ __forceinline__ void mx_wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+template <int MI, int AT, bool GROUPED>
+__global__ void __launch_bounds__(1024) mx_skinny_kernel(MxGemmArgs a) {
+    constexpr int W = 16;
+    static_assert(AT == A_PACKED || MI == 1, "quantised rows: one row block");
+    __shared__ __attribute__((aligned(1024))) uint8_t b_lds[W][4 * kMxFrag];
+    __shared__ __attribute__((aligned(1024))) uint8_t a_lds[AT == A_PACKED ? 1 : W][4 * kMxFrag + kMxScaleFrag];
+    __shared__ mx_f4 red[W][MI][64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r16 = lane & 15, kg = lane >> 4;
     const int C = a.C, Q = (C + 3) / 4;
-    const int tiles_n = (a.RBb + NI - 1) / NI;
-    const int tn = (int)(blockIdx.x % (unsigned)tiles_n);
-    const int tm = (int)(blockIdx.x / (unsigned)tiles_n);  // row tile, or group
-    const int cb0 = tn * NI;
+    const int cb = (int)(blockIdx.x % (unsigned)a.RBb);  // row block of B
+    const int tm = (int)(blockIdx.x / (unsigned)a.RBb);  // row tile, or group
     int r0 = tm * 16 * MI, r1 = min(r0 + 16 * MI, a.M);
-    const uint8_t* bc = a.b_codes;
-    const uint8_t* bs = a.b_scales;
+    int64_t brow = cb;
     if constexpr (GROUPED) {
         r0 = min(max(a.offsets[tm], 0), a.M);
         r1 = min(max(a.offsets[tm + 1], r0), a.M);
-        bc += (int64_t)tm * a.RBb * C * kMxFrag;
-        bs += (int64_t)tm * a.RBb * Q * kMxScaleFrag;
+        brow += (int64_t)tm * a.RBb;
     }
-    // this lane's pieces of the column tile's row blocks (past B's end: its last)
-    const uint8_t* bcp[NI];
-    const uint8_t* bsp[NI];
-#pragma unroll
-    for (int j = 0; j < NI; ++j) {
-        const int64_t rb = min(cb0 + j, a.RBb - 1);
-        bcp[j] = bc + rb * C * kMxFrag + mx_code_at(r16, kg);
-        bsp[j] = bs + rb * Q * kMxScaleFrag + mx_scale_at(r16, kg);
-    }
+    const uint8_t* bc = a.b_codes + brow * C * kMxFrag;
+    const uint8_t* bs = a.b_scales + brow * Q * kMxScaleFrag;
+    const int at_code = mx_code_at(r16, kg), at_scale = mx_scale_at(r16, kg);
+    const uint32_t b_base = lds_addr(b_lds[wave]);
 
     for (int m0 = r0; m0 < r1; m0 += 16 * MI) {
-        int64_t arow[MI];
+        const uint8_t *ac[MI], *as[MI];  // this lane's block of its row, at step 0
+        bool live[MI];
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
-            int r = min(m0 + i * 16 + r16, r1 - 1);
-            if (GROUPED && a.a_rows) r = min(max(a.a_rows[r], 0), a.A_rows - 1);
-            arow[i] = r;
+            int r = m0 + i * 16 + r16;
+            live[i] = r < r1;
+            if (GROUPED && a.a_rows && live[i]) r = min(max(a.a_rows[r], 0), a.A_rows - 1);
+            ac[i] = a.a_codes + (int64_t)(r >> 4) * C * kMxFrag + mx_code_at(r & 15, kg);
+            as[i] = a.a_scales + (int64_t)(r >> 4) * Q * kMxScaleFrag + mx_scale_at(r & 15, kg);
         }
-        mx_f4 acc[MI][NI];
+        mx_f4 acc[MI];
 #pragma unroll
-        for (int i = 0; i < MI; ++i)
-#pragma unroll
-            for (int j = 0; j < NI; ++j) acc[i][j] = mx_f4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = 0; i < MI; ++i) acc[i] = mx_f4{0.0f, 0.0f, 0.0f, 0.0f};
 
         for (int q = wave; q < Q; q += W) {
-            uint32_t sb[NI], sa[MI];
-            mx_u4 wb[4][NI], wa[4][MI];
+            const int n = min(4, C - 4 * q);  // steps of this word
+            const __amdgpu_buffer_rsrc_t rb = make_rsrc(bc + (int64_t)q * 4 * kMxFrag, (uint32_t)n * kMxFrag);
+            mx_each<4>([&](auto S) {
+                if (S.value < n) mx_dma<16, S.value * kMxFrag>(rb, lane * 16, S.value * kMxFrag, b_base);
+            });
+            const uint32_t sb = *reinterpret_cast<const uint32_t*>(bs + (int64_t)q * kMxScaleFrag + at_scale);
+            mx_u4 wa[4][MI];
+            uint32_t sa[MI];
+            if constexpr (AT == A_PACKED) {
 #pragma unroll
-            for (int j = 0; j < NI; ++j) sb[j] = *reinterpret_cast<const uint32_t*>(bsp[j] + (int64_t)q * kMxScaleFrag);
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const int64_t c = min(4 * q + s, C - 1);
-#pragma unroll
-                for (int j = 0; j < NI; ++j) wb[s][j] = *reinterpret_cast<const mx_u4*>(bcp[j] + c * kMxFrag);
-            }
-#pragma unroll
-            for (int i = 0; i < MI; ++i) {
-                if constexpr (AT == A_PACKED) {
-                    const int64_t rb = arow[i] >> 4;
-                    const int rr = (int)(arow[i] & 15);
-                    sa[i] = *reinterpret_cast<const uint32_t*>(a.a_scales + (rb * Q + q) * kMxScaleFrag + mx_scale_at(rr, kg));
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        const int64_t c = min(4 * q + s, C - 1);
-                        wa[s][i] = *reinterpret_cast<const mx_u4*>(a.a_codes + (rb * C + c) * kMxFrag + mx_code_at(rr, kg));
-                    }
-                } else {
+                for (int i = 0; i < MI; ++i) {
                     sa[i] = 0;
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        const int k = (4 * q + s) * kMxStep + kg * kMxBlock;
-                        const bool live = k < a.K;
-                        uint32_t byte;
-                        const int64_t at = arow[i] * a.ldx + (live ? k : 0);
-                        if constexpr (AT == A_F32)
-                            byte = mx_quant_load(static_cast<const float*>(a.x) + at, wa[s][i]);
-                        else
-                            byte = mx_quant_load(static_cast<const uint16_t*>(a.x) + at, wa[s][i]);
-                        if (!live) wa[s][i] = mx_u4{0, 0, 0, 0};
-                        sa[i] |= (live ? byte : 0u) << (8 * s);
+                    for (int s = 0; s < 4; ++s) wa[s][i] = mx_u4{0, 0, 0, 0};
+                    if (live[i]) {
+                        sa[i] = *reinterpret_cast<const uint32_t*>(as[i] + (int64_t)q * kMxScaleFrag);
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+                            wa[s][i] = *reinterpret_cast<const mx_u4*>(ac[i] + (int64_t)min(4 * q + s, C - 1) * kMxFrag);
                     }
                 }
-            }
-            const int n = min(4, C - 4 * q);  // steps of this word (uniform)
-            auto step = [&](auto S) {
-                if (S.value < n) {
-#pragma unroll
-                    for (int i = 0; i < MI; ++i)
-#pragma unroll
-                        for (int j = 0; j < NI; ++j)
-                            acc[i][j] = mx_mfma16<S.value>(wb[S.value][j], sb[j], wa[S.value][i], sa[i], acc[i][j]);
+            } else {
+                using T = std::conditional_t<AT == A_F32, float, uint16_t>;
+                const int s = (lane & 15) >> 2, b = lane & 3;  // the lane's block
+                const int k = (4 * q + s) * kMxStep + b * kMxBlock;
+                for (int p = 0; p < r1 - m0; p += 4) {
+                    const int row = p + (lane >> 4);
+                    if (m0 + row < r1) {
+                        mx_u4 w = {0, 0, 0, 0};
+                        uint32_t byte = 0;
+                        if (k < a.K) byte = mx_quant_load(static_cast<const T*>(a.x) + (int64_t)(m0 + row) * a.ldx + k, w);
+                        uint8_t* d = a_lds[wave];
+                        *reinterpret_cast<mx_u4*>(d + s * kMxFrag + mx_code_at(row, b)) = w;
+                        d[4 * kMxFrag + mx_scale_at(row, b) + s] = (uint8_t)byte;
+                    }
                 }
-            };
-            step(std::integral_constant<int, 0>{});
-            step(std::integral_constant<int, 1>{});
-            step(std::integral_constant<int, 2>{});
-            step(std::integral_constant<int, 3>{});
+                mx_wave_fence();
+                // (rows past the last one: whatever LDS holds, not stored)
+                sa[0] = *reinterpret_cast<const uint32_t*>(a_lds[wave] + 4 * kMxFrag + at_scale);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) wa[t][0] = *reinterpret_cast<const mx_u4*>(a_lds[wave] + t * kMxFrag + at_code);
+            }
+            wait_vmcnt<0>();
+            asm volatile("" ::: "memory");  // B has landed
+            mx_each<4>([&](auto S) {
+                if (S.value < n) {
+                    const mx_u4 wb = *reinterpret_cast<const mx_u4*>(b_lds[wave] + S.value * kMxFrag + at_code);
+#pragma unroll
+                    for (int i = 0; i < MI; ++i) acc[i] = mx_mfma16<S.value>(wb, sb, wa[S.value][i], sa[i], acc[i]);
+                }
+            });
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // LDS is read before it is filled again
+            mx_wave_fence();
         }
 
         if (m0 != r0) __syncthreads();  // the previous rows' sums are read
 #pragma unroll
-        for (int i = 0; i < MI; ++i)
-#pragma unroll
-            for (int j = 0; j < NI; ++j) red[wave][i * NI + j][lane] = acc[i][j];
+        for (int i = 0; i < MI; ++i) red[wave][i][lane] = acc[i];
         __syncthreads();
-        for (int f = wave; f < MI * NI; f += W) {
+        for (int f = wave; f < MI; f += W) {
             mx_f4 sum = red[0][f][lane];
 #pragma unroll
             for (int w = 1; w < W; ++w) sum += red[w][f][lane];
-            const int row = m0 + (f / NI) * 16 + r16;
-            const int col = (cb0 + f % NI) * 16 + 4 * kg;
-            if (row < r1) mx_store4(a, row, col, sum);
+            const int row = m0 + f * 16 + r16;
+            if (row < r1) mx_store4(a, row, cb * 16 + 4 * kg, sum);
         }
     }
 }
@@ -562,15 +573,13 @@ struct Launch {
     hipError_t error;
 };
 
-template <int MI, int NI, int W, int AT, bool GROUPED>
-void run_split(Launch& l) {
+template <int MI, int AT, bool GROUPED>
+void run_skinny(Launch& l) {
     const MxGemmArgs& a = l.a;
-    const int64_t tiles_n = (a.RBb + NI - 1) / NI;
-    const int64_t tiles_m = GROUPED ? a.groups : (a.M + 16 * MI - 1) / (16 * MI);
-    l.items = tiles_m * tiles_n * W * 64;
+    const int64_t tiles = (GROUPED ? a.groups : (a.M + 16 * MI - 1) / (16 * MI)) * (int64_t)a.RBb;
+    l.items = tiles * 1024;
     if (l.dry) return;
-    hipLaunchKernelGGL((mx_split_kernel<MI, NI, W, AT, GROUPED>), dim3((unsigned)(tiles_m * tiles_n)),
-                       dim3(W * 64), 0, l.stream, a);
+    hipLaunchKernelGGL((mx_skinny_kernel<MI, AT, GROUPED>), dim3((unsigned)tiles), dim3(1024), 0, l.stream, a);
     l.error = hipGetLastError();
 }
 
@@ -586,44 +595,63 @@ void run_tile(Launch& l) {
     l.error = hipGetLastError();
 }
 
-template <int AT>
-void run_few_rows(Launch& l) {
-    if (l.a.M <= 16) return run_split<1, 1, 16, AT, false>(l);
-    if (l.a.M <= 32) return run_split<2, 1, 16, AT, false>(l);
-    return run_split<4, 1, 16, AT, false>(l);
+// The kernel by sizes.  Times are of K = 6144 unless they say otherwise, with
+// operands beyond the L2; "short" ranges of K run on one team of waves, long
+// ones on two.
+constexpr int kMxShort = 24;  // steps
+
+template <bool GROUPED>
+void run_small_tiles(Launch& l) {
+    // 512 x 512 x 512: 3.6 us on one team, 4.3 on two; 300 x 1000 x 1024: 4.1
+    // and 4.5; 96 x 256 x 2048: 4.7 and 4.9; 256 x 4096 x 4096: 8.1 and 7.8; 512
+    // x 2048 x 6144: 10.4 and 9.4; 1000 x 300 x 8192: 11.9 and 10.0.
+    if (l.a.C <= kMxShort) return run_tile<64, 64, 4, 2, 1, GROUPED>(l);
+    return run_tile<64, 64, 4, 2, 2, GROUPED>(l);
 }
 
 void choose(Launch& l) {
     const MxGemmArgs& a = l.a;
-    if (a.groups > 0) {
-        const char* e = getenv("MXV"); const int v = e ? atoi(e) : 0;
-        if (v == 10) return run_split<2, 4, 4, A_PACKED, true>(l);
-        if (v == 11) return run_split<4, 4, 8, A_PACKED, true>(l);
-        if (v == 12) return run_split<1, 4, 8, A_PACKED, true>(l);
-        if (v == 13) return run_split<2, 2, 8, A_PACKED, true>(l);
-        if (v == 14) return run_split<2, 4, 8, A_PACKED, true>(l);
-        if (v == 1) return run_tile<128, 256, 3, 2, 1, true>(l);
-        if (v == 2) return run_tile<64, 256, 3, 1, 1, true>(l);
-        if (v == 20) return run_tile<64, 64, 4, 2, 4, true>(l);
-        if (v == 21) return run_tile<64, 64, 4, 2, 2, true>(l);
-        if (v == 22) return run_tile<64, 128, 4, 2, 2, true>(l);
-        if (v == 3) return run_tile<256, 256, 4, 2, 1, true>(l);
-        if (v == 8) return run_tile<128, 128, 3, 2, 1, true>(l);
-        return run_tile<128, 128, 4, 2, 1, true>(l);
+    const int64_t M = a.M, N = a.N, G = a.groups;
+    // (a bound on the) tiles of rows x cols
+    auto tiles = [&](int64_t rows, int64_t cols) {
+        return ((M + rows - 1) / rows + std::min(G, M)) * ((N + cols - 1) / cols);
+    };
+    if (G > 0) {
+        // the tile kernel addresses A with 32-bit offsets and numbers row blocks in 32 bits
+        if (a.C > kMxTileSteps || M >= 1 << 28 || (int64_t)a.RBa * a.C * kMxFrag >= (int64_t)1 << 31)
+            return run_skinny<2, A_PACKED, true>(l);
+        // Few tiles, so that one tile's time counts (8 experts x 2048 columns,
+        // 16 rows each: 13.4 us, 18.1 with 64 x 256 tiles); about even at 64
+        // experts x 512 x K 2048 with 16 rows (640 tiles).
+        if (tiles(64, 64) <= 640) return run_small_tiles<true>(l);
+        // From 128 rows each, larger tiles read the weights less often (256
+        // experts x 256 columns, 128 rows: 75 against 77 us; 16 x 2048 x K 2048,
+        // 1024 rows: 56 against 64), if they are enough to fill the GPU or the
+        // weights come from memory (8 x 2048, 256 rows: 27 against 33; but 4 x
+        // 768, 1024 rows: 25 against 20).
+        const int64_t weights = G * a.RBb * a.C * kMxFrag;
+        if (M >= 128 * G && (tiles(128, 256) >= 256 || weights >= 32 << 20))
+            return run_tile<128, 256, 3, 2, 1, true>(l);
+        // 64 x 256 tiles stream the weights of small groups at the memory's
+        // rate (256 experts x 256 columns, 16 rows: 44 us, 49 with 128 x 128);
+        // narrow weights would leave them half empty.
+        if (N <= 128) return run_tile<128, 128, 4, 2, 1, true>(l);
+        return run_tile<64, 256, 3, 1, 1, true>(l);
     }
-    if (!a.a_codes) return a.x_bf16 ? run_few_rows<A_BF16>(l) : run_few_rows<A_F32>(l);
-    if (a.M <= 64) return run_few_rows<A_PACKED>(l);
-    const char* e = getenv("MXV"); const int v = e ? atoi(e) : 0;
-    if (v == 1) return run_tile<128, 256, 3, 2, 1, false>(l);
-    if (v == 2) return run_tile<64, 256, 3, 1, 1, false>(l);
-    if (v == 3) return run_tile<256, 256, 4, 2, 1, false>(l);
-    if (v == 4) return run_tile<128, 128, 4, 2, 1, false>(l);
-    if (v == 5) return run_tile<128, 128, 4, 2, 2, false>(l);
-    if (v == 20) return run_tile<64, 64, 4, 2, 4, false>(l);
-    if (v == 21) return run_tile<64, 64, 4, 2, 2, false>(l);
-    if (v == 22) return run_tile<64, 128, 4, 2, 2, false>(l);
-    if (v == 24) return run_tile<64, 128, 3, 2, 4, false>(l);
-    return run_split<4, 4, 8, A_PACKED, false>(l);
+    if (!a.a_codes) return a.x_bf16 ? run_skinny<1, A_BF16, false>(l) : run_skinny<1, A_F32, false>(l);
+    // Up to 16 rows always the kernel that quantises too: the same bits (1 x
+    // 768: 3.5 us, 7.3 with 64 x 64 tiles; 16 x 6144: 7.1 and 8.4).
+    if (M <= kMxQuantRows) return run_skinny<1, A_PACKED, false>(l);
+    // Up to 64 rows while its workgroups fit the GPU at once (64 x 768: 5.3
+    // against 7.4 us; 64 x 6144: 14.0 against 8.8).
+    if ((M <= 64 && (M + 31) / 32 * a.RBb <= 256) || a.C > kMxTileSteps) return run_skinny<2, A_PACKED, false>(l);
+    // 2048 x 6144 (192 tiles of 256 x 256): 43 us with these, 43 with 128 x 128;
+    // 8192 x 2048 (256): 51 and 55; 1024 x 6144 (96): 37 and 26.
+    if (tiles(256, 256) >= 192) return run_tile<256, 256, 4, 2, 1, false>(l);
+    // 1237 x 2056 (170 tiles of 128 x 128): 15.2 us with these, 18.0 with 64 x
+    // 64; 256 x 4096 x 4096 (64): 10.7 and 7.8; 200 x 8192 x 512 (128): 5.3 and 4.6.
+    if (tiles(128, 128) >= 150) return run_tile<128, 128, 4, 2, 1, false>(l);
+    run_small_tiles<false>(l);
 }
 
 }  // namespace

@@ -58,7 +58,7 @@ struct MxGemmArgs {
     bool x_bf16, out_bf16;
 };
 // Rows of A up to which the one-launch product from activations runs.
-constexpr int kMxQuantRows = 64;
+constexpr int kMxQuantRows = 16;
 hipError_t launch_mx_gemm(const MxGemmArgs& a, hipStream_t stream);
 // Whether the grid of the kernel that the sizes choose stays within the
 // runtime's limit on work-items.

@@ -22,7 +22,7 @@ from . import Nvfp4Error, _i64, _u8p, _vp, lib
 TYPE_F32 = 0    # element types of rows (nvfp4_mx.h)
 TYPE_BF16 = 1
 MX_BLOCK = 32   # elements that share a scale
-MX_QUANT_ROWS = 64  # most rows of mx_gemm_quantized
+MX_QUANT_ROWS = 16  # most rows of mx_gemm_quantized
 
 MX_EXPORTS = ["nvfp4_mx_packed_size", "nvfp4_mx_pack", "nvfp4_mx_unpack", "nvfp4_mx_quantize",
               "nvfp4_mx_dequantize", "nvfp4_mx_gemm", "nvfp4_mx_gemm_quantized",
@@ -347,19 +347,14 @@ def mx_gemm_quantized(x, b: MxOperand, alpha: float = 1.0, out=None, dtype=None,
 
 def mx_linear(x, b: MxOperand, alpha: float = 1.0, out=None, dtype=None, stream=None):
     """C = alpha * (quantise(x) . B^T) for plain activations x (rows x K,
-    fp32 or bfloat16): one launch where mx_gemm_quantized is the faster form
-    (few rows), else mx_quantize and mx_gemm.  Both give the same bits."""
+    fp32 or bfloat16): one launch (mx_gemm_quantized) for up to MX_QUANT_ROWS
+    rows, else mx_quantize and mx_gemm.  Both give the same bits."""
     if stream is not None:
         with _on(stream):
             return mx_linear(x, b, alpha, out, dtype)
-    if x.dim() == 2 and x.shape[0] <= _one_launch_rows(x, b):
+    if x.dim() == 2 and x.shape[0] <= MX_QUANT_ROWS:
         return mx_gemm_quantized(x, b, alpha, out, dtype)
     return mx_gemm(mx_quantize(x), b, alpha, out, dtype)
-
-
-def _one_launch_rows(x, b) -> int:
-    """Rows up to which the one-launch form is the faster one."""
-    return 16
 
 
 def _grouped_args(a, b, row_offsets, alpha, rows, out, dtype):

@@ -107,7 +107,7 @@ int nvfp4_mx_gemm(const void* a_packed, const void* a_scales, const void* b_pack
 /* nvfp4_mx_gemm(nvfp4_mx_quantize(X), B) in one launch, bit for bit, for
  * decode steps, where a second launch costs as much as the product.
  *   x : DEVICE, M x K values of x_type, row stride ldx elements (as
- *       nvfp4_mx_quantize); M is 1..64 (NVFP4_ERR_UNSUPPORTED above) */
+ *       nvfp4_mx_quantize); M is at most 16 (NVFP4_ERR_UNSUPPORTED above) */
 int nvfp4_mx_gemm_quantized(const void* x, int x_type, int64_t ldx, const void* b_packed,
                             const void* b_scales, float alpha, void* out, int out_type,
                             int64_t M, int64_t N, int64_t K, void* stream);

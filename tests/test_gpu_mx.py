@@ -131,7 +131,8 @@ def test_dequantize_strided_and_empty():
 
 # ---- product -----------------------------------------------------------------
 
-SHAPES = [(1, 1, 32), (1, 768, 6144), (2, 17, 128), (16, 256, 6144), (17, 33, 544), (40, 100, 2080),
+# (every kernel and both of its ends: few rows, one and two teams of waves, 128 and 256 tiles)
+SHAPES = [(1, 1, 32), (1, 768, 6144), (2, 17, 128), (16, 256, 6144), (17, 33, 544), (40, 100, 2080), (33, 4500, 160),
           (64, 64, 512), (65, 64, 128), (100, 130, 6112), (130, 200, 640), (257, 260, 1024),
           (300, 1000, 384), (512, 768, 512),
           (1300, 1290, 672), (1285, 1283, 2080), (4010, 3304, 544), (3900, 3301, 128)]
@@ -184,8 +185,8 @@ def test_gemm_nan_blocks_and_extreme_scales():
 
 
 @pytest.mark.parametrize("dtype", list(DT))
-@pytest.mark.parametrize("M,N,K", [(1, 768, 6144), (3, 50, 160), (16, 256, 2080), (17, 64, 32), (33, 40, 6112),
-                                   (64, 128, 1056)])
+@pytest.mark.parametrize("M,N,K", [(1, 768, 6144), (3, 50, 160), (16, 256, 2080), (4, 64, 32), (5, 40, 6112),
+                                   (13, 128, 8704)])
 def test_gemm_quantized_is_the_two_calls(M, N, K, dtype):
     say(f"gemm_quantized {M}x{N}x{K} {dtype}")
     g = rng(5, M, N, K)
@@ -220,7 +221,8 @@ def test_nan_row_of_activations():
     x[7, 100] = float("nan")
     x[9, 3] = float("inf")
     B = nv.mx_quantize(torch.ones(48, 256, device=DEV))
-    for c in (nv.mx_linear(x, B), nv.mx_gemm_quantized(x, B), nv.mx_gemm(nv.mx_quantize(x), B)):
+    for c in (nv.mx_linear(x, B), torch.cat([nv.mx_gemm_quantized(x[:10], B), nv.mx_gemm_quantized(x[10:], B)]),
+              nv.mx_gemm(nv.mx_quantize(x), B)):
         nan = torch.isnan(c).all(dim=1).cpu()
         assert nan.nonzero().flatten().tolist() == [7, 9]
         assert (c[~nan.to(DEV)] == 256).all()
@@ -247,6 +249,9 @@ def grouped_reference(va, vb, offsets, rows, alpha, out_eps):
     ([5, 27, 2], 73, 4128, 3),                  # odd columns
     ([130, 64, 1, 200], 130, 544, 7),           # dozens of rows each
     ([700, 0, 300], 264, 1152, 2),              # hundreds of rows each
+    ([30, 0, 1, 64] * 50, 256, 160, 6),         # many small groups: 64 x 256 tiles
+    ([40, 3] * 120, 100, 96, 1),                # the same, narrow: 128 x 128
+    ([130, 400] * 40, 290, 224, 4),             # many larger ones: 128 x 256
     ([0, 0, 0], 32, 64, 4),                     # nothing but a tail
 ])
 @pytest.mark.parametrize("indirect", [False, True])
@@ -271,6 +276,44 @@ def test_grouped(sizes, N, K, tail, indirect):
         kept = int(off[-1])
         assert (np.abs(host(out)[:kept] - want[:kept]) <= bound[:kept]).all()
         assert (out[kept:] == 5).all()
+
+
+def test_operands_past_32_bits():
+    """Row blocks of A behind 4 GiB of codes (and, grouped, tables that point
+    there), and a quantisation of more than 2^32 values."""
+    K, rows = 8192, 1_100_000                                 # 4.5 GB of codes
+    cb, sb = nv.mx_packed_size(rows, K)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(12)
+    A = nv.MxOperand(torch.randint(0, 256, (cb,), dtype=torch.uint8, device=DEV, generator=g),
+                     torch.randint(120, 130, (sb,), dtype=torch.uint8, device=DEV, generator=g), rows, K)
+    b = mx_ref.random_operand(rng(12), 3 * 16, K)
+    vb = mx_ref.values(*b)
+    c1, s1 = nv.mx_packed_size(16, K)
+
+    def values(block):
+        """The 16 rows of a row block, unpacked on the host."""
+        return mx_ref.values(*nv.mx_unpack(A.codes[block * c1:(block + 1) * c1].cpu().numpy(),
+                                           A.scales[block * s1:(block + 1) * s1].cpu().numpy(), 16, K))
+
+    c = nv.mx_gemm(A, nv.mx_to_device(b[0][:16], b[1][:16]))
+    last = rows // 16 - 1
+    for block in (0, 40000, last):
+        check(c[block * 16:block * 16 + 16], values(block), vb[:16], 1.0)
+    del c
+    W = nv.mx_groups_to_device(b[0].reshape(3, 16, -1), b[1].reshape(3, 16, -1))
+    pick = torch.tensor([rows - 1, 3, 640000, rows - 2, 17], dtype=torch.int32, device=DEV)
+    off = torch.tensor([0, 2, 2, 5], dtype=torch.int32, device=DEV)
+    y = nv.mx_grouped_gemm(A, W, off, rows=pick)
+    va = np.stack([values(r // 16)[r % 16] for r in pick.tolist()])
+    check(y[:2], va[:2], vb[:16], 1.0)
+    check(y[2:], va[2:], vb[32:], 1.0)
+    del A
+    x = torch.empty(rows // 2, K, dtype=torch.bfloat16, device=DEV).normal_(generator=g)
+    q = nv.mx_quantize(x)
+    tail = nv.MxOperand(q.codes[-c1:], q.scales[-s1:], 16, K)
+    equal_bytes(tail, host(x[-16:]))
+    assert torch.equal(nv.mx_dequantize(q, x.dtype)[-16:], nv.mx_dequantize(tail, x.dtype))
 
 
 def test_grouped_malformed_tables_stay_inside():
@@ -323,13 +366,13 @@ def test_streams_and_graph_replays():
 
 def test_sequence():
     g = rng(10)
-    x = torch.from_numpy(g.standard_normal((24, 544)).astype(np.float32)).to(DEV).to(torch.bfloat16)
+    x = torch.from_numpy(g.standard_normal((15, 544)).astype(np.float32)).to(DEV).to(torch.bfloat16)
     B = nv.mx_to_device(*mx_ref.random_operand(g, 64, 544))
     W = nv.mx_groups_to_device(*(t.reshape(2, 32, -1) for t in mx_ref.random_operand(g, 64, 544)))
-    off = torch.tensor([0, 9, 24], dtype=torch.int32, device=DEV)
+    off = torch.tensor([0, 9, 15], dtype=torch.int32, device=DEV)
     q = nv.mx_quantize(x)
-    c1, c2 = (torch.empty(24, 64, dtype=torch.bfloat16, device=DEV) for _ in range(2))
-    c3 = torch.empty(24, 32, device=DEV)
+    c1, c2 = (torch.empty(15, 64, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    c3 = torch.empty(15, 32, device=DEV)
     seq = nv.Sequence()
     seq.add_mx_quantize(x, q)
     seq.add_mx_gemm(q, B, c1, 0.5)

@@ -106,7 +106,7 @@ def test_gemm_refusals():
     for bad in (dict(x=None), dict(kind=7), dict(ld=32), dict(ld=60), dict(ok=3), dict(N=-1), dict(K=80)):
         assert gemm_q(**bad) == INV, bad
     assert gemm_q(x=P + 2) == MIS
-    assert gemm_q(M=65) == UNS
+    assert gemm_q(M=17) == UNS
     for bad in (dict(off=None), dict(G=0), dict(G=-1), dict(n=3), dict(n=0), dict(rows=P, n=0), dict(out=None),
                 dict(M=-1), dict(N=0), dict(K=100), dict(kind=-1)):
         assert grouped(**bad) == INV, bad
@@ -157,7 +157,7 @@ def test_sequence_refuses_the_same(tmp_path):
     assert L.nvfp4_sequence_create(ctypes.byref(h)) == nv.OK
     try:
         assert L.nvfp4_sequence_add_mx_gemm(h, P, P, P, P, 1.0, P, 1, 4, 4, 40) == INV
-        assert L.nvfp4_sequence_add_mx_gemm_quantized(h, P, 1, 64, P, P, 1.0, P, 1, 65, 4, 64) == UNS
+        assert L.nvfp4_sequence_add_mx_gemm_quantized(h, P, 1, 64, P, P, 1.0, P, 1, 17, 4, 64) == UNS
         assert L.nvfp4_sequence_add_mx_quantize(h, P + 1, 1, 4, 64, 64, P, P) == MIS
         assert L.nvfp4_sequence_add_mx_grouped_gemm(h, P, P, 4, None, P, P, None, 2, 1.0, P, 1, 4, 4, 64) == INV
         assert ML.nvfp4_sequence_add_moe_sort(h, P, 0, 4, 2, 0, P, P, P) == INV
