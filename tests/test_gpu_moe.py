@@ -53,7 +53,8 @@ def check_sort(ids, E, wide=False):
 @pytest.mark.parametrize("T,k,E,drop", [
     (1, 1, 1, 0.0), (1, 8, 256, 0.0), (64, 8, 256, 0.0), (7, 3, 2, 0.5), (512, 8, 256, 0.1), (33, 1, 2048, 0.0),
     (513, 8, 64, 0.0), (1024, 4, 300, 0.05), (3000, 7, 257, 0.3), (9001, 2, 1, 0.5), (100, 6, 40, 1.0),
-    (4096, 1, 7, 0.0), (700, 64, 512, 0.2)])
+    (4096, 1, 7, 0.0), (700, 64, 512, 0.2), (2048, 8, 256, 0.0), (2049, 8, 2048, 0.1),
+    (20000, 3, 5, 0.3), (8192, 8, 256, 0.05)])
 @pytest.mark.parametrize("wide", [False, True])
 def test_sort(T, k, E, drop, wide):
     say(f"sort T={T} k={k} E={E} drop={drop} wide={wide}")
@@ -65,6 +66,21 @@ def test_sort_one_expert_takes_all_and_wide_numbers():
     ids = torch.tensor([[2 ** 32 + 1, 1], [-2 ** 40, 0]], device=DEV)   # low words that look like experts
     r = nv.moe_sort(ids, 4)
     assert r.row_offsets.tolist() == [0, 1, 2, 2, 2] and r.slots.tolist() == [[-1, 1], [-1, 0]]
+
+
+def test_sort_a_long_list():
+    """More than 1024 chunks: larger ones, sorted against torch."""
+    E, ids = 37, torch.from_numpy(choices(rng(1), 600_001, 8, 37, 0.1)).to(DEV)
+    r = nv.moe_sort(ids, E)
+    flat = ids.flatten().long()
+    key = torch.where((flat >= 0) & (flat < E), flat, E)
+    order = torch.argsort(key, stable=True)
+    kept = int((key < E).sum())
+    assert torch.equal(r.row_offsets.long(), torch.searchsorted(key[order], torch.arange(E + 1, device=DEV)))
+    assert torch.equal(r.tokens[:kept].long(), order[:kept] // 8) and (r.tokens[kept:] == -1).all()
+    slots = torch.empty_like(flat)
+    slots[order] = torch.arange(flat.numel(), device=DEV)
+    assert torch.equal(r.slots.flatten().long(), torch.where(key < E, slots, -1))
 
 
 def test_sort_no_tokens():
