@@ -226,9 +226,17 @@ __device__ __forceinline__ Piece<T, V> load_piece(const T* p) {
     __builtin_memcpy(&r, p, sizeof(r));
     return r;
 }
-template <typename T, int V>
+// NT: with the non-temporal hint.
+template <bool NT, typename T, int V>
 __device__ __forceinline__ void store_piece(T* p, const Piece<T, V>& r) {
-    __builtin_memcpy(p, &r, sizeof(r));
+    if constexpr (NT && sizeof(r) == 16) {
+        typedef unsigned int u4 __attribute__((ext_vector_type(4), aligned(2)));
+        u4 t;
+        __builtin_memcpy(&t, &r, 16);
+        __builtin_nontemporal_store(t, reinterpret_cast<u4*>(p));
+    } else {
+        __builtin_memcpy(p, &r, sizeof(r));
+    }
 }
 __device__ __forceinline__ float widen(float x) { return x; }
 __device__ __forceinline__ float widen(uint16_t x) { return __builtin_bit_cast(float, (uint32_t)x << 16); }
@@ -261,7 +269,7 @@ struct Choices {
 };
 
 // out[slot(t, j)] = x[t] for every kept choice: a token's row is read once.
-template <typename T, int V, int B>
+template <typename T, int V, int B, bool NT>
 __global__ void __launch_bounds__(256) moe_gather_kernel(MoeArgs a) {
     const int64_t t = blockIdx.x;
     int64_t col = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * V;
@@ -272,13 +280,13 @@ __global__ void __launch_bounds__(256) moe_gather_kernel(MoeArgs a) {
         const Choices<B> c(a, t, j);
 #pragma unroll
         for (int b = 0; b < B; ++b)
-            if (in && c.row[b] >= 0) store_piece<T, V>(static_cast<T*>(a.out) + (int64_t)c.row[b] * a.hidden + col, r);
+            if (in && c.row[b] >= 0) store_piece<NT, T, V>(static_cast<T*>(a.out) + (int64_t)c.row[b] * a.hidden + col, r);
     }
 }
 
 // out[t] = sum_j w[t][j] * x[slot(t, j)], in fp32 and in the order of j.  B
 // rows are read at a time (row 0 in the place of a dropped choice's, unused).
-template <typename T, int V, int B>
+template <typename T, int V, int B, bool NT>
 __global__ void __launch_bounds__(256) moe_combine_kernel(MoeArgs a) {
     const int64_t t = blockIdx.x;
     int64_t col = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * V;
@@ -302,13 +310,13 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(MoeArgs a) {
     Piece<T, V> o;
 #pragma unroll
     for (int i = 0; i < V; ++i) narrow(sum[i], o.v[i]);
-    if (in) store_piece<T, V>(static_cast<T*>(a.out) + t * a.hidden + col, o);
+    if (in) store_piece<NT, T, V>(static_cast<T*>(a.out) + t * a.hidden + col, o);
 }
 
 // dy[slot(t, j)] = w[t][j] * dout[t];  dw[t][j] = <dout[t], y[slot(t, j)]>.
 // A workgroup per token, B choices at a time; the dot products are added
 // over the lanes of a wave and then over the waves, in a fixed order.
-template <typename T, int V, int B>
+template <typename T, int V, int B, bool NT>
 __global__ void __launch_bounds__(256) moe_combine_grad_kernel(MoeArgs a) {
     __shared__ float part[2][4][B];
     const int64_t t = blockIdx.x;
@@ -338,7 +346,7 @@ __global__ void __launch_bounds__(256) moe_combine_grad_kernel(MoeArgs a) {
                         dot[b] += widen(gv.v[i]) * widen(yv[b].v[i]);
                         narrow(c.weight[b] * widen(gv.v[i]), o.v[i]);
                     }
-                    store_piece<T, V>(d + (int64_t)c.row[b] * a.hidden, o);
+                    store_piece<NT, T, V>(d + (int64_t)c.row[b] * a.hidden, o);
                 }
             } else {  // only its own elements: dy may be y, and the piece before reads the others
 #pragma unroll
@@ -370,7 +378,7 @@ __global__ void __launch_bounds__(256) moe_combine_grad_kernel(MoeArgs a) {
 
 enum RowKernel { GATHER, COMBINE, COMBINE_GRAD };
 
-template <RowKernel K, typename T, int V, int B>
+template <RowKernel K, typename T, int V, int B, bool NT>
 hipError_t run_rows(const MoeArgs& a, hipStream_t stream) {
     // whole waves, as many as the row has pieces for
     const int64_t pieces = (a.hidden + V - 1) / V;
@@ -378,25 +386,37 @@ hipError_t run_rows(const MoeArgs& a, hipStream_t stream) {
     dim3 grid((unsigned)a.tokens);
     if (K != COMBINE_GRAD) grid.y = (unsigned)((pieces + threads - 1) / threads);
     if constexpr (K == GATHER)
-        hipLaunchKernelGGL((moe_gather_kernel<T, V, B>), grid, dim3(threads), 0, stream, a);
+        hipLaunchKernelGGL((moe_gather_kernel<T, V, B, NT>), grid, dim3(threads), 0, stream, a);
     else if constexpr (K == COMBINE)
-        hipLaunchKernelGGL((moe_combine_kernel<T, V, B>), grid, dim3(threads), 0, stream, a);
+        hipLaunchKernelGGL((moe_combine_kernel<T, V, B, NT>), grid, dim3(threads), 0, stream, a);
     else
-        hipLaunchKernelGGL((moe_combine_grad_kernel<T, V, B>), grid, dim3(threads), 0, stream, a);
+        hipLaunchKernelGGL((moe_combine_grad_kernel<T, V, B, NT>), grid, dim3(threads), 0, stream, a);
     return hipGetLastError();
+}
+
+// With rows that outgrow the last-level cache every store is non-temporal: a
+// gather of 65536 rows of 4 KB takes 50 us instead of 59, a combine of them
+// with its gradients 139 instead of 171.  (Non-temporal loads slowed that
+// down: the gradient reads the rows again.)
+template <RowKernel K, typename T, int V, int B>
+hipError_t pick_stores(const MoeArgs& a, hipStream_t stream) {
+    return a.tokens * a.topk * a.hidden * (int64_t)sizeof(T) > kStreamBytes ? run_rows<K, T, V, B, true>(a, stream)
+                                                             : run_rows<K, T, V, B, false>(a, stream);
 }
 
 template <RowKernel K, typename T, int V>
 hipError_t pick_batch(const MoeArgs& a, hipStream_t stream) {
-    if (a.topk >= 7) return run_rows<K, T, V, 8>(a, stream);
-    if (a.topk >= 3) return run_rows<K, T, V, 4>(a, stream);
-    return run_rows<K, T, V, 2>(a, stream);
+    if (a.topk >= 7) return pick_stores<K, T, V, 8>(a, stream);
+    if (a.topk >= 3) return pick_stores<K, T, V, 4>(a, stream);
+    return pick_stores<K, T, V, 2>(a, stream);
 }
 
 template <RowKernel K>
 hipError_t pick(const MoeArgs& a, hipStream_t stream) {
-    if (a.bf16) return a.hidden >= 8 ? pick_batch<K, uint16_t, 8>(a, stream) : run_rows<K, uint16_t, 1, 4>(a, stream);
-    return a.hidden >= 4 ? pick_batch<K, float, 4>(a, stream) : run_rows<K, float, 1, 4>(a, stream);
+    if (a.bf16)
+        return a.hidden >= 8 ? pick_batch<K, uint16_t, 8>(a, stream)
+                             : run_rows<K, uint16_t, 1, 4, false>(a, stream);
+    return a.hidden >= 4 ? pick_batch<K, float, 4>(a, stream) : run_rows<K, float, 1, 4, false>(a, stream);
 }
 
 template <typename I, int MAXE>
