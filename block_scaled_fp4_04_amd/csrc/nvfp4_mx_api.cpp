@@ -33,8 +33,12 @@ int prepare_mx_quantize(bool inverse, const void* x, int x_type, int64_t groups,
         !valid_rows_k(rows, K))
         return NVFP4_ERR_INVALID_VALUE;
     const int64_t per16 = x_type == NVFP4_TYPE_BF16 ? 8 : 4;  // elements in 16 bytes
-    if ((rows > 1 && ld < K) || ld < 0 || ld % per16 || group_stride < 0 || group_stride % per16)
+    // (strides that nothing is reached by are not looked at)
+    if (rows <= 1) ld = K;
+    if (groups <= 1) group_stride = 0;
+    if (ld < K || ld % per16 || group_stride < 0 || group_stride % per16)
         return NVFP4_ERR_INVALID_VALUE;
+    if (inverse && groups > 1 && group_stride < K) return NVFP4_ERR_INVALID_VALUE;  // would overlap
     if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 16)) return NVFP4_ERR_MISALIGNED;
     const int64_t RB = mx_row_blocks(rows), C = mx_steps(K);
     // (a wave per fragment; groups * RB * C cannot wrap: each factor is checked first)
@@ -75,7 +79,8 @@ int prepare_mx_gemm(const void* a_packed, const void* a_scales, const void* x, i
         return NVFP4_ERR_INVALID_VALUE;
     if (x) {
         const int64_t per16 = x_type == NVFP4_TYPE_BF16 ? 8 : 4;
-        if ((M > 1 && ldx < K) || ldx < 0 || ldx % per16) return NVFP4_ERR_INVALID_VALUE;
+        if (M <= 1) ldx = K;
+        if (ldx < K || ldx % per16) return NVFP4_ERR_INVALID_VALUE;
     }
     if (!aligned(a_packed, 16) || !aligned(a_scales, 16) || !aligned(x, 16) ||
         !aligned(b_packed, 16) || !aligned(b_scales, 16) || !aligned(out, 16) ||
@@ -149,7 +154,7 @@ int prepare_moe_rows(const void* x, const void* y, int type, int64_t tokens, int
                      void* out, float* dweights, bool grad, Job* job) {
     if (!valid_type(type) || hidden < 1 || hidden > ((int64_t)1 << 22) ||
         (tokens > 0 && (!x || !slots || !out || (grad && (!y || !dweights)))) ||
-        (tokens > 1 && ld < hidden) || ld < 0 || ld > kMaxDim)
+        (tokens > 1 && (ld < hidden || ld > kMaxDim)))
         return NVFP4_ERR_INVALID_VALUE;
     const int st = prepare_moe(tokens, topk, job);
     if (st != NVFP4_OK) return st;
@@ -160,7 +165,7 @@ int prepare_moe_rows(const void* x, const void* y, int type, int64_t tokens, int
     MoeArgs& a = job->moe;
     a.bf16 = type == NVFP4_TYPE_BF16;
     a.hidden = hidden;
-    a.ld_in = ld;
+    a.ld_in = tokens > 1 ? ld : hidden;
     a.slots = const_cast<int32_t*>(slots);
     a.x = x;
     a.y = y;

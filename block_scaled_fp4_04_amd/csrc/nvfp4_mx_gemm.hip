@@ -236,10 +236,18 @@ __global__ void __launch_bounds__(KS * 256, KS > 1 || BM * BN > 128 * 256 ? KS :
     constexpr int SPW = CPW;                              // a wave's scale loads, every fourth step
     constexpr int STAGE = (AF + BF) * kMxFrag;
     constexpr int SCALES = (AF + BF) * kMxScaleFrag;      // of four steps
-    // (NS <= 4: the next scale word's loads, issued in the middle of a word's
-    // first step, have landed in the middle of its last one)
-    static_assert((AF + BF) % 4 == 0 && NS >= 2 && NS <= 4 && NS * CPW + SPW < 64, "ring");
-    constexpr int RING = NS * STAGE + SCALES;
+    // Step c's place in the ring is filled again, for step c + NS, from the
+    // middle of step c on; a scale word's first step c fills the place of word
+    // c / 4 with the one NQ words on, which is not needed before.
+    constexpr int NQ = (NS + 3) / 4;
+    // scale loads among those issued at the `many` steps before step k
+    constexpr auto scale_loads = [](int k, int many) {
+        int n = 0;
+        for (int d = 1; d <= many; ++d) n += ((k - d) & 3) == 0 ? SPW : 0;
+        return n;
+    };
+    static_assert((AF + BF) % 4 == 0 && NS >= 2 && (NS + 1) * CPW + NQ * SPW < 64, "ring");
+    constexpr int RING = NS * STAGE + NQ * SCALES;
     static_assert(BM * WN * (BN / WN * 2 + 16) <= RING, "the output is staged in the first ring");
     static_assert((KS - 1) * BM * BN * 4 <= KS * RING, "and partial tiles in all");
     __shared__ __attribute__((aligned(1024))) uint8_t lds_all[KS * RING];
@@ -372,11 +380,11 @@ __global__ void __launch_bounds__(KS * 256, KS > 1 || BM * BN > 128 * 256 ? KS :
         mx_dma<16, i * kMxFrag>(wave * CPW + i < AF ? rac : rbc, code_at[i], (uint32_t)min(c0 + c, C - 1) * kMxFrag,
                                 lds0 + (uint32_t)(stage * STAGE + wave * CPW * kMxFrag));
     };
-    auto load_scale = [&](auto I, int q) {
+    auto load_scale = [&](auto I, int q, int place) {
         constexpr int i = I.value;
         mx_dma<4, NS * STAGE + i * kMxScaleFrag>(wave * CPW + i < AF ? ras : rbs, scale_at[i],
                                                  (uint32_t)min(q0 + q, Q - 1) * kMxScaleFrag,
-                                                 lds0 + (uint32_t)(wave * CPW * kMxScaleFrag));
+                                                 lds0 + (uint32_t)(place * SCALES + wave * CPW * kMxScaleFrag));
     };
 
     mx_f16 acc[MI][NI];
@@ -413,14 +421,14 @@ __global__ void __launch_bounds__(KS * 256, KS > 1 || BM * BN > 128 * 256 ? KS :
             h.b[i - MI] = *reinterpret_cast<const mx_u4*>(p + (fb + 2 * (i - MI)) * kMxFrag);
     };
     // the two scale words of 32-row block I
-    auto read_scale = [&](auto I, Scales& s) {
+    auto read_scale = [&](auto I, Scales& s, int place) {
         constexpr int i = I.value;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
             if constexpr (i < MI)
-                s.a[i][h] = *reinterpret_cast<const uint32_t*>(lane_sa + 2 * i * kMxScaleFrag + h * 8);
+                s.a[i][h] = *reinterpret_cast<const uint32_t*>(lane_sa + place * SCALES + 2 * i * kMxScaleFrag + h * 8);
             else
-                s.b[i - MI][h] = *reinterpret_cast<const uint32_t*>(lane_sb + 2 * (i - MI) * kMxScaleFrag + h * 8);
+                s.b[i - MI][h] = *reinterpret_cast<const uint32_t*>(lane_sb + place * SCALES + 2 * (i - MI) * kMxScaleFrag + h * 8);
     };
     Scales sc, sn;
     auto mfma = [&](auto N, auto S, const Half& h, int half) {
@@ -429,19 +437,26 @@ __global__ void __launch_bounds__(KS * 256, KS > 1 || BM * BN > 128 * 256 ? KS :
     };
 
     // fill the ring
-    mx_each<SPW>([&](auto I) { load_scale(I, 0); });
-    mx_each<NS>([&](auto c) { mx_each<CPW>([&](auto I) { load_code(I, c.value, c.value); }); });
-    wait_vmcnt<(NS - 1) * CPW>();  // step 0 and the first scale word
+    mx_each<NQ>([&](auto q) {
+        if constexpr (q.value < NQ - NS / 4) mx_each<SPW>([&](auto I) { load_scale(I, q.value, q.value); });
+    });
+    mx_each<NS>([&](auto c) {
+        mx_each<CPW>([&](auto I) { load_code(I, c.value, c.value); });
+        // (as if at step c - NS)
+        constexpr int q = (c.value - NS) / 4 + NQ;
+        if constexpr ((c.value - NS) % 4 == 0) mx_each<SPW>([&](auto I) { load_scale(I, q, q); });
+    });
+    wait_vmcnt<(NS - 1) * CPW + scale_loads(0, NS - 1)>();  // step 0 and the first scale word
     wg_barrier();
     Half h0, h1;
-    mx_each<P>([&](auto I) { read_scale(I, sc); });
+    mx_each<P>([&](auto I) { read_scale(I, sc, 0); });
     mx_each<P>([&](auto I) { read(I, h0, 0, 0); });
 
     // One step.  The order is fixed (the scheduling barriers): behind each
     // MFMA one LDS read and its share of the loads, which issue while the
     // MFMA runs; left to itself the compiler moves the reads to their uses
     // and the MFMAs wait for each.
-    int c = 0, stage = 0;
+    int c = 0, stage = 0, place = 0;
     auto step = [&](auto S) {
         constexpr int s = S.value;
         mx_each<MM>([&](auto N) {
@@ -451,8 +466,8 @@ __global__ void __launch_bounds__(KS * 256, KS > 1 || BM * BN > 128 * 256 ? KS :
         });
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         // step c + 1 has landed: what may be in flight was issued in the last
-        // NS - 2 steps (the scales in a word's first one)
-        wait_vmcnt<(NS - 2) * CPW + (s > 0 && s <= NS - 2 ? SPW : 0)>();
+        // NS - 2 steps
+        wait_vmcnt<(NS - 2) * CPW + scale_loads(s, NS - 2)>();
         wg_barrier();
         __builtin_amdgcn_sched_barrier(0);
         const int freed = stage;
@@ -462,16 +477,19 @@ __global__ void __launch_bounds__(KS * 256, KS > 1 || BM * BN > 128 * 256 ? KS :
             mfma(N, S, h1, 1);
             mx_each<P>([&](auto I) {
                 if constexpr (slot_of(I.value) == n) read(I, h0, stage, 0);
-                if constexpr (s == 3 && MM - 1 - slot_of(I.value) == n) read_scale(I, sn);
+                if constexpr (s == 3 && MM - 1 - slot_of(I.value) == n) read_scale(I, sn, NQ > 1 ? (place + 1) % NQ : 0);
             });
             mx_each<(n + 1) * CPW / MM - n * CPW / MM>([&](auto I) {
                 constexpr int i = n * CPW / MM + I.value;
                 load_code(std::integral_constant<int, i>{}, c + NS, freed);
-                if constexpr (s == 0) load_scale(std::integral_constant<int, i>{}, c / 4 + 1);
+                if constexpr (s == 0) load_scale(std::integral_constant<int, i>{}, c / 4 + NQ, place);
             });
             __builtin_amdgcn_sched_barrier(0);
         });
-        if constexpr (s == 3) sc = sn;
+        if constexpr (s == 3) {
+            sc = sn;
+            if constexpr (NQ > 1) place = (place + 1) % NQ;
+        }
         ++c;
     };
     // whole scale words, then the steps that are left (one loop exit: the

@@ -73,8 +73,9 @@ int nvfp4_mx_unpack(const uint8_t* packed_codes, const uint8_t* packed_scales, i
  * codes: it reads as NaN, and so do the results that it enters.
  *   x            : DEVICE, `groups` matrices of rows x K values of type
  *                  x_type (NVFP4_TYPE_F32 or NVFP4_TYPE_BF16), row stride ld
- *                  and group stride group_stride elements: ld >= K (any if
- *                  rows is 1), both multiples of 4 (fp32) or 8 (bfloat16)
+ *                  and group stride group_stride elements: ld >= K, both
+ *                  multiples of 4 (fp32) or 8 (bfloat16); a single row's or
+ *                  group's stride is not looked at
  *   packed_codes,
  *   packed_scales: DEVICE, groups x nvfp4_mx_packed_size(rows, K) bytes
  *                  (group g at g times those); every byte is written
@@ -86,8 +87,9 @@ int nvfp4_mx_quantize(const void* x, int x_type, int64_t groups, int64_t group_s
 
 /* The values that packed operands stand for, as fp32 or bfloat16 rows (exact
  * in both: a code has two significant bits; NaN for blocks with scale 255).
- * Buffers and strides as nvfp4_mx_quantize; writes the rows x K elements of
- * every group and nothing between them. */
+ * Buffers and strides as nvfp4_mx_quantize (group_stride >= K: groups must not
+ * overlap); writes the rows x K elements of every group and nothing between
+ * them. */
 int nvfp4_mx_dequantize(const void* packed_codes, const void* packed_scales, int64_t groups,
                         int64_t rows, int64_t K, void* x, int x_type, int64_t group_stride,
                         int64_t ld, void* stream);

@@ -202,6 +202,43 @@ def test_strided_and_unaligned_rows():
         assert torch.equal(nv.moe_combine(flat, r), nv.moe_combine(flat.clone(), r))
 
 
+def test_more_than_2_31_elements():
+    """Rows behind 2^32 bytes and 2^31 elements of the experts' order."""
+    T, k, E, H = 300_000, 8, 16, 1024
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+    ids = torch.randint(0, E, (T, k), device=DEV, generator=g)
+    r = nv.moe_sort(ids, E)
+    x = torch.randn(T, H, device=DEV, generator=g).to(torch.bfloat16)
+    rows = nv.moe_gather(x, r)
+    for i in (0, T * k // 2, T * k - 1):
+        assert torch.equal(rows[i], x[r.tokens[i].long()])
+    dy, dw = nv.moe_combine_grad(x, rows, r)
+    assert torch.equal(dy[-1000:], rows[-1000:])              # every row holds its token's gradient
+    want = (x[-50:].double() ** 2).sum(1, keepdim=True).expand(50, k)
+    assert ((dw[-50:].double() - want).abs() <= (H + 1) * 2.0 ** -24 * want).all()
+    back = nv.moe_gather_grad(rows, r)
+    # k equal values of 8 bits: their sums are exact in fp32, and rounded once
+    assert torch.equal(back, (k * x.float()).to(torch.bfloat16))
+
+
+def test_other_streams_and_shared_tables():
+    """Two streams at once with the same route: no call keeps anything."""
+    T, k, E, H = 128, 4, 8, 512
+    ids, r, make, w = case(T, k, E, H, "bf16")
+    x, wd, idt = make(T, H).to(DEV), w.to(DEV), torch.from_numpy(ids).to(DEV)
+    want = nv.moe_combine(nv.moe_gather(x, r, out=torch.zeros(T * k, H, dtype=x.dtype, device=DEV)), r, wd)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(10):
+        for s in streams:
+            route = nv.moe_sort(idt, E, stream=s)
+            got.append(nv.moe_combine(nv.moe_gather(x, route, stream=s), route, wd, stream=s))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in got)
+
+
 def test_malformed_slots_stay_inside():
     ids, r, make, w = case(16, 2, 4, 32, "fp32", drop=0.0)
     bad = nv.MoeRoute(r.row_offsets, torch.full_like(r.slots, 1 << 30), r.tokens, 4)

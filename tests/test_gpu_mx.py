@@ -96,6 +96,14 @@ def test_quantize_strided_rows_and_groups():
             equal_bytes(one, host(t[i, :18, :160]))
 
 
+def test_one_row_of_a_wider_buffer():
+    """A single row's stride does not matter."""
+    x = torch.randn(1, 70, device=DEV).to(torch.bfloat16)[:, :64]
+    B = nv.mx_quantize(torch.randn(32, 64, device=DEV))
+    equal_bytes(nv.mx_quantize(x), host(x))
+    assert torch.equal(nv.mx_gemm_quantized(x, B), nv.mx_gemm(nv.mx_quantize(x.contiguous()), B))
+
+
 def test_quantize_refuses_misaligned_rows():
     x = torch.zeros(4, 64 + 4, dtype=torch.bfloat16, device=DEV)
     with pytest.raises(nv.Nvfp4Error) as e:

@@ -78,11 +78,14 @@ def quant(fn="nvfp4_mx_quantize", x=P, kind=1, groups=1, gs=0, rows=4, K=64, ld=
 @pytest.mark.parametrize("fn", ["nvfp4_mx_quantize", "nvfp4_mx_dequantize"])
 def test_quantize_refusals(fn):
     for bad in (dict(x=None), dict(c=None), dict(s=None), dict(kind=2), dict(kind=-1), dict(groups=-1),
-                dict(rows=-1), dict(K=0), dict(K=48), dict(ld=32), dict(ld=68), dict(gs=4), dict(gs=-8),
+                dict(rows=-1), dict(K=0), dict(K=48), dict(ld=32), dict(ld=68), dict(groups=2, gs=4), dict(groups=2, gs=-8),
                 dict(kind=0, ld=66), dict(groups=2 ** 40), dict(rows=2 ** 30, K=2 ** 20, ld=2 ** 20)):
         assert quant(fn, **bad) == INV, bad
     for bad in (dict(x=P + 8), dict(c=P + 4), dict(s=P + 1)):
         assert quant(fn, **bad) == MIS, bad
+    overlap = quant(fn, groups=2, gs=32, x=P + 8)          # one matrix for all groups may be read, not written
+    assert overlap == (MIS if fn == "nvfp4_mx_quantize" else INV)
+    assert quant(fn, rows=1, ld=3, x=P + 8) == MIS         # (a single row's stride is not looked at)
 
 
 def gemm(a=P, sa=P, b=P, sb=P, out=P, kind=1, M=4, N=4, K=64):
@@ -130,7 +133,7 @@ def test_moe_refusals():
         return L.nvfp4_moe_gather(x, kind, T, k, H, ld, slots, out, None)
 
     for bad in (dict(x=None), dict(slots=None), dict(out=None), dict(kind=5), dict(T=-2), dict(k=0), dict(H=0),
-                dict(H=2 ** 23), dict(ld=7), dict(ld=-8)):
+                dict(H=2 ** 23), dict(ld=7), dict(ld=-8), dict(ld=2 ** 31)):
         assert gather(**bad) == INV, bad
     for bad in (dict(x=P + 1), dict(out=P + 1), dict(slots=P + 2), dict(kind=0, x=P + 2)):
         assert gather(**bad) == MIS, bad
