@@ -666,6 +666,7 @@ class Sequence:
 
     def add_mx_quantize(self, x, out: "MxOperand") -> None:
         """Records mx_quantize(x, out) for a 2-D x."""
+        from . import mx
         if x.dim() != 2:
             raise ValueError("x must be a 2-D tensor")
         out, a = mx._quantize_args(x, out)
@@ -674,6 +675,7 @@ class Sequence:
 
     def add_mx_gemm(self, a: "MxOperand", b: "MxOperand", out, alpha: float = 1.0) -> None:
         """Records mx_gemm(a, b, alpha, out)."""
+        from . import mx
         out, args = mx._gemm_args(a, b, alpha, out, None)
         mx._gpu_of((a.codes, a.scales, b.codes, b.scales, out))
         self._record(mx.mx_lib().nvfp4_sequence_add_mx_gemm, args,
@@ -681,6 +683,7 @@ class Sequence:
 
     def add_mx_gemm_quantized(self, x, b: "MxOperand", out, alpha: float = 1.0) -> None:
         """Records mx_gemm_quantized(x, b, alpha, out)."""
+        from . import mx
         out, args = mx._gemm_quantized_args(x, b, alpha, out, None)
         mx._gpu_of((x, b.codes, b.scales, out))
         self._record(mx.mx_lib().nvfp4_sequence_add_mx_gemm_quantized, args, [x, b, out])
@@ -688,12 +691,14 @@ class Sequence:
     def add_mx_grouped_gemm(self, a: "MxOperand", b: "MxGroups", row_offsets, out,
                             alpha: float = 1.0, rows=None) -> None:
         """Records mx_grouped_gemm(a, b, row_offsets, alpha, rows, out)."""
+        from . import mx
         out, args = mx._grouped_args(a, b, row_offsets, alpha, rows, out, None)
         mx._gpu_of((a.codes, a.scales, b.codes, b.scales, row_offsets, rows, out))
         self._record(mx.mx_lib().nvfp4_sequence_add_mx_grouped_gemm, args, [a, b, row_offsets, rows, out])
 
     def add_moe_sort(self, expert_ids, out: "MoeRoute") -> None:
         """Records moe_sort(expert_ids, out.experts, out)."""
+        from . import moe, mx
         out, args = moe._sort_args(expert_ids, out.experts, out)
         mx._gpu_of((expert_ids, out.row_offsets, out.slots, out.tokens))
         self._record(moe.moe_lib().nvfp4_sequence_add_moe_sort, args,
@@ -701,12 +706,14 @@ class Sequence:
 
     def add_moe_gather(self, x, route: "MoeRoute", out) -> None:
         """Records moe_gather(x, route, out)."""
+        from . import moe, mx
         out, args = moe._gather_args(x, route, out)
         mx._gpu_of((x, route.slots, out))
         self._record(moe.moe_lib().nvfp4_sequence_add_moe_gather, args, [x, route, out])
 
     def add_moe_combine(self, y, route: "MoeRoute", weights, out) -> None:
         """Records moe_combine(y, route, weights, out)."""
+        from . import moe, mx
         out, args = moe._combine_args(y, route, weights, out)
         mx._gpu_of((y, route.slots, weights, out))
         self._record(moe.moe_lib().nvfp4_sequence_add_moe_combine, args, [y, route, weights, out])
@@ -735,10 +742,26 @@ class Sequence:
             pass
 
 
-from . import mx, moe  # noqa: E402  (they use the names above)
-from .mx import (MX_BLOCK, MX_EXPORTS, MX_QUANT_ROWS, TYPE_BF16, TYPE_F32,  # noqa: E402,F401
-                 MxGroups, MxOperand, mx_dequantize, mx_gemm, mx_gemm_quantized,
-                 mx_grouped_gemm, mx_groups_to_device, mx_linear, mx_pack, mx_packed_size,
-                 mx_quantize, mx_to_device, mx_unpack)
-from .moe import (INDEX_I32, INDEX_I64, MOE_EXPORTS, MOE_MAX_EXPERTS, MoeRoute,  # noqa: E402,F401
-                  moe_combine, moe_combine_grad, moe_gather, moe_gather_grad, moe_sort)
+# The MXFP4 operators and the expert routing (mx.py, moe.py) need torch at
+# import: they are loaded when one of their names is first asked for.
+_LATER = {"mx": ("mx", "MX_BLOCK", "MX_EXPORTS", "MX_QUANT_ROWS", "TYPE_BF16", "TYPE_F32", "MxGroups",
+                 "MxOperand", "mx_dequantize", "mx_gemm", "mx_gemm_quantized", "mx_grouped_gemm",
+                 "mx_groups_to_device", "mx_linear", "mx_pack", "mx_packed_size", "mx_quantize",
+                 "mx_to_device", "mx_unpack"),
+          "moe": ("moe", "INDEX_I32", "INDEX_I64", "MOE_EXPORTS", "MOE_MAX_EXPERTS", "MoeRoute",
+                  "moe_combine", "moe_combine_grad", "moe_gather", "moe_gather_grad", "moe_sort")}
+
+
+def __getattr__(name: str):
+    for part, names in _LATER.items():
+        if name in names:
+            import importlib
+            module = importlib.import_module(f"{__name__}.{part}")
+            globals().update({n: getattr(module, n) for n in names[1:]})
+            globals()[part] = module
+            return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def __dir__():
+    return sorted(set(globals()) | {n for names in _LATER.values() for n in names})

@@ -15,6 +15,8 @@ from __future__ import annotations
 import ctypes
 from dataclasses import dataclass
 
+import torch
+
 from . import _i64, _vp, lib
 from .mx import _on, _rows_2d, _run
 
@@ -66,15 +68,13 @@ class MoeRoute:
     def check(self) -> None:
         import torch
         off, slots, tokens = self.row_offsets, self.slots, self.tokens
-        for what, t, ok in (("row_offsets", off, off.numel() == self.experts + 1),
-                            ("slots", slots, slots.dim() == 2),
-                            ("tokens", tokens, tokens.numel() == slots.numel())):
-            if t.dtype != torch.int32 or not t.is_contiguous() or not ok:
-                raise ValueError(f"route.{what} must be a contiguous int32 tensor of its shape")
+        if not (off.dtype is slots.dtype is tokens.dtype is torch.int32 and slots.dim() == 2
+                and off.numel() == self.experts + 1 and tokens.numel() == slots.numel()
+                and off.is_contiguous() and slots.is_contiguous() and tokens.is_contiguous()):
+            raise ValueError("the tables of a route must be contiguous int32 tensors of their shapes")
 
 
 def _sort_args(ids, experts, out):
-    import torch
     if ids.dim() != 2 or ids.dtype not in (torch.int32, torch.int64) or not ids.is_contiguous():
         raise ValueError("expert_ids must be a contiguous [tokens, topk] int32 or int64 tensor")
     T, k = ids.shape
@@ -104,7 +104,6 @@ def moe_sort(expert_ids, experts: int, out: MoeRoute | None = None, stream=None)
 
 
 def _weights(weights, route):
-    import torch
     if weights is None:
         return None
     if (weights.dtype != torch.float32 or weights.shape != route.slots.shape
@@ -116,7 +115,6 @@ def _weights(weights, route):
 
 def _like(t, name: str, rows: int, hidden: int, dtype, like):
     """`t` made beside `like`, or checked to be a contiguous rows x hidden tensor of `dtype`."""
-    import torch
     if t is None:
         return like.new_empty((rows, hidden), dtype=dtype)
     if tuple(t.shape) != (rows, hidden) or t.dtype != dtype or not t.is_contiguous():
@@ -184,7 +182,6 @@ def moe_combine_grad(dout, y, route: MoeRoute, weights=None, dy=None, dweights=N
     if stream is not None:
         with _on(stream):
             return moe_combine_grad(dout, y, route, weights, dy, dweights)
-    import torch
     kind = _rows_2d(dout, "dout")
     route.check()
     T, k = route.slots.shape

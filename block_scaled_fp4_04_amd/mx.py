@@ -16,6 +16,7 @@ import ctypes
 from dataclasses import dataclass
 
 import numpy as np
+import torch
 
 from . import Nvfp4Error, _i64, _u8p, _vp, lib
 
@@ -119,11 +120,12 @@ def mx_unpack(packed_codes: np.ndarray, packed_scales: np.ndarray, rows: int, K:
 
 
 def _check_packed(name: str, codes, scales, groups: int, rows: int, K: int) -> None:
-    import torch
     cb, sb = _packed(rows, K)
-    for what, t, need in ((".codes", codes, cb * groups), (".scales", scales, sb * groups)):
-        if t.dtype != torch.uint8 or t.numel() != need or not t.is_contiguous():
-            raise ValueError(f"{name}{what} must be a contiguous uint8 tensor of {need} bytes")
+    if (codes.dtype is torch.uint8 and scales.dtype is torch.uint8 and codes.numel() == cb * groups
+            and scales.numel() == sb * groups and codes.is_contiguous() and scales.is_contiguous()):
+        return
+    raise ValueError(f"{name}.codes and {name}.scales must be contiguous uint8 tensors of "
+                     f"{cb * groups} and {sb * groups} bytes")
 
 
 @dataclass
@@ -156,7 +158,6 @@ class MxGroups:
 
 def mx_to_device(codes: np.ndarray, scales: np.ndarray, device="cuda") -> MxOperand:
     """Pack canonical host arrays and copy them to ``device``."""
-    import torch
     rows, K = _check_canonical(codes, scales)
     pc, ps = mx_pack(codes, scales)
     return MxOperand(torch.from_numpy(pc).to(device), torch.from_numpy(ps).to(device), rows, K)
@@ -165,7 +166,6 @@ def mx_to_device(codes: np.ndarray, scales: np.ndarray, device="cuda") -> MxOper
 def mx_groups_to_device(codes: np.ndarray, scales: np.ndarray, device="cuda") -> MxGroups:
     """Pack canonical weights [G, rows, K/2] and [G, rows, K/32] and copy
     them to ``device``."""
-    import torch
     if codes.ndim != 3 or scales.ndim != 3 or codes.shape[0] != scales.shape[0]:
         raise ValueError("codes and scales must be [G, rows, K/2] and [G, rows, K/32]")
     parts = [mx_pack(c, s) for c, s in zip(codes, scales)]
@@ -191,43 +191,46 @@ def _gpu_of(tensors) -> int:
 def _on(stream):
     """The context of a stream (a torch stream or a raw handle): what a call
     allocates in it belongs to that stream."""
-    import torch
     if not hasattr(stream, "cuda_stream"):
         stream = (torch.cuda.ExternalStream(int(stream)) if int(stream)
                   else torch.cuda.default_stream())
     return torch.cuda.stream(stream)
 
 
+_current_gpu = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _run(fn, args: tuple, tensors: tuple) -> None:
     """Calls the C function on the GPU where the tensors lie, on its current
     stream."""
-    import torch
     gpu = _gpu_of(tensors)
-    if gpu == torch._C._cuda_getDevice():
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(gpu))
+    if gpu == _current_gpu():
+        st = fn(*args, _current_stream(gpu))
     else:
         with torch.cuda.device(gpu):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(gpu))
+            st = fn(*args, _current_stream(gpu))
     if st:
         sizes = ", ".join(str(a) for a in args if isinstance(a, int) and 0 <= a < 1 << 31)
         raise Nvfp4Error(st, f"{fn.__name__}({sizes})")
 
 
+_KINDS = {torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16}
+
+
 def _type_of(dtype, what: str) -> int:
-    import torch
-    if dtype is torch.bfloat16:
-        return TYPE_BF16
-    if dtype is torch.float32:
-        return TYPE_F32
-    raise ValueError(f"{what} must be float32 or bfloat16, not {dtype}")
+    kind = _KINDS.get(dtype)
+    if kind is None:
+        raise ValueError(f"{what} must be float32 or bfloat16, not {dtype}")
+    return kind
 
 
 def _out(out, dtype, M: int, N: int, like):
     """The output tensor (made beside `like`, or the given one checked) and its
     type code."""
     if out is None:
-        out = like.new_empty((M, N), dtype=dtype)
-    elif tuple(out.shape) != (M, N) or not out.is_contiguous():
+        return like.new_empty((M, N), dtype=dtype), _type_of(dtype, "out")
+    if tuple(out.shape) != (M, N) or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous tensor of shape ({M}, {N})")
     return out, _type_of(out.dtype, "out")
 
@@ -235,33 +238,35 @@ def _out(out, dtype, M: int, N: int, like):
 def _rows_2d(x, what: str = "x") -> int:
     """Checks a 2-D float32 / bfloat16 tensor with unit stride along K and
     returns its type code."""
-    if x.dim() != 2 or (x.stride(1) != 1 and x.shape[1] != 1):
+    strides = x.stride()
+    if len(strides) != 2 or (strides[1] != 1 and x.shape[1] != 1):
         raise ValueError(f"{what} must be a 2-D tensor with unit stride along its rows")
     return _type_of(x.dtype, what)
 
 
 def _quantize_args(x, out):
     """(operand, C arguments) of mx_quantize for a 2-D or 3-D x."""
-    import torch
-    if x.dim() not in (2, 3) or x.stride(-1) != 1:
+    strides, shape = x.stride(), x.shape
+    if len(shape) not in (2, 3) or strides[-1] != 1:
         raise ValueError("x must be a 2-D or 3-D tensor with unit stride along K")
     kind = _type_of(x.dtype, "x")
-    groups = x.shape[0] if x.dim() == 3 else 1
-    rows, K = x.shape[-2:]
+    grouped = len(shape) == 3
+    groups, group_stride = (shape[0], strides[0]) if grouped else (1, 0)
+    rows, K = shape[-2:]
     if out is None:
         if K < MX_BLOCK or K % MX_BLOCK:
             raise ValueError(f"K must be a positive multiple of {MX_BLOCK}, not {K}")
         cb, sb = _packed(rows, K)
         codes = x.new_empty(cb * groups, dtype=torch.uint8)
         scales = x.new_empty(sb * groups, dtype=torch.uint8)
-        out = (MxGroups(codes, scales, groups, rows, K) if x.dim() == 3
-               else MxOperand(codes, scales, rows, K))
+        out = MxGroups(codes, scales, groups, rows, K) if grouped else MxOperand(codes, scales, rows, K)
     else:
-        if (out.rows, out.K) != (rows, K) or getattr(out, "groups", 1) != groups:
+        if (out.rows, out.K, getattr(out, "groups", None)) != (rows, K, groups if grouped else None):
             raise ValueError("out has the wrong shape")
         out.check("out")
-    return out, (x.data_ptr(), kind, groups, x.stride(0) if x.dim() == 3 else 0, rows, K,
-                 x.stride(-2), out.codes.data_ptr(), out.scales.data_ptr())
+        codes, scales = out.codes, out.scales
+    return out, (x.data_ptr(), kind, groups, group_stride, rows, K, strides[-2], codes.data_ptr(),
+                 scales.data_ptr())
 
 
 def mx_quantize(x, out=None, stream=None):
@@ -284,7 +289,6 @@ def mx_dequantize(a, dtype=None, out=None, stream=None):
     if stream is not None:
         with _on(stream):
             return mx_dequantize(a, dtype, out)
-    import torch
     groups = getattr(a, "groups", None)
     shape = (a.rows, a.K) if groups is None else (groups, a.rows, a.K)
     if out is None:
@@ -315,7 +319,6 @@ def mx_gemm(a: MxOperand, b: MxOperand, alpha: float = 1.0, out=None, dtype=None
     if stream is not None:
         with _on(stream):
             return mx_gemm(a, b, alpha, out, dtype)
-    import torch
     out, args = _gemm_args(a, b, alpha, out, dtype or torch.bfloat16)
     _run(mx_lib().nvfp4_mx_gemm, args, (a.codes, a.scales, b.codes, b.scales, out))
     return out
@@ -339,7 +342,6 @@ def mx_gemm_quantized(x, b: MxOperand, alpha: float = 1.0, out=None, dtype=None,
     if stream is not None:
         with _on(stream):
             return mx_gemm_quantized(x, b, alpha, out, dtype)
-    import torch
     out, args = _gemm_quantized_args(x, b, alpha, out, dtype or torch.bfloat16)
     _run(mx_lib().nvfp4_mx_gemm_quantized, args, (x, b.codes, b.scales, out))
     return out
@@ -358,7 +360,6 @@ def mx_linear(x, b: MxOperand, alpha: float = 1.0, out=None, dtype=None, stream=
 
 
 def _grouped_args(a, b, row_offsets, alpha, rows, out, dtype):
-    import torch
     if a.K != b.K:
         raise ValueError(f"K dimension mismatch: A has K={a.K}, B has K={b.K}")
     if (row_offsets.dtype != torch.int32 or row_offsets.numel() != b.groups + 1
@@ -387,7 +388,6 @@ def mx_grouped_gemm(a: MxOperand, b: MxGroups, row_offsets, alpha: float = 1.0, 
     if stream is not None:
         with _on(stream):
             return mx_grouped_gemm(a, b, row_offsets, alpha, rows, out, dtype)
-    import torch
     out, args = _grouped_args(a, b, row_offsets, alpha, rows, out, dtype or torch.bfloat16)
     _run(mx_lib().nvfp4_mx_grouped_gemm, args,
          (a.codes, a.scales, b.codes, b.scales, row_offsets, rows, out))
