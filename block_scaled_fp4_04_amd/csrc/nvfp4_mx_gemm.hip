@@ -41,29 +41,35 @@ __device__ __forceinline__ void mx_each(F&& f, std::integer_sequence<int, I...>)
 template <int N, typename F>
 __device__ __forceinline__ void mx_each(F&& f) { mx_each(f, std::make_integer_sequence<int, N>{}); }
 
-// Four consecutive columns of C, scaled and rounded; N need not be a multiple
-// of anything.
+// Stores of rows of C that may start anywhere (N need not be a multiple of
+// anything): a piece is one access, aligned to its elements only.
+typedef unsigned int mx_u2_any __attribute__((ext_vector_type(2), aligned(2)));
+typedef unsigned int mx_u4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef float mx_f4_any __attribute__((ext_vector_type(4), aligned(4)));
+
+__device__ __forceinline__ uint32_t mx_bf16_pair(float x, float y) {
+    return mx_to_bf16(x) | (uint32_t)mx_to_bf16(y) << 16;
+}
+
+// Four consecutive columns of C, scaled and rounded.
 __device__ __forceinline__ void mx_store4(const MxGemmArgs& a, int row, int col, mx_f4 f) {
-    if (col >= a.N) return;
     const int64_t at = (int64_t)row * a.N + col;
-    if ((a.N & 3) == 0) {
-        if (a.out_bf16) {
-            uint2 o;
-            o.x = mx_to_bf16(a.alpha * f[0]) | (uint32_t)mx_to_bf16(a.alpha * f[1]) << 16;
-            o.y = mx_to_bf16(a.alpha * f[2]) | (uint32_t)mx_to_bf16(a.alpha * f[3]) << 16;
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = o;
-        } else {
-            *reinterpret_cast<mx_f4*>(static_cast<float*>(a.out) + at) = f * a.alpha;
-        }
+    f *= a.alpha;
+    if (col + 4 <= a.N) {
+        if (a.out_bf16)
+            *reinterpret_cast<mx_u2_any*>(static_cast<uint16_t*>(a.out) + at) =
+                mx_u2_any{mx_bf16_pair(f[0], f[1]), mx_bf16_pair(f[2], f[3])};
+        else
+            *reinterpret_cast<mx_f4_any*>(static_cast<float*>(a.out) + at) = f;
         return;
     }
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
         if (col + v >= a.N) break;
         if (a.out_bf16)
-            static_cast<uint16_t*>(a.out)[at + v] = mx_to_bf16(a.alpha * f[v]);
+            static_cast<uint16_t*>(a.out)[at + v] = mx_to_bf16(f[v]);
         else
-            static_cast<float*>(a.out)[at + v] = a.alpha * f[v];
+            static_cast<float*>(a.out)[at + v] = f[v];
     }
 }
 
@@ -533,7 +539,7 @@ __global__ void __launch_bounds__(KS * 256, KS > 1 || BM * BN > 128 * 256 ? KS :
     // 8 (v / 4) + 4 (l / 32) + v % 4.
     constexpr int PM = BM / WM, PN = BN / WN;  // the wave's part
     const int row0 = m0 + wm * PM, col0 = n0 + wn * PN;
-    if (a.out_bf16 && (a.N & 7) == 0) {
+    if (a.out_bf16) {
         // through LDS, a wave's part each, so that whole lines are stored
         constexpr int ROW = PN * 2 + 16;  // bytes, 16 of them padding
         uint8_t* part = lds_all + wave * PM * ROW;
@@ -544,9 +550,8 @@ __global__ void __launch_bounds__(KS * 256, KS > 1 || BM * BN > 128 * 256 ? KS :
                 for (int j = 0; j < NI; ++j)
 #pragma unroll
                     for (int v = 0; v < 16; v += 4) {
-                        uint32_t o[2];
-                        o[0] = mx_to_bf16(a.alpha * acc[i][j][v]) | (uint32_t)mx_to_bf16(a.alpha * acc[i][j][v + 1]) << 16;
-                        o[1] = mx_to_bf16(a.alpha * acc[i][j][v + 2]) | (uint32_t)mx_to_bf16(a.alpha * acc[i][j][v + 3]) << 16;
+                        const uint32_t o[2] = {mx_bf16_pair(a.alpha * acc[i][j][v], a.alpha * acc[i][j][v + 1]),
+                                               mx_bf16_pair(a.alpha * acc[i][j][v + 2], a.alpha * acc[i][j][v + 3])};
                         __builtin_memcpy(__builtin_assume_aligned(part + (i * 32 + q32) * ROW + (j * 32 + 2 * v + 4 * kgl) * 2, 8), o, 8);
                     }
         }
@@ -561,12 +566,16 @@ __global__ void __launch_bounds__(KS * 256, KS > 1 || BM * BN > 128 * 256 ? KS :
             const int row = row0 + k + r;
             mx_u4 o;
             __builtin_memcpy(&o, __builtin_assume_aligned(part + (k + r) * ROW + (lane % LPR) * 16, 16), 16);
-            if (row < row_end && col < a.N) {
-                mx_u4* d = reinterpret_cast<mx_u4*>(static_cast<uint16_t*>(a.out) + (int64_t)row * a.N + col);
-                if (stream_out)
-                    __builtin_nontemporal_store(o, d);
-                else
-                    *d = o;
+            if (row >= row_end || col >= a.N) continue;
+            uint16_t* d = static_cast<uint16_t*>(a.out) + (int64_t)row * a.N + col;
+            if (col + 8 > a.N) {
+#pragma unroll
+                for (int v = 0; v < 7; ++v)
+                    if (col + v < a.N) d[v] = (uint16_t)(o[v >> 1] >> (v & 1) * 16);
+            } else if (stream_out) {
+                __builtin_nontemporal_store((mx_u4_any)o, reinterpret_cast<mx_u4_any*>(d));
+            } else {
+                *reinterpret_cast<mx_u4_any*>(d) = o;
             }
         }
     } else if (KS == 1 || team == 0) {
