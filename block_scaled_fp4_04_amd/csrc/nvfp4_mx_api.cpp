@@ -117,7 +117,7 @@ int prepare_mx_gemm(const void* a_packed, const void* a_scales, const void* x, i
 }
 
 int prepare_moe(int64_t tokens, int64_t topk, Job* job) {
-    if (tokens < 0 || tokens >= ((int64_t)1 << 24) || topk < 1 || topk > INT32_MAX ||
+    if (tokens < 0 || tokens >= ((int64_t)1 << 24) || topk < 1 || topk >= ((int64_t)1 << 24) ||
         tokens * topk > INT32_MAX)
         return NVFP4_ERR_INVALID_VALUE;
     *job = Job{};

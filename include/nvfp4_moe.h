@@ -23,8 +23,8 @@
  * tables are 4-byte aligned (int64 expert numbers: 8), else
  * NVFP4_ERR_MISALIGNED.
  *
- * Sizes: 0 <= tokens < 2^24 (0: nothing but row_offsets is written), topk >=
- * 1, tokens * topk < 2^31, 1 <= experts <= 2048, 1 <= hidden <= 2^22.
+ * Sizes: 0 <= tokens < 2^24 (0: nothing but row_offsets is written), 1 <=
+ * topk < 2^24, tokens * topk < 2^31, 1 <= experts <= 2048, 1 <= hidden <= 2^22.
  * Status codes and streams as in nvfp4.h.  No workspace, no allocation, no
  * atomics on results: calls may be captured, may run at the same time on
  * several streams, and give the same bits every time.  Slots outside

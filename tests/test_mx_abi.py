@@ -154,6 +154,16 @@ def test_moe_refusals():
         assert grad(**bad) == MIS, bad
 
 
+def test_moe_refuses_long_rows_of_choices():
+    """The kernels number a token's choices in 32 bits, some past its last one."""
+    L = nv.moe.moe_lib()
+    for k in (2 ** 24, 2 ** 31 - 1):
+        assert L.nvfp4_moe_sort(P, 0, 1, k, 8, P, P, P, None) == INV
+        assert L.nvfp4_moe_gather(P, 1, 1, k, 8, 8, P, P, None) == INV
+        assert L.nvfp4_moe_combine(P, 1, 1, k, 8, P, None, P, None) == INV
+        assert L.nvfp4_moe_combine_grad(P, 8, P, 1, 1, k, 8, P, None, P, P, None) == INV
+
+
 def test_sequence_refuses_the_same(tmp_path):
     L, ML = nv.mx.mx_lib(), nv.moe.moe_lib()
     h = ctypes.c_void_p()
