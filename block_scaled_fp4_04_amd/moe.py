@@ -66,7 +66,6 @@ class MoeRoute:
     experts: int
 
     def check(self) -> None:
-        import torch
         off, slots, tokens = self.row_offsets, self.slots, self.tokens
         if not (off.dtype is slots.dtype is tokens.dtype is torch.int32 and slots.dim() == 2
                 and off.numel() == self.experts + 1 and tokens.numel() == slots.numel()
@@ -77,6 +76,8 @@ class MoeRoute:
 def _sort_args(ids, experts, out):
     if ids.dim() != 2 or ids.dtype not in (torch.int32, torch.int64) or not ids.is_contiguous():
         raise ValueError("expert_ids must be a contiguous [tokens, topk] int32 or int64 tensor")
+    if not 1 <= experts <= MOE_MAX_EXPERTS:
+        raise ValueError(f"experts must be 1 to {MOE_MAX_EXPERTS}, not {experts}")
     T, k = ids.shape
     if out is None:
         tables = ids.new_empty(2 * T * k + experts + 1, dtype=torch.int32)
@@ -96,7 +97,7 @@ def moe_sort(expert_ids, experts: int, out: MoeRoute | None = None, stream=None)
     expert, those of one expert by token (nvfp4_moe_sort).  At most
     MOE_MAX_EXPERTS experts."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, expert_ids):
             return moe_sort(expert_ids, experts, out)
     out, args = _sort_args(expert_ids, experts, out)
     _run(moe_lib().nvfp4_moe_sort, args, (expert_ids, out.row_offsets, out.slots, out.tokens))
@@ -139,7 +140,7 @@ def moe_gather(x, route: MoeRoute, out=None, stream=None):
     hidden].  Rows that no choice owns (behind row_offsets[-1]) are left as
     they were in ``out``."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, x):
             return moe_gather(x, route, out)
     out, args = _gather_args(x, route, out)
     _run(moe_lib().nvfp4_moe_gather, args, (x, route.slots, out))
@@ -161,7 +162,7 @@ def moe_combine(y, route: MoeRoute, weights=None, out=None, stream=None):
     choice] (nvfp4_moe_combine), summed in fp32 in the order of j: [tokens,
     hidden].  ``weights``: float32 [tokens, topk]; None for ones."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, y):
             return moe_combine(y, route, weights, out)
     out, args = _combine_args(y, route, weights, out)
     _run(moe_lib().nvfp4_moe_combine, args, (y, route.slots, weights, out))
@@ -180,7 +181,7 @@ def moe_combine_grad(dout, y, route: MoeRoute, weights=None, dy=None, dweights=N
     (nvfp4_moe_combine_grad).  Rows of dy that no choice owns are left as they
     were; dweights of dropped choices are zero.  ``dy`` may be y itself."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, dout):
             return moe_combine_grad(dout, y, route, weights, dy, dweights)
     kind = _rows_2d(dout, "dout")
     route.check()

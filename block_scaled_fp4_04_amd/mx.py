@@ -188,12 +188,16 @@ def _gpu_of(tensors) -> int:
     return gpu
 
 
-def _on(stream):
-    """The context of a stream (a torch stream or a raw handle): what a call
-    allocates in it belongs to that stream."""
+def _on(stream, like):
+    """The context of a stream (a torch stream, or a raw handle of one of the
+    GPU that `like` is on): what a call allocates in it belongs to that
+    stream."""
+    gpu = _gpu_of((like,))
     if not hasattr(stream, "cuda_stream"):
-        stream = (torch.cuda.ExternalStream(int(stream)) if int(stream)
-                  else torch.cuda.default_stream())
+        stream = (torch.cuda.ExternalStream(int(stream), device=gpu) if int(stream)
+                  else torch.cuda.default_stream(gpu))
+    if stream.device_index != gpu:
+        raise ValueError(f"the stream is one of {stream.device}, the tensors are on {like.device}")
     return torch.cuda.stream(stream)
 
 
@@ -226,10 +230,13 @@ def _type_of(dtype, what: str) -> int:
 
 
 def _out(out, dtype, M: int, N: int, like):
-    """The output tensor (made beside `like`, or the given one checked) and its
-    type code."""
+    """The output tensor (made beside `like`, bfloat16 by default, or the given
+    one checked) and its type code."""
     if out is None:
+        dtype = dtype or torch.bfloat16
         return like.new_empty((M, N), dtype=dtype), _type_of(dtype, "out")
+    if dtype not in (None, out.dtype):
+        raise ValueError(f"out is of type {out.dtype}, not {dtype}")
     if tuple(out.shape) != (M, N) or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous tensor of shape ({M}, {N})")
     return out, _type_of(out.dtype, "out")
@@ -276,7 +283,7 @@ def mx_quantize(x, out=None, stream=None):
     ``out``.  K is a multiple of 32; rows and groups may be strided (by whole
     16 bytes)."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, x):
             return mx_quantize(x, out)
     out, args = _quantize_args(x, out)
     _run(mx_lib().nvfp4_mx_quantize, args, (x, out.codes, out.scales))
@@ -287,7 +294,7 @@ def mx_dequantize(a, dtype=None, out=None, stream=None):
     """The values of an MxOperand (rows x K) or MxGroups (groups x rows x K)
     as bfloat16 (default) or float32, exact in both (nvfp4_mx_dequantize)."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, a.codes):
             return mx_dequantize(a, dtype, out)
     groups = getattr(a, "groups", None)
     shape = (a.rows, a.K) if groups is None else (groups, a.rows, a.K)
@@ -317,9 +324,9 @@ def mx_gemm(a: MxOperand, b: MxOperand, alpha: float = 1.0, out=None, dtype=None
     """C = alpha * (A . B^T) of packed MXFP4 operands (nvfp4_mx_gemm): M x N,
     bfloat16 unless ``dtype`` or ``out`` says float32."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, a.codes):
             return mx_gemm(a, b, alpha, out, dtype)
-    out, args = _gemm_args(a, b, alpha, out, dtype or torch.bfloat16)
+    out, args = _gemm_args(a, b, alpha, out, dtype)
     _run(mx_lib().nvfp4_mx_gemm, args, (a.codes, a.scales, b.codes, b.scales, out))
     return out
 
@@ -340,9 +347,9 @@ def mx_gemm_quantized(x, b: MxOperand, alpha: float = 1.0, out=None, dtype=None,
     (nvfp4_mx_gemm_quantized): x holds up to MX_QUANT_ROWS rows of fp32 or
     bfloat16 activations."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, x):
             return mx_gemm_quantized(x, b, alpha, out, dtype)
-    out, args = _gemm_quantized_args(x, b, alpha, out, dtype or torch.bfloat16)
+    out, args = _gemm_quantized_args(x, b, alpha, out, dtype)
     _run(mx_lib().nvfp4_mx_gemm_quantized, args, (x, b.codes, b.scales, out))
     return out
 
@@ -352,7 +359,7 @@ def mx_linear(x, b: MxOperand, alpha: float = 1.0, out=None, dtype=None, stream=
     fp32 or bfloat16): one launch (mx_gemm_quantized) for up to MX_QUANT_ROWS
     rows, else mx_quantize and mx_gemm.  Both give the same bits."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, x):
             return mx_linear(x, b, alpha, out, dtype)
     if x.dim() == 2 and x.shape[0] <= MX_QUANT_ROWS:
         return mx_gemm_quantized(x, b, alpha, out, dtype)
@@ -386,9 +393,9 @@ def mx_grouped_gemm(a: MxOperand, b: MxGroups, row_offsets, alpha: float = 1.0, 
     activations are quantised once per token and never copied), or row r
     without ``rows``.  Rows behind the last group are left as they were."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, a.codes):
             return mx_grouped_gemm(a, b, row_offsets, alpha, rows, out, dtype)
-    out, args = _grouped_args(a, b, row_offsets, alpha, rows, out, dtype or torch.bfloat16)
+    out, args = _grouped_args(a, b, row_offsets, alpha, rows, out, dtype)
     _run(mx_lib().nvfp4_mx_grouped_gemm, args,
          (a.codes, a.scales, b.codes, b.scales, row_offsets, rows, out))
     return out

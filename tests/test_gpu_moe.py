@@ -239,6 +239,45 @@ def test_other_streams_and_shared_tables():
     assert all(torch.equal(o, want) for o in got)
 
 
+@pytest.mark.parametrize("T,k,E", [(9000, 2, 40), (3000, 7, 2048)])
+def test_a_long_sort_replayed(T, k, E):
+    """Three launches, the histograms in row_tokens: every replay starts from what the last one left there."""
+    g = rng(13)
+    ids = torch.empty(T, k, dtype=torch.int32, device=DEV)
+    ids.copy_(torch.from_numpy(choices(g, T, k, E, 0.1)))
+    r = nv.moe_sort(ids, E)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        nv.moe_sort(ids, E, out=r)
+    for _ in range(3):
+        new = choices(g, T, k, E, 0.2)
+        ids.copy_(torch.from_numpy(new))
+        want = nv.moe_sort(ids, E)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in ((r.row_offsets, want.row_offsets), (r.slots, want.slots), (r.tokens, want.tokens)):
+            assert torch.equal(a, b)
+        check_sort(new, E)
+
+
+def test_raw_stream_handles():
+    g = rng(14)
+    x = torch.randn(40, 128, device=DEV)
+    ids = torch.from_numpy(choices(g, 40, 3, 6, 0.0)).to(DEV)
+    s = torch.cuda.Stream()
+    want = nv.mx_quantize(x)
+    torch.cuda.synchronize()
+    for handle in (0, s.cuda_stream, s):
+        q = nv.mx_quantize(x, stream=handle)
+        r = nv.moe_sort(ids, 6, stream=handle)
+        y = nv.moe_gather(x, r, stream=handle)
+        torch.cuda.synchronize()
+        assert torch.equal(q.codes, want.codes) and torch.equal(q.scales, want.scales)
+        assert torch.equal(y, x[r.tokens.long()])
+
+
 def test_malformed_slots_stay_inside():
     ids, r, make, w = case(16, 2, 4, 32, "fp32", drop=0.0)
     bad = nv.MoeRoute(r.row_offsets, torch.full_like(r.slots, 1 << 30), r.tokens, 4)

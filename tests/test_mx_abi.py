@@ -211,11 +211,20 @@ def test_binding_refuses():
         nv.mx_gemm(a, a, dtype=torch.float16)
     with pytest.raises(ValueError):
         nv.mx_dequantize(a, torch.float16)
+    with pytest.raises(ValueError, match="float32"):
+        nv.mx_gemm(a, a, out=torch.zeros(4, 4, dtype=torch.bfloat16), dtype=torch.float32)
+    for experts in (-9, 0, 2049):
+        with pytest.raises(ValueError, match="experts"):
+            nv.moe_sort(torch.zeros(0, 2, dtype=torch.int32), experts)
     w = nv.MxGroups(torch.zeros(2048, **u8), torch.zeros(512, **u8), 2, 4, 64)
     with pytest.raises(ValueError, match="row_offsets"):
         nv.mx_grouped_gemm(a, w, torch.zeros(4, dtype=torch.int32))
     with pytest.raises(ValueError, match="rows"):
         nv.mx_grouped_gemm(a, w, torch.zeros(3, dtype=torch.int32), rows=torch.zeros(4))
+    for f in (lambda: nv.mx_quantize(x, stream=0), lambda: nv.mx_gemm(a, a, stream=7),
+              lambda: nv.moe_sort(torch.zeros(4, 2, dtype=torch.int32), 8, stream=0)):
+        with pytest.raises(ValueError, match="GPU"):
+            f()
     i32 = dict(dtype=torch.int32)
     r = nv.MoeRoute(torch.zeros(9, **i32), torch.zeros(4, 2, **i32), torch.zeros(8, **i32), 8)
     with pytest.raises(ValueError):
