@@ -295,7 +295,9 @@ __global__ void __launch_bounds__(KS * 256, KS > 1 || BM * BN > 128 * 256 ? KS :
             rows_of(g, r0, r1);
             cnt += (r1 - r0 + BM - 1) / BM;
         }
-        const int mine = (int)min(cnt, (int64_t)1 << 22);  // (M < 2^28: no more in a sound one)
+        // (M < 2^28 and groups < 2^30: at most 2^22 full ones and 2^22 broken
+        // ones in a sound table; the sum over a wave stays below 2^31)
+        const int mine = (int)min(cnt, (int64_t)1 << 24);
         int incl = mine;
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
