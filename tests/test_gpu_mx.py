@@ -261,6 +261,9 @@ def grouped_reference(va, vb, offsets, rows, alpha, out_eps):
     ([40, 3] * 120, 100, 96, 1),                # the same, narrow: 128 x 128
     ([130, 400] * 40, 290, 224, 4),             # many larger ones: 128 x 256
     ([0, 0, 0], 32, 64, 4),                     # nothing but a tail
+    ([150, 0, 200, 110] * 30, 200, 160, 3),     # about a hundred rows each
+    ([130, 200, 97, 0, 223] * 13, 520, 3232, 1),  # and deep
+    ([66, 47, 80, 130] * 30, 515, 416, 2),      # fewer
 ])
 @pytest.mark.parametrize("indirect", [False, True])
 def test_grouped(sizes, N, K, tail, indirect):
