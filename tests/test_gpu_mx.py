@@ -327,6 +327,42 @@ def test_operands_past_32_bits():
     assert torch.equal(nv.mx_dequantize(q, x.dtype)[-16:], nv.mx_dequantize(tail, x.dtype))
 
 
+@pytest.mark.parametrize("K", [131071 * 128, 131073 * 128 - 96])
+def test_very_deep_products(K):
+    """The deepest operands of the tile kernel's 32-bit offsets, and deeper ones: zeros but for a few blocks,
+    whose products are small integers, so that sums are exact in any order."""
+    M, N = 80, 72
+    say(f"deep K={K}")
+    g = torch.Generator(device=DEV)
+    g.manual_seed(14)
+    at = [0, 4096, K // 2 // 32 * 32, K - 4128, K - 32]
+
+    def rows(n):
+        x = torch.zeros(n, K, dtype=torch.bfloat16, device=DEV)
+        parts = [torch.randint(-2, 3, (n, 32), device=DEV, generator=g) for _ in at]
+        for k, p in zip(at, parts):
+            x[:, k:k + 32] = p.to(torch.bfloat16)
+        return nv.mx_quantize(x), torch.cat(parts, 1).double().cpu()
+
+    (A, va), (B, vb) = rows(M), rows(N)
+    assert torch.equal(nv.mx_gemm(A, B, dtype=torch.float32).double().cpu(), va @ vb.T)
+    W = nv.MxGroups(B.codes, B.scales, 1, N, K)
+    off = torch.tensor([3, 75], dtype=torch.int32, device=DEV)
+    out = torch.zeros(M, N, device=DEV)
+    nv.mx_grouped_gemm(A, W, off, out=out)
+    assert torch.equal(out[3:75].double().cpu(), (va @ vb.T)[3:75]) and (out[:3] == 0).all() and (out[75:] == 0).all()
+
+
+@pytest.mark.parametrize("N", [33_000, 33_001])
+def test_result_of_more_than_2_31_elements(N):
+    M, K = 66_000, 32
+    a, b, va, vb = operands(15, M, N, K)
+    A, B = nv.mx_to_device(*a), nv.mx_to_device(*b)
+    c = nv.mx_gemm(A, B)
+    for r in (0, 65_072, M - 16):                 # (behind row 65072: more than 2^31 elements)
+        check(c[r:r + 16], va[r:r + 16], vb, 1.0)
+
+
 def test_grouped_malformed_tables_stay_inside():
     """Offsets and row numbers out of range are clamped: rows may be wrong,
     the memory behind the output is untouched."""
