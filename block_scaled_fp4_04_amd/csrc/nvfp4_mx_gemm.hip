@@ -238,7 +238,8 @@ __global__ void __launch_bounds__(KS * 256, KS > 1 || BM * BN > 128 * 256 ? KS :
     constexpr int WN = 4 / WM;                            // waves along M and N
     constexpr int MI = BM / 32 / WM, NI = BN / 32 / WN;   // 32 x 32 blocks of a wave
     constexpr int AF = BM / 16, BF = BN / 16;             // fragments of a step
-    constexpr int CPW = (AF + BF) / 4;                    // of them, a wave's loads
+    constexpr int APW = AF / 4, BPW = BF / 4;             // of them, a wave's loads: first A's, then B's
+    constexpr int CPW = APW + BPW;
     constexpr int SPW = CPW;                              // a wave's scale loads, every fourth step
     constexpr int STAGE = (AF + BF) * kMxFrag;
     constexpr int SCALES = (AF + BF) * kMxScaleFrag;      // of four steps
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(KS * 256, KS > 1 || BM * BN > 128 * 256 ? KS :
         for (int d = 1; d <= many; ++d) n += ((k - d) & 3) == 0 ? SPW : 0;
         return n;
     };
-    static_assert((AF + BF) % 4 == 0 && NS >= 2 && (NS + 1) * CPW + NQ * SPW < 64, "ring");
+    static_assert(AF % 4 == 0 && BF % 4 == 0 && NS >= 2 && (NS + 1) * CPW + NQ * SPW < 64, "ring");
     constexpr int RING = NS * STAGE + NQ * SCALES;
     static_assert(BM * WN * (BN / WN * 2 + 16) <= RING, "the output is staged in the first ring");
     static_assert((KS - 1) * BM * BN * 4 <= KS * RING, "and partial tiles in all");
@@ -362,17 +363,17 @@ __global__ void __launch_bounds__(KS * 256, KS > 1 || BM * BN > 128 * 256 ? KS :
         return (uint32_t)(a.a_rows ? min(max(a.a_rows[r], 0), a.A_rows - 1) : r);
     };
 
-    // A wave's loads: number i is fragment wave * CPW + i of a step's codes, or
-    // of a scale word.  Where they come from in the operands' memory, per lane:
+    // A wave's loads: number i < APW is fragment wave * APW + i of A's part of a
+    // step's codes, or of a scale word, and the others are BPW of B's.  Where
+    // they come from in the operands' memory, per lane:
     uint32_t code_at[CPW], scale_at[SPW];
 #pragma unroll
     for (int i = 0; i < CPW; ++i) {
-        const int f = wave * CPW + i;
-        const uint32_t k = (uint32_t)(f < AF ? f : f - AF);
+        const uint32_t k = (uint32_t)(i < APW ? wave * APW + i : wave * BPW + i - APW);
         code_at[i] = k * (uint32_t)C * kMxFrag + lane * 16;
         scale_at[i] = k * (uint32_t)Q * kMxScaleFrag + lane * 4;
-        if (GROUPED && f < AF) {
-            const uint32_t r = a_row(f);
+        if (GROUPED && i < APW) {
+            const uint32_t r = a_row((int)k);
             code_at[i] = (r >> 4) * (uint32_t)C * kMxFrag + mx_code_at(r & 15, (lane & 3) ^ (lane >> 4));
             scale_at[i] = (r >> 4) * (uint32_t)Q * kMxScaleFrag + mx_scale_at(r & 15, lane & 3);
         }
@@ -385,14 +386,22 @@ __global__ void __launch_bounds__(KS * 256, KS > 1 || BM * BN > 128 * 256 ? KS :
     // word q.
     auto load_code = [&](auto I, int c, int stage) {
         constexpr int i = I.value;
-        mx_dma<16, i * kMxFrag>(wave * CPW + i < AF ? rac : rbc, code_at[i], (uint32_t)min(c0 + c, C - 1) * kMxFrag,
-                                lds0 + (uint32_t)(stage * STAGE + wave * CPW * kMxFrag));
+        const uint32_t from = (uint32_t)min(c0 + c, C - 1) * kMxFrag;
+        if constexpr (i < APW)
+            mx_dma<16, i * kMxFrag>(rac, code_at[i], from, lds0 + (uint32_t)(stage * STAGE + wave * APW * kMxFrag));
+        else
+            mx_dma<16, (AF + i - APW) * kMxFrag>(rbc, code_at[i], from,
+                                                 lds0 + (uint32_t)(stage * STAGE + wave * BPW * kMxFrag));
     };
     auto load_scale = [&](auto I, int q, int place) {
         constexpr int i = I.value;
-        mx_dma<4, NS * STAGE + i * kMxScaleFrag>(wave * CPW + i < AF ? ras : rbs, scale_at[i],
-                                                 (uint32_t)min(q0 + q, Q - 1) * kMxScaleFrag,
-                                                 lds0 + (uint32_t)(place * SCALES + wave * CPW * kMxScaleFrag));
+        const uint32_t from = (uint32_t)min(q0 + q, Q - 1) * kMxScaleFrag;
+        if constexpr (i < APW)
+            mx_dma<4, NS * STAGE + i * kMxScaleFrag>(ras, scale_at[i], from,
+                                                     lds0 + (uint32_t)(place * SCALES + wave * APW * kMxScaleFrag));
+        else
+            mx_dma<4, NS * STAGE + (AF + i - APW) * kMxScaleFrag>(
+                rbs, scale_at[i], from, lds0 + (uint32_t)(place * SCALES + wave * BPW * kMxScaleFrag));
     };
 
     mx_f16 acc[MI][NI];
