@@ -35,76 +35,68 @@ __device__ __forceinline__ float mx_scale(uint32_t byte) {
     return __builtin_bit_cast(float, byte << 23);
 }
 
-// 32 values -> 16 bytes of codes and the scale byte.  The conversion divides
-// by the scale exactly (a power of two), rounds to the nearest E2M1 value,
-// ties to the even code, and saturates at 6.
-__device__ __forceinline__ uint32_t mx_quant_block(const float (&v)[32], mx_u4& w) {
+// Two bfloat16 values of a word.  (By value: a bit cast of a vector's element
+// in place takes the vector's first one.)
+__device__ __forceinline__ mx_b2 mx_pair(uint32_t w) { return __builtin_bit_cast(mx_b2, w); }
+
+// The largest magnitude, as fp32 bits, of 16 bytes of values: 4 fp32, or 8
+// bfloat16 (element 2i in the low half of word i).  Magnitudes order like
+// their bits, so two bfloat16 are compared at once with the packed 16-bit
+// maximum.
+template <typename T>
+__device__ __forceinline__ uint32_t mx_top(const mx_u4& v) {
+    if constexpr (sizeof(T) == 2) {
+        typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+        u16x2 m = {0, 0};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, v[j] & 0x7FFF7FFFu));
+        return (uint32_t)(m[0] > m[1] ? m[0] : m[1]) << 16;
+    } else {
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = max(top, v[j] & 0x7FFFFFFFu);
+        return top;
+    }
+}
+// The codes of the same values under scale s: a word from bfloat16 ones, half
+// HALF of word c from fp32 ones.  The conversion divides by the scale exactly
+// (a power of two), rounds to the nearest E2M1 value, ties to the even code,
+// and saturates at 6; from bfloat16 it equals the one from fp32.
+template <typename T, int HALF>
+__device__ __forceinline__ uint32_t mx_codes(uint32_t c, const mx_u4& v, float s) {
+    if constexpr (sizeof(T) == 2) {
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, mx_pair(v[0]), s, 0);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, mx_pair(v[1]), s, 1);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, mx_pair(v[2]), s, 2);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, mx_pair(v[3]), s, 3);
+    } else {
+        const mx_f4 f = __builtin_bit_cast(mx_f4, v);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[0], f[1], s, 2 * HALF);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[2], f[3], s, 2 * HALF + 1);
+    }
+    return c;
+}
+
+// A whole block in one lane: the 32 values at p (16-byte aligned) -> 16 bytes
+// of codes and the scale byte.
+template <typename T>
+__device__ __forceinline__ uint32_t mx_quant_load(const T* p, mx_u4& w) {
+    constexpr int L = kMxBlock * (int)sizeof(T) / 16, PER = L / 4;  // loads; of them, to a word of codes
+    mx_u4 v[L];
+#pragma unroll
+    for (int i = 0; i < L; ++i) v[i] = reinterpret_cast<const mx_u4*>(p)[i];
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        const uint32_t b = __builtin_bit_cast(uint32_t, v[i]) & 0x7FFFFFFFu;
-        top = top > b ? top : b;
-    }
+    for (int i = 0; i < L; ++i) top = max(top, mx_top<T>(v[i]));
     const uint32_t byte = mx_scale_byte(top);
     const float s = mx_scale(byte);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        uint32_t c = 0;
-        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[8 * j + 0], v[8 * j + 1], s, 0);
-        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[8 * j + 2], v[8 * j + 3], s, 1);
-        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[8 * j + 4], v[8 * j + 5], s, 2);
-        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[8 * j + 6], v[8 * j + 7], s, 3);
+        uint32_t c = mx_codes<T, 0>(0, v[PER * j], s);
+        if constexpr (PER == 2) c = mx_codes<T, 1>(c, v[PER * j + 1], s);
         w[j] = byte == 255u ? 0u : c;
     }
     return byte;
-}
-// Two bfloat16 values of a word.  (By value: a bit cast of a vector's element
-// in place takes the vector's first one.)
-__device__ __forceinline__ mx_b2 mx_pair(uint32_t w) { return __builtin_bit_cast(mx_b2, w); }
-// The same from 32 bfloat16 values (element 2i in the low half of word i).
-// Magnitudes order like their 15 bits, so two are compared at once with the
-// packed 16-bit maximum; the bfloat16 conversion equals the fp32 one.
-__device__ __forceinline__ uint32_t mx_quant_block(const mx_u4 (&q)[4], mx_u4& w) {
-    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
-    u16x2 m = {0, 0};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, q[i][j] & 0x7FFF7FFFu));
-    const uint32_t top = (uint32_t)(m[0] > m[1] ? m[0] : m[1]) << 16;
-    const uint32_t byte = mx_scale_byte(top);
-    const float s = mx_scale(byte);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t c = 0;
-        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, mx_pair(q[i][0]), s, 0);
-        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, mx_pair(q[i][1]), s, 1);
-        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, mx_pair(q[i][2]), s, 2);
-        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, mx_pair(q[i][3]), s, 3);
-        w[i] = byte == 255u ? 0u : c;
-    }
-    return byte;
-}
-
-// The 32 values of a lane's block at p (16-byte aligned), quantised.
-template <typename T>
-__device__ __forceinline__ uint32_t mx_quant_load(const T* p, mx_u4& w) {
-    if constexpr (sizeof(T) == 2) {
-        mx_u4 q[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) q[i] = reinterpret_cast<const mx_u4*>(p)[i];
-        return mx_quant_block(q, w);
-    } else {
-        float v[32];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const mx_f4 t = reinterpret_cast<const mx_f4*>(p)[i];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[4 * i + j] = t[j];
-        }
-        return mx_quant_block(v, w);
-    }
 }
 
 __device__ __forceinline__ mx_v8i mx_operand(const mx_u4& w) {
