@@ -18,13 +18,16 @@ namespace nvfp4 {
 namespace {
 
 // dma16 / dma4 (nvfp4_device.h) with the LDS address as a uniform base plus a
-// constant: one scalar instruction a load.
+// constant: one scalar instruction a load.  NT: with the non-temporal hint.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
-template <int BYTES, int AT>
+template <int BYTES, int AT, bool NT = false>
 __device__ __forceinline__ void mx_dma(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff,
                                        uint32_t lds) {
-    if constexpr (BYTES == 16)
+    if constexpr (BYTES == 16 && NT)
+        asm volatile("s_add_u32 m0, %3, %4\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds"
+                     :: "v"(voff), "s"(r), "s"(soff), "s"(lds), "n"(AT) : "memory", "m0", "scc");
+    else if constexpr (BYTES == 16)
         asm volatile("s_add_u32 m0, %3, %4\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
                      :: "v"(voff), "s"(r), "s"(soff), "s"(lds), "n"(AT) : "memory", "m0", "scc");
     else
@@ -276,6 +279,7 @@ __global__ void __launch_bounds__(KS * 256, KS > 1 || BM * BN > 128 * 256 ? KS :
         return k < per + (x < more) ? x * per + min(x, more) + k : -1;
     };
     int tn, m0, row_end = a.M;
+    bool stream = false;
     int64_t b_first;  // first row block of this tile's B
     if constexpr (GROUPED) {
         // Row blocks are numbered in group order, ceil(rows / BM) to a group;
@@ -324,6 +328,7 @@ __global__ void __launch_bounds__(KS * 256, KS > 1 || BM * BN > 128 * 256 ? KS :
                     sch[NW] = g;
                     sch[NW + 1] = r0 + (int)at * BM;
                     sch[NW + 2] = r1;
+                    sch[NW + 3] = n;
                     break;
                 }
                 at -= n;
@@ -333,6 +338,8 @@ __global__ void __launch_bounds__(KS * 256, KS > 1 || BM * BN > 128 * 256 ? KS :
         m0 = __builtin_amdgcn_readfirstlane(sch[NW + 1]);
         row_end = __builtin_amdgcn_readfirstlane(sch[NW + 2]);
         b_first = (int64_t)g * a.RBb + (int64_t)tn * BF;
+        stream = __builtin_amdgcn_readfirstlane(sch[NW + 3]) == 1 &&
+                 (int64_t)a.groups * a.RBb * (C * kMxFrag + Q * kMxScaleFrag) > kStreamBytes;
         __syncthreads();  // everyone has read before the ring fills
     } else {
         constexpr int GROUP_M = 8;
@@ -384,14 +391,14 @@ __global__ void __launch_bounds__(KS * 256, KS > 1 || BM * BN > 128 * 256 ? KS :
     const int steps = KS > 1 ? min(4 * (int)((int64_t)Q * (team + 1) / KS), C) - c0 : C;
     // Load number I of the team's step c into buffer `stage`, and of its scale
     // word q.
-    auto load_code = [&](auto I, int c, int stage) {
+    auto load_code = [&](auto I, auto NT, int c, int stage) {
         constexpr int i = I.value;
         const uint32_t from = (uint32_t)min(c0 + c, C - 1) * kMxFrag;
         if constexpr (i < APW)
             mx_dma<16, i * kMxFrag>(rac, code_at[i], from, lds0 + (uint32_t)(stage * STAGE + wave * APW * kMxFrag));
         else
-            mx_dma<16, (AF + i - APW) * kMxFrag>(rbc, code_at[i], from,
-                                                 lds0 + (uint32_t)(stage * STAGE + wave * BPW * kMxFrag));
+            mx_dma<16, (AF + i - APW) * kMxFrag, NT.value>(rbc, code_at[i], from,
+                                                           lds0 + (uint32_t)(stage * STAGE + wave * BPW * kMxFrag));
     };
     auto load_scale = [&](auto I, int q, int place) {
         constexpr int i = I.value;
@@ -453,70 +460,80 @@ __global__ void __launch_bounds__(KS * 256, KS > 1 || BM * BN > 128 * 256 ? KS :
         acc[i][j] = mx_mfma32<S.value>(h.b[j], sc.b[j][half], h.a[i], sc.a[i][half], acc[i][j]);
     };
 
-    // fill the ring
-    mx_each<NQ>([&](auto q) {
-        if constexpr (q.value < NQ - NS / 4) mx_each<SPW>([&](auto I) { load_scale(I, q.value, q.value); });
-    });
-    mx_each<NS>([&](auto c) {
-        mx_each<CPW>([&](auto I) { load_code(I, c.value, c.value); });
-        // (as if at step c - NS)
-        constexpr int q = (c.value - NS) / 4 + NQ;
-        if constexpr ((c.value - NS) % 4 == 0) mx_each<SPW>([&](auto I) { load_scale(I, q, q); });
-    });
-    wait_vmcnt<(NS - 1) * CPW + scale_loads(0, NS - 1)>();  // step 0 and the first scale word
-    wg_barrier();
-    Half h0, h1;
-    mx_each<P>([&](auto I) { read_scale(I, sc, 0); });
-    mx_each<P>([&](auto I) { read(I, h0, 0, 0); });
-
-    // One step.  The order is fixed (the scheduling barriers): behind each
-    // MFMA one LDS read and its share of the loads, which issue while the
-    // MFMA runs; left to itself the compiler moves the reads to their uses
-    // and the MFMAs wait for each.
-    int c = 0, stage = 0, place = 0;
-    auto step = [&](auto S) {
-        constexpr int s = S.value;
-        mx_each<MM>([&](auto N) {
-            mfma(N, S, h0, 0);
-            mx_each<P>([&](auto I) { if constexpr (slot_of(I.value) == N.value) read(I, h1, stage, 1); });
-            __builtin_amdgcn_sched_barrier(0);
+    auto pipeline = [&](auto NT) {
+        // fill the ring
+        mx_each<NQ>([&](auto q) {
+            if constexpr (q.value < NQ - NS / 4) mx_each<SPW>([&](auto I) { load_scale(I, q.value, q.value); });
         });
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        // step c + 1 has landed: what may be in flight was issued in the last
-        // NS - 2 steps
-        wait_vmcnt<(NS - 2) * CPW + scale_loads(s, NS - 2)>();
+        mx_each<NS>([&](auto c) {
+            mx_each<CPW>([&](auto I) { load_code(I, NT, c.value, c.value); });
+            // (as if at step c - NS)
+            constexpr int q = (c.value - NS) / 4 + NQ;
+            if constexpr ((c.value - NS) % 4 == 0) mx_each<SPW>([&](auto I) { load_scale(I, q, q); });
+        });
+        wait_vmcnt<(NS - 1) * CPW + scale_loads(0, NS - 1)>();  // step 0 and the first scale word
         wg_barrier();
-        __builtin_amdgcn_sched_barrier(0);
-        const int freed = stage;
-        stage = stage + 1 == NS ? 0 : stage + 1;
-        mx_each<MM>([&](auto N) {
-            constexpr int n = N.value;
-            mfma(N, S, h1, 1);
-            mx_each<P>([&](auto I) {
-                if constexpr (slot_of(I.value) == n) read(I, h0, stage, 0);
-                if constexpr (s == 3 && MM - 1 - slot_of(I.value) == n) read_scale(I, sn, NQ > 1 ? (place + 1) % NQ : 0);
+        Half h0, h1;
+        mx_each<P>([&](auto I) { read_scale(I, sc, 0); });
+        mx_each<P>([&](auto I) { read(I, h0, 0, 0); });
+
+        // One step.  The order is fixed (the scheduling barriers): behind each
+        // MFMA one LDS read and its share of the loads, which issue while the
+        // MFMA runs; left to itself the compiler moves the reads to their uses
+        // and the MFMAs wait for each.
+        int c = 0, stage = 0, place = 0;
+        auto step = [&](auto S) {
+            constexpr int s = S.value;
+            mx_each<MM>([&](auto N) {
+                mfma(N, S, h0, 0);
+                mx_each<P>([&](auto I) { if constexpr (slot_of(I.value) == N.value) read(I, h1, stage, 1); });
+                __builtin_amdgcn_sched_barrier(0);
             });
-            mx_each<(n + 1) * CPW / MM - n * CPW / MM>([&](auto I) {
-                constexpr int i = n * CPW / MM + I.value;
-                load_code(std::integral_constant<int, i>{}, c + NS, freed);
-                if constexpr (s == 0) load_scale(std::integral_constant<int, i>{}, c / 4 + NQ, place);
-            });
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            // step c + 1 has landed: what may be in flight was issued in the last
+            // NS - 2 steps
+            wait_vmcnt<(NS - 2) * CPW + scale_loads(s, NS - 2)>();
+            wg_barrier();
             __builtin_amdgcn_sched_barrier(0);
-        });
-        if constexpr (s == 3) {
-            sc = sn;
-            if constexpr (NQ > 1) place = (place + 1) % NQ;
+            const int freed = stage;
+            stage = stage + 1 == NS ? 0 : stage + 1;
+            mx_each<MM>([&](auto N) {
+                constexpr int n = N.value;
+                mfma(N, S, h1, 1);
+                mx_each<P>([&](auto I) {
+                    if constexpr (slot_of(I.value) == n) read(I, h0, stage, 0);
+                    if constexpr (s == 3 && MM - 1 - slot_of(I.value) == n) read_scale(I, sn, NQ > 1 ? (place + 1) % NQ : 0);
+                });
+                mx_each<(n + 1) * CPW / MM - n * CPW / MM>([&](auto I) {
+                    constexpr int i = n * CPW / MM + I.value;
+                    load_code(std::integral_constant<int, i>{}, NT, c + NS, freed);
+                    if constexpr (s == 0) load_scale(std::integral_constant<int, i>{}, c / 4 + NQ, place);
+                });
+                __builtin_amdgcn_sched_barrier(0);
+            });
+            if constexpr (s == 3) {
+                sc = sn;
+                if constexpr (NQ > 1) place = (place + 1) % NQ;
+            }
+            ++c;
+        };
+        // whole scale words, then the steps that are left (one loop exit: the
+        // accumulators stay where they are)
+        for (int q = steps / 4; q > 0; --q) mx_each<4>(step);
+        if (steps & 3) {
+            step(std::integral_constant<int, 0>{});
+            if ((steps & 3) > 1) step(std::integral_constant<int, 1>{});
+            if ((steps & 3) > 2) step(std::integral_constant<int, 2>{});
         }
-        ++c;
     };
-    // whole scale words, then the steps that are left (one loop exit: the
-    // accumulators stay where they are)
-    for (int q = steps / 4; q > 0; --q) mx_each<4>(step);
-    if (steps & 3) {
-        step(std::integral_constant<int, 0>{});
-        if ((steps & 3) > 1) step(std::integral_constant<int, 1>{});
-        if ((steps & 3) > 2) step(std::integral_constant<int, 2>{});
-    }
+    // A group of one row block reads its weights once: non-temporally, if
+    // those of all groups outgrow the last-level cache (256 experts x 256
+    // columns, 16 rows: 42.5 -> 38.6 us; groups of several row blocks share theirs
+    // in the L2, which keeps such loads for less long: 128 rows 76 -> 80 us).
+    if (GROUPED && stream)
+        pipeline(std::bool_constant<GROUPED>{});
+    else
+        pipeline(std::false_type{});
     // a team with fewer steps than another meets it at the barriers that are left
     if constexpr (KS > 1)
         for (int k = 4 * ((Q + KS - 1) / KS) - steps; k > 0; --k) wg_barrier();
@@ -677,7 +694,7 @@ void choose(Launch& l) {
         if (M >= 128 * G && (tiles(128, 256) >= 256 || weights >= 32 << 20))
             return run_tile<128, 256, 3, 2, 1, true>(l);
         // 64 x 256 tiles stream the weights of small groups at the memory's
-        // rate (256 experts x 256 columns, 16 rows: 44 us, 49 with 128 x 128);
+        // rate (256 experts x 256 columns, 16 rows: 39 us, 49 with 128 x 128);
         // narrow weights would leave them half empty.
         if (N <= 128) return run_tile<128, 128, 4, 2, 1, true>(l);
         return run_tile<64, 256, 3, 1, 1, true>(l);
