@@ -99,6 +99,8 @@ __device__ __forceinline__ void mx_store4(const MxGemmArgs& a, int row, int col,
 // group's B and walks the group's rows.  Offsets are clamped to [0, M] and row
 // numbers to A's rows, so a malformed table gives wrong rows but no access
 // outside the buffers.
+//
+// NT: B loaded non-temporally.
 // ---------------------------------------------------------------------------
 enum { A_PACKED = 0, A_F32 = 1, A_BF16 = 2 };
 
@@ -108,7 +110,7 @@ __device__ __forceinline__ void mx_wave_fence() {
     __builtin_amdgcn_wave_barrier();
 }
 
-template <int MI, int AT, bool GROUPED>
+template <int MI, int AT, bool GROUPED, bool NT>
 __global__ void __launch_bounds__(1024) mx_skinny_kernel(MxGemmArgs a) {
     constexpr int W = 16;
     static_assert(AT == A_PACKED || MI == 1, "quantised rows: one row block");
@@ -152,7 +154,7 @@ __global__ void __launch_bounds__(1024) mx_skinny_kernel(MxGemmArgs a) {
             const int n = min(4, C - 4 * q);  // steps of this word
             const __amdgpu_buffer_rsrc_t rb = make_rsrc(bc + (int64_t)q * 4 * kMxFrag, (uint32_t)n * kMxFrag);
             mx_each<4>([&](auto S) {
-                if (S.value < n) mx_dma<16, S.value * kMxFrag>(rb, lane * 16, S.value * kMxFrag, b_base);
+                if (S.value < n) mx_dma<16, S.value * kMxFrag, NT>(rb, lane * 16, S.value * kMxFrag, b_base);
             });
             const uint32_t sb = *reinterpret_cast<const uint32_t*>(bs + (int64_t)q * kMxScaleFrag + at_scale);
             mx_u4 wa[4][MI];
@@ -634,13 +636,13 @@ struct Launch {
     hipError_t error;
 };
 
-template <int MI, int AT, bool GROUPED>
+template <int MI, int AT, bool GROUPED, bool NT = false>
 void run_skinny(Launch& l) {
     const MxGemmArgs& a = l.a;
     const int64_t tiles = (GROUPED ? a.groups : (a.M + 16 * MI - 1) / (16 * MI)) * (int64_t)a.RBb;
     l.items = tiles * 1024;
     if (l.dry) return;
-    hipLaunchKernelGGL((mx_skinny_kernel<MI, AT, GROUPED>), dim3((unsigned)tiles), dim3(1024), 0, l.stream, a);
+    hipLaunchKernelGGL((mx_skinny_kernel<MI, AT, GROUPED, NT>), dim3((unsigned)tiles), dim3(1024), 0, l.stream, a);
     l.error = hipGetLastError();
 }
 
@@ -702,7 +704,12 @@ void choose(Launch& l) {
     if (!a.a_codes) return a.x_bf16 ? run_skinny<1, A_BF16, false>(l) : run_skinny<1, A_F32, false>(l);
     // Up to 16 rows always the kernel that quantises too: the same bits (1 x
     // 768: 3.5 us, 7.3 with 64 x 64 tiles; 16 x 6144: 7.1 and 8.4).
-    if (M <= kMxQuantRows) return run_skinny<1, A_PACKED, false>(l);
+    if (M <= kMxQuantRows) {
+        // (weights beyond the last-level cache: 1 x 131072 x 8192 93 -> 87 us, 16
+        // rows 103 -> 98)
+        const int64_t weights = a.RBb * ((int64_t)a.C * kMxFrag + (a.C + 3) / 4 * kMxScaleFrag);
+        return weights > kStreamBytes ? run_skinny<1, A_PACKED, false, true>(l) : run_skinny<1, A_PACKED, false>(l);
+    }
     // Up to 64 rows while its workgroups fit the GPU at once (64 x 768: 5.3
     // against 7.4 us; 64 x 6144: 14.0 against 8.8).
     if ((M <= 64 && (M + 31) / 32 * a.RBb <= 256) || a.C > kMxTileSteps) return run_skinny<2, A_PACKED, false>(l);

@@ -356,12 +356,16 @@ def mx_gemm_quantized(x, b: MxOperand, alpha: float = 1.0, out=None, dtype=None,
 
 def mx_linear(x, b: MxOperand, alpha: float = 1.0, out=None, dtype=None, stream=None):
     """C = alpha * (quantise(x) . B^T) for plain activations x (rows x K,
-    fp32 or bfloat16): one launch (mx_gemm_quantized) for up to MX_QUANT_ROWS
-    rows, else mx_quantize and mx_gemm.  Both give the same bits."""
+    fp32 or bfloat16): one launch (mx_gemm_quantized) for few rows, else
+    mx_quantize and mx_gemm.  Both give the same bits."""
     if stream is not None:
         with _on(stream, x):
             return mx_linear(x, b, alpha, out, dtype)
-    if x.dim() == 2 and x.shape[0] <= MX_QUANT_ROWS:
+    # In one launch every 16 columns quantise the rows again: that takes about
+    # N K (6 + rows) / 2e8 us more than the product, where a launch of its own takes
+    # 2.7 us and the call another 8 (1 x 16384 x 8192: 18.0 us and 13.5 + 2.7; 16 x
+    # 65536 x 8192: 119 and 59 + 2.7).
+    if x.dim() == 2 and x.shape[0] <= MX_QUANT_ROWS and b.rows * b.K * (6 + x.shape[0]) <= 800_000_000:
         return mx_gemm_quantized(x, b, alpha, out, dtype)
     return mx_gemm(mx_quantize(x), b, alpha, out, dtype)
 

@@ -211,6 +211,27 @@ def test_gemm_quantized_is_the_two_calls(M, N, K, dtype):
     check(two, va, mx_ref.values(*b), 0.5)
 
 
+def test_linear_wide():
+    """A few rows by so many columns that they are quantised once, in a launch of their own."""
+    g = rng(16)
+    x = torch.from_numpy(g.standard_normal((3, 2080)).astype(np.float32)).to(DEV)
+    b = mx_ref.random_operand(g, 50_000, 2080)
+    B = nv.mx_to_device(*b)
+    c = nv.mx_linear(x, B)
+    check(c, mx_ref.values(*mx_ref.quantize(host(x))), mx_ref.values(*b), 1.0)
+    assert torch.equal(c, nv.mx_gemm_quantized(x, B))
+    K, N = 8192, 49_200                           # weights beyond the last-level cache
+    W = nv.mx_quantize(torch.randn(N, K, device=DEV, dtype=torch.bfloat16))
+    for M in (1, 16):
+        x = torch.randn(M, K, device=DEV)
+        c = nv.mx_linear(x, W)
+        assert torch.equal(c, nv.mx_gemm_quantized(x, W))
+        c1, s1 = nv.mx_packed_size(16, K)
+        for at in (0, N // 16 - 1):               # the first and the last 16 columns by themselves
+            part = nv.MxOperand(W.codes[at * c1:(at + 1) * c1], W.scales[at * s1:(at + 1) * s1], 16, K)
+            assert torch.equal(c[:, at * 16:at * 16 + 16], nv.mx_linear(x, part))
+
+
 def test_linear_many_rows_and_none():
     g = rng(6)
     x = torch.from_numpy(g.standard_normal((150, 416)).astype(np.float32)).to(DEV)
