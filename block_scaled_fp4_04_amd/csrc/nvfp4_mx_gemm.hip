@@ -713,13 +713,23 @@ void choose(Launch& l) {
     // Up to 64 rows while its workgroups fit the GPU at once (64 x 768: 5.3
     // against 7.4 us; 64 x 6144: 14.0 against 8.8).
     if ((M <= 64 && (M + 31) / 32 * a.RBb <= 256) || a.C > kMxTileSteps) return run_skinny<2, A_PACKED, false>(l);
-    // 2048 x 6144 (192 tiles of 256 x 256): 43 us with these, 43 with 128 x 128;
-    // 8192 x 2048 (256): 51 and 55; 1024 x 6144 (96): 37 and 26.
-    if (tiles(256, 256) >= 192) return run_tile<256, 256, 4, 2, 1, false>(l);
-    // 1237 x 2056 (170 tiles of 128 x 128): 15.2 us with these, 18.0 with 64 x
-    // 64; 256 x 4096 x 4096 (64): 10.7 and 7.8; 200 x 8192 x 512 (128): 5.3 and 4.6.
-    if (tiles(128, 128) >= 150) return run_tile<128, 128, 4, 2, 1, false>(l);
-    run_small_tiles<false>(l);
+    // The smallest tiles that one round of the 256 CUs holds (256 x 4096 x 4096,
+    // 256 tiles of 64 x 64: 7.9 us, 9.6 with 64 x 128; 400 x 4096 x 4096, 224 of
+    // 64 x 128: 9.0, 10.3 with 64 x 64, 10.6 with 128 x 128).
+    if (tiles(64, 64) <= 256) return run_small_tiles<false>(l);
+    if (tiles(64, 128) <= 256) return run_tile<64, 128, 4, 2, 1, false>(l);
+    // 256 x 256 for large sizes that are deep or many (4096 x 4096 x 8192: 63 us,
+    // 64 with 128 x 256; 8192 x 8192 x 4096: 148 and 150; but 4096 x 8192 x 4096:
+    // 71 and 67), unless they would be half empty (128 x 65536 x 8192: 71, 61 with
+    // 128 x 128).
+    const int64_t large = tiles(256, 256);
+    if (M > 128 && large >= 256 && (a.C > 32 || large >= 1024)) return run_tile<256, 256, 4, 2, 1, false>(l);
+    // 128 x 256, two to a CU, unless a few of them need a second round (256 x
+    // 32768 x 8192, 256 tiles: 44 us, 49 with 128 x 128; 2048 x 6144 x 6144, 384: 44
+    // and 46; 3000 x 3000 x 6144, 288: 39 and 37; 1237 x 2056 x 6112, 90: 21 and 15).
+    const int64_t wide = tiles(128, 256);
+    if (wide >= 360 || (wide >= 180 && wide <= 256)) return run_tile<128, 256, 3, 2, 1, false>(l);
+    run_tile<128, 128, 4, 2, 1, false>(l);
 }
 
 }  // namespace

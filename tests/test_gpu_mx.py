@@ -173,6 +173,25 @@ def test_gemm(M, N, K, dtype):
     assert (out[M * N:] == 3).all()
 
 
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("M,N,K", [
+    (421, 2503, 416), (130, 8190, 4128),        # one round of 64 x 128 tiles
+    (1301, 2601, 416), (330, 6144, 672),        # 128 x 128
+    (1303, 4701, 288), (3007, 4101, 160),       # 128 x 256
+    (4011, 4051, 4192), (8201, 7950, 96)])      # 256 x 256: deep, or many
+def test_gemm_large(M, N, K, dtype):
+    """The first and the last rows of large products."""
+    say(f"gemm {M}x{N}x{K} {dtype}")
+    a, b, va, vb = operands(17, M, N, K)
+    out = torch.full((M * N + 64,), 3.0, dtype=DT[dtype], device=DEV)
+    c = out[:M * N].view(M, N)
+    nv.mx_gemm(nv.mx_to_device(*a), nv.mx_to_device(*b), 0.5, out=c)
+    w = min(M, 140)
+    check(c[:w], va[:w], vb, 0.5)
+    check(c[M - w:], va[M - w:], vb, 0.5)
+    assert not torch.isnan(c).any() and (out[M * N:] == 3).all()
+
+
 def test_gemm_nan_blocks_and_extreme_scales():
     """A NaN block reaches its own row (or column) and nothing else; products
     of the largest and smallest scales stay within fp32's rules."""
