@@ -92,7 +92,10 @@ __device__ __forceinline__ void mx_store4(const MxGemmArgs& a, int row, int col,
 // rows of sixteen blocks at a time, a block to a lane, and hands the codes
 // to the lanes that multiply them through LDS.  (With a lane quantising the
 // four blocks that it multiplies, one row cost as much as sixteen: 5.0 us
-// at 1 x 768 x 6144, where packed operands take 3.7.)
+// at 1 x 768 x 6144, where packed operands take 3.7.)  A workgroup then walks
+// the row blocks of B that its turn comes to: with one scale word to a wave (K
+// up to 8192) the rows are quantised once and the next row block is loaded
+// while the sums of this one are added.
 //
 // GROUPED (operands past the tile kernel's 32-bit offsets): group g owns rows
 // offsets[g] .. offsets[g+1]-1 of C; a workgroup takes one row block of one
@@ -121,20 +124,35 @@ __global__ void __launch_bounds__(1024) mx_skinny_kernel(MxGemmArgs a) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r16 = lane & 15, kg = lane >> 4;
     const int C = a.C, Q = (C + 3) / 4;
-    const int cb = (int)(blockIdx.x % (unsigned)a.RBb);  // row block of B
-    const int tm = (int)(blockIdx.x / (unsigned)a.RBb);  // row tile, or group
+    const int cb0 = (int)(blockIdx.x % (unsigned)a.RBb);  // (first) row block of B
+    const int tm = (int)(blockIdx.x / (unsigned)a.RBb);   // row tile, or group
+    const int turn = AT == A_PACKED ? a.RBb : (int)gridDim.x;
+    const bool once = AT != A_PACKED && Q <= W;
     int r0 = tm * 16 * MI, r1 = min(r0 + 16 * MI, a.M);
-    int64_t brow = cb;
+    int64_t b_first = 0;
     if constexpr (GROUPED) {
         r0 = min(max(a.offsets[tm], 0), a.M);
         r1 = min(max(a.offsets[tm + 1], r0), a.M);
-        brow += (int64_t)tm * a.RBb;
+        b_first = (int64_t)tm * a.RBb;
     }
-    const uint8_t* bc = a.b_codes + brow * C * kMxFrag;
-    const uint8_t* bs = a.b_scales + brow * Q * kMxScaleFrag;
     const int at_code = mx_code_at(r16, kg), at_scale = mx_scale_at(r16, kg);
     const uint32_t b_base = lds_addr(b_lds[wave]);
+    // Loads scale word q of row block cb of B: the codes to LDS, the lane's
+    // scales returned.
+    auto load_b = [&](int cb, int q) {
+        const int n = min(4, C - 4 * q);  // steps of this word
+        const uint8_t* bc = a.b_codes + (b_first + cb) * C * kMxFrag;
+        const __amdgpu_buffer_rsrc_t rb = make_rsrc(bc + (int64_t)q * 4 * kMxFrag, (uint32_t)n * kMxFrag);
+        mx_each<4>([&](auto S) {
+            if (S.value < n) mx_dma<16, S.value * kMxFrag, NT>(rb, lane * 16, S.value * kMxFrag, b_base);
+        });
+        const uint8_t* bs = a.b_scales + (b_first + cb) * Q * kMxScaleFrag;
+        return *reinterpret_cast<const uint32_t*>(bs + (int64_t)q * kMxScaleFrag + at_scale);
+    };
+    bool first = true, loaded = false;
+    uint32_t sb = 0;
 
+    for (int cb = cb0; cb < a.RBb; cb += turn)
     for (int m0 = r0; m0 < r1; m0 += 16 * MI) {
         const uint8_t *ac[MI], *as[MI];  // this lane's block of its row, at step 0
         bool live[MI];
@@ -152,11 +170,8 @@ __global__ void __launch_bounds__(1024) mx_skinny_kernel(MxGemmArgs a) {
 
         for (int q = wave; q < Q; q += W) {
             const int n = min(4, C - 4 * q);  // steps of this word
-            const __amdgpu_buffer_rsrc_t rb = make_rsrc(bc + (int64_t)q * 4 * kMxFrag, (uint32_t)n * kMxFrag);
-            mx_each<4>([&](auto S) {
-                if (S.value < n) mx_dma<16, S.value * kMxFrag, NT>(rb, lane * 16, S.value * kMxFrag, b_base);
-            });
-            const uint32_t sb = *reinterpret_cast<const uint32_t*>(bs + (int64_t)q * kMxScaleFrag + at_scale);
+            if (!loaded) sb = load_b(cb, q);
+            loaded = false;
             mx_u4 wa[4][MI];
             uint32_t sa[MI];
             if constexpr (AT == A_PACKED) {
@@ -176,7 +191,7 @@ __global__ void __launch_bounds__(1024) mx_skinny_kernel(MxGemmArgs a) {
                 using T = std::conditional_t<AT == A_F32, float, uint16_t>;
                 const int s = (lane & 15) >> 2, b = lane & 3;  // the lane's block
                 const int k = (4 * q + s) * kMxStep + b * kMxBlock;
-                for (int p = 0; p < r1 - m0; p += 4) {
+                for (int p = 0; p < r1 - m0 && !(once && cb != cb0); p += 4) {
                     const int row = p + (lane >> 4);
                     if (m0 + row < r1) {
                         mx_u4 w = {0, 0, 0, 0};
@@ -204,9 +219,14 @@ __global__ void __launch_bounds__(1024) mx_skinny_kernel(MxGemmArgs a) {
             });
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // LDS is read before it is filled again
             mx_wave_fence();
+            if (once && cb + turn < a.RBb) {
+                sb = load_b(cb + turn, q);
+                loaded = true;
+            }
         }
 
-        if (m0 != r0) __syncthreads();  // the previous rows' sums are read
+        if (!first) __syncthreads();  // the previous sums are read
+        first = false;
 #pragma unroll
         for (int i = 0; i < MI; ++i) red[wave][i][lane] = acc[i];
         __syncthreads();
@@ -639,7 +659,10 @@ struct Launch {
 template <int MI, int AT, bool GROUPED, bool NT = false>
 void run_skinny(Launch& l) {
     const MxGemmArgs& a = l.a;
-    const int64_t tiles = (GROUPED ? a.groups : (a.M + 16 * MI - 1) / (16 * MI)) * (int64_t)a.RBb;
+    // (with activations to quantise a workgroup takes most of a CU's LDS, and the
+    // GPU has 256)
+    const int64_t tiles = AT == A_PACKED ? (GROUPED ? a.groups : (a.M + 16 * MI - 1) / (16 * MI)) * (int64_t)a.RBb
+                                         : std::min(a.RBb, 256);
     l.items = tiles * 1024;
     if (l.dry) return;
     hipLaunchKernelGGL((mx_skinny_kernel<MI, AT, GROUPED, NT>), dim3((unsigned)tiles), dim3(1024), 0, l.stream, a);
@@ -701,13 +724,16 @@ void choose(Launch& l) {
         if (N <= 128) return run_tile<128, 128, 4, 2, 1, true>(l);
         return run_tile<64, 256, 3, 1, 1, true>(l);
     }
-    if (!a.a_codes) return a.x_bf16 ? run_skinny<1, A_BF16, false>(l) : run_skinny<1, A_F32, false>(l);
+    const int64_t weights = a.RBb * ((int64_t)a.C * kMxFrag + (a.C + 3) / 4 * kMxScaleFrag);
+    if (!a.a_codes) {  // (1 x 131072 x 8192: 103 -> 89 us with the weights non-temporal)
+        if (weights > kStreamBytes) return a.x_bf16 ? run_skinny<1, A_BF16, false, true>(l) : run_skinny<1, A_F32, false, true>(l);
+        return a.x_bf16 ? run_skinny<1, A_BF16, false>(l) : run_skinny<1, A_F32, false>(l);
+    }
     // Up to 16 rows always the kernel that quantises too: the same bits (1 x
     // 768: 3.5 us, 7.3 with 64 x 64 tiles; 16 x 6144: 7.1 and 8.4).
     if (M <= kMxQuantRows) {
         // (weights beyond the last-level cache: 1 x 131072 x 8192 93 -> 87 us, 16
         // rows 103 -> 98)
-        const int64_t weights = a.RBb * ((int64_t)a.C * kMxFrag + (a.C + 3) / 4 * kMxScaleFrag);
         return weights > kStreamBytes ? run_skinny<1, A_PACKED, false, true>(l) : run_skinny<1, A_PACKED, false>(l);
     }
     // Up to 64 rows while its workgroups fit the GPU at once (64 x 768: 5.3

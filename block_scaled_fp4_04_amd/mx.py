@@ -361,11 +361,12 @@ def mx_linear(x, b: MxOperand, alpha: float = 1.0, out=None, dtype=None, stream=
     if stream is not None:
         with _on(stream, x):
             return mx_linear(x, b, alpha, out, dtype)
-    # In one launch every 16 columns quantise the rows again: that takes about
-    # N K (6 + rows) / 2e8 us more than the product, where a launch of its own takes
-    # 2.7 us and the call another 8 (1 x 16384 x 8192: 18.0 us and 13.5 + 2.7; 16 x
-    # 65536 x 8192: 119 and 59 + 2.7).
-    if x.dim() == 2 and x.shape[0] <= MX_QUANT_ROWS and b.rows * b.K * (6 + x.shape[0]) <= 800_000_000:
+    # (one launch: 16 x 65536 x 8192 52 us, 57 + 2.7 in two; 1 x 6144 x 6144 6.9, 6.4
+    # + 2.7.  Behind K = 8192 every 16 columns quantise the rows again, which takes
+    # about N K (6 + rows) / 2e8 us: worth it up to the 2.7 us and part of the
+    # other call's 8.)
+    if x.dim() == 2 and x.shape[0] <= MX_QUANT_ROWS and (
+            b.K <= 8192 or b.rows * b.K * (6 + x.shape[0]) <= 800_000_000):
         return mx_gemm_quantized(x, b, alpha, out, dtype)
     return mx_gemm(mx_quantize(x), b, alpha, out, dtype)
 

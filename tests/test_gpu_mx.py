@@ -231,8 +231,16 @@ def test_gemm_quantized_is_the_two_calls(M, N, K, dtype):
 
 
 def test_linear_wide():
-    """A few rows by so many columns that they are quantised once, in a launch of their own."""
+    """A few rows by so many columns that a workgroup takes several blocks of them, up to K = 8192 with the rows
+    quantised once; behind that they may take a launch of their own."""
     g = rng(16)
+    for M, N, K in ((3, 50_000, 2080), (16, 8300, 6112), (5, 4130, 8224), (2, 9000, 16416)):
+        x = torch.from_numpy(g.standard_normal((M, K)).astype(np.float32)).to(DEV)
+        b = mx_ref.random_operand(g, N, K)
+        B = nv.mx_to_device(*b)
+        c = nv.mx_gemm_quantized(x, B)
+        check(c, mx_ref.values(*mx_ref.quantize(host(x))), mx_ref.values(*b), 1.0)
+        assert torch.equal(c, nv.mx_linear(x, B)) and torch.equal(c, nv.mx_gemm(nv.mx_quantize(x), B))
     x = torch.from_numpy(g.standard_normal((3, 2080)).astype(np.float32)).to(DEV)
     b = mx_ref.random_operand(g, 50_000, 2080)
     B = nv.mx_to_device(*b)
