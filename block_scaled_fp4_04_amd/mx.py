@@ -156,6 +156,13 @@ class MxGroups:
         _check_packed(name, self.codes, self.scales, self.groups, self.rows, self.K)
 
 
+def _kind(x, name: str, *kinds) -> None:
+    """Refuses an operand of another class: groups, and the operands of the
+    other format, have the same fields."""
+    if not isinstance(x, kinds):
+        raise ValueError(f"{name} must be {' or '.join(k.__name__ for k in kinds)}, not {type(x).__name__}")
+
+
 def mx_to_device(codes: np.ndarray, scales: np.ndarray, device="cuda") -> MxOperand:
     """Pack canonical host arrays and copy them to ``device``."""
     rows, K = _check_canonical(codes, scales)
@@ -268,7 +275,8 @@ def _quantize_args(x, out):
         scales = x.new_empty(sb * groups, dtype=torch.uint8)
         out = MxGroups(codes, scales, groups, rows, K) if grouped else MxOperand(codes, scales, rows, K)
     else:
-        if (out.rows, out.K, getattr(out, "groups", None)) != (rows, K, groups if grouped else None):
+        _kind(out, "out", MxGroups if grouped else MxOperand)
+        if (out.rows, out.K) != (rows, K) or grouped and out.groups != groups:
             raise ValueError("out has the wrong shape")
         out.check("out")
         codes, scales = out.codes, out.scales
@@ -293,6 +301,7 @@ def mx_quantize(x, out=None, stream=None):
 def mx_dequantize(a, dtype=None, out=None, stream=None):
     """The values of an MxOperand (rows x K) or MxGroups (groups x rows x K)
     as bfloat16 (default) or float32, exact in both (nvfp4_mx_dequantize)."""
+    _kind(a, "a", MxOperand, MxGroups)
     if stream is not None:
         with _on(stream, a.codes):
             return mx_dequantize(a, dtype, out)
@@ -311,6 +320,8 @@ def mx_dequantize(a, dtype=None, out=None, stream=None):
 
 
 def _gemm_args(a, b, alpha, out, dtype):
+    _kind(a, "a", MxOperand)
+    _kind(b, "b", MxOperand)
     if a.K != b.K:
         raise ValueError(f"K dimension mismatch: A has K={a.K}, B has K={b.K}")
     a.check("a")
@@ -332,6 +343,7 @@ def mx_gemm(a: MxOperand, b: MxOperand, alpha: float = 1.0, out=None, dtype=None
 
 
 def _gemm_quantized_args(x, b, alpha, out, dtype):
+    _kind(b, "b", MxOperand)
     kind = _rows_2d(x)
     M, K = x.shape
     if K != b.K:
@@ -357,10 +369,19 @@ def mx_gemm_quantized(x, b: MxOperand, alpha: float = 1.0, out=None, dtype=None,
 def mx_linear(x, b: MxOperand, alpha: float = 1.0, out=None, dtype=None, stream=None):
     """C = alpha * (quantise(x) . B^T) for plain activations x (rows x K,
     fp32 or bfloat16): one launch (mx_gemm_quantized) for few rows, else
-    mx_quantize and mx_gemm.  Both give the same bits."""
+    mx_quantize and mx_gemm.  Both give the same bits.  Dimensions in front of
+    K (batch x sequence x K) are rows, and C has them in front of N; an x whose
+    rows do not follow each other at one stride is copied first."""
     if stream is not None:
         with _on(stream, x):
             return mx_linear(x, b, alpha, out, dtype)
+    _kind(b, "b", MxOperand)
+    if x.dim() > 2:
+        shape = (*x.shape[:-1], b.rows)
+        if out is not None and (tuple(out.shape) != shape or not out.is_contiguous()):
+            raise ValueError(f"out must be a contiguous tensor of shape {shape}")
+        c = mx_linear(x.flatten(0, -2), b, alpha, None if out is None else out.flatten(0, -2), dtype)
+        return c.view(shape) if out is None else out
     # (one launch: 16 x 65536 x 8192 52 us, 57 + 2.7 in two; 1 x 6144 x 6144 6.9, 6.4
     # + 2.7.  Behind K = 8192 every 16 columns quantise the rows again, which takes
     # about N K (6 + rows) / 2e8 us: worth it up to the 2.7 us and part of the
@@ -372,6 +393,8 @@ def mx_linear(x, b: MxOperand, alpha: float = 1.0, out=None, dtype=None, stream=
 
 
 def _grouped_args(a, b, row_offsets, alpha, rows, out, dtype):
+    _kind(a, "a", MxOperand)
+    _kind(b, "b", MxGroups)
     if a.K != b.K:
         raise ValueError(f"K dimension mismatch: A has K={a.K}, B has K={b.K}")
     if (row_offsets.dtype != torch.int32 or row_offsets.numel() != b.groups + 1

@@ -482,3 +482,28 @@ def test_sequence():
         torch.cuda.synchronize()
         assert torch.equal(c1, want) and torch.equal(c2, want) and torch.equal(c3, want3)
     seq.close()
+
+
+@pytest.mark.parametrize("lead", [(2, 3), (3, 1, 4), (5, 40)])
+@pytest.mark.parametrize("dtype", list(DT))
+def test_linear_with_leading_dimensions(lead, dtype):
+    """Activations [batch, sequence, K]: every batch, few rows and many, strided rows and ones that need a copy."""
+    g = rng(21, *lead)
+    n = int(np.prod(lead))
+    B = nv.mx_to_device(*mx_ref.random_operand(g, 72, 160))
+    wide = torch.from_numpy(g.standard_normal((*lead, 168)).astype(np.float32)).to(DT[dtype]).to(DEV)
+    x = wide[..., :160]
+    want = nv.mx_linear(x.reshape(n, 160), B, 0.5)
+    vb = mx_ref.values(*nv.mx_unpack(B.codes.cpu().numpy(), B.scales.cpu().numpy(), 72, 160))
+    check(want, mx_ref.values(*mx_ref.quantize(host(x).reshape(n, 160))), vb, 0.5)
+    want = want.view(*lead, 72)
+    assert torch.equal(nv.mx_linear(x, B, 0.5), want)
+    turned = x.transpose(0, 1).contiguous().transpose(0, 1)      # the same rows at two strides
+    out = torch.empty_like(want)
+    assert nv.mx_linear(turned, B, 0.5, out=out) is out and torch.equal(out, want)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    other = nv.mx_linear(turned, B, 0.5, stream=s)
+    s.synchronize()
+    assert torch.equal(other, want)
+    assert nv.mx_linear(x[:0], B).shape == (0, *lead[1:], 72)

@@ -237,3 +237,66 @@ def test_binding_refuses():
         nv.moe_gather(x, nv.MoeRoute(r.row_offsets, r.slots, r.tokens.long(), 8))
     with pytest.raises(ValueError):
         nv.moe_combine_grad(x, torch.zeros(8, 64), r)
+
+
+def test_binding_refuses_operands_of_another_class():
+    """Groups where one operand is meant (all but the first would be dropped) and the other way round, and operands
+    of the 16-element format, whose buffers have other sizes."""
+    u8 = dict(dtype=torch.uint8)
+    a = nv.MxOperand(torch.zeros(1024, **u8), torch.zeros(256, **u8), 4, 64)
+    w = nv.MxGroups(torch.zeros(3072, **u8), torch.zeros(768, **u8), 3, 4, 64)
+    one = nv.MxGroups(a.codes, a.scales, 1, 4, 64)
+    cb, sb = nv.packed_size(4, 64)
+    p = nv.PackedOperand(torch.zeros(cb, **u8), torch.zeros(sb, **u8), 4, 64)
+    pw = nv.PackedGroups(torch.zeros(3 * cb, **u8), torch.zeros(3 * sb, **u8), 3, 4, 64)
+    x, off = torch.zeros(4, 64), torch.zeros(4, dtype=torch.int32)
+    out = torch.zeros(4, 4, dtype=torch.bfloat16)
+    seq = nv.Sequence()
+    for bad in (w, one, p, pw):
+        for f in (lambda: nv.mx_gemm(bad, a), lambda: nv.mx_gemm(a, bad), lambda: nv.mx_gemm_quantized(x, bad),
+                  lambda: nv.mx_linear(x, bad), lambda: nv.mx_linear(x.repeat(9, 1), bad),
+                  lambda: nv.mx_linear(x[None], bad), lambda: nv.mx_grouped_gemm(bad, w, off),
+                  lambda: nv.mx_quantize(x, out=bad), lambda: seq.add_mx_gemm(bad, a, out),
+                  lambda: seq.add_mx_gemm(a, bad, out), lambda: seq.add_mx_gemm_quantized(x, bad, out),
+                  lambda: seq.add_mx_grouped_gemm(bad, w, off, out), lambda: seq.add_mx_quantize(x, bad)):
+            with pytest.raises(ValueError, match="must be MxOperand"):
+                f()
+    for bad in (a, p, pw):
+        for f in (lambda: nv.mx_grouped_gemm(a, bad, off), lambda: seq.add_mx_grouped_gemm(a, bad, off, out),
+                  lambda: nv.mx_quantize(x.expand(3, 4, 64), out=bad)):
+            with pytest.raises(ValueError, match="must be MxGroups"):
+                f()
+    for bad in (p, pw):
+        with pytest.raises(ValueError, match="MxOperand or MxGroups"):
+            nv.mx_dequantize(bad)
+    assert seq.calls == 0
+
+
+def test_linear_takes_leading_dimensions(monkeypatch):
+    """Every row of a batch reaches the product (the calls' arguments, without a GPU)."""
+    calls = []
+    monkeypatch.setattr(nv.mx, "_run", lambda fn, args, tensors: calls.append((fn.__name__, args)))
+    u8 = dict(dtype=torch.uint8)
+    b = nv.MxOperand(torch.zeros(1024, **u8), torch.zeros(256, **u8), 7, 64)
+    for lead in ((2, 3), (4, 100), (1, 1), (3, 1, 5), (0, 4), (2, 0)):
+        rows = int(np.prod(lead))
+        out = torch.empty(*lead, 7, dtype=torch.bfloat16)
+        for given in (None, out):
+            calls.clear()
+            c = nv.mx_linear(torch.zeros(*lead, 64), b, out=given)
+            assert c.shape == (*lead, 7) and (given is None or c is given)
+            name, args = calls[-1]
+            assert name == ("nvfp4_mx_gemm_quantized" if rows <= 16 else "nvfp4_mx_gemm")
+            assert args[-3:] == (rows, 7, 64)
+            assert rows <= 16 or calls[0][1][2:6] == (1, 0, rows, 64)   # one group of all the rows is quantised
+            assert given is None or rows == 0 or out.data_ptr() in args
+    x = torch.zeros(2, 5, 72)[:, :, :64]                  # rows of a wider buffer: one stride, no copy
+    nv.mx_linear(x, b)
+    assert calls[-1][1][0] == x.data_ptr() and calls[-1][1][2] == 72
+    for bad in (torch.empty(10, 7), torch.empty(2, 5, 8), torch.empty(2, 7, 5).transpose(1, 2)):
+        with pytest.raises(ValueError, match="out"):
+            nv.mx_linear(x, b, out=bad)
+    with pytest.raises(ValueError):
+        nv.mx_linear(torch.zeros(64), b)
+    with pytest.raises(ValueError, match="mismatch"):
+        nv.mx_linear(torch.zeros(2, 5, 96), b)
