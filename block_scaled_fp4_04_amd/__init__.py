@@ -320,6 +320,14 @@ class PackedOperand:
                 raise ValueError(f"{name}{what} must be a contiguous uint8 tensor of {need} bytes")
 
 
+def _check_operand(x, name: str) -> None:
+    """x.check(name), behind a refusal of MXFP4 operands: they have the same
+    fields, but buffers of other sizes."""
+    if getattr(x, "block", 16) != 16:
+        raise ValueError(f"{name} must hold blocks of 16 elements, not the {x.block} of {type(x).__name__}")
+    x.check(name)
+
+
 def to_device(codes: np.ndarray, scales: np.ndarray, device="cuda") -> PackedOperand:
     """Pack canonical host arrays and copy them to ``device``."""
     import torch
@@ -350,8 +358,8 @@ def gemm(a: PackedOperand, b: PackedOperand, alpha: float = 1.0, out=None,
         out = torch.empty((M, N), dtype=torch.bfloat16, device=a.codes.device)
     elif out.dtype != torch.bfloat16 or tuple(out.shape) != (M, N) or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous bfloat16 tensor of shape ({M}, {N})")
-    a.check("a")
-    b.check("b")
+    _check_operand(a, "a")
+    _check_operand(b, "b")
     st = lib().nvfp4_gemm_with_plan(a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(),
                                     b.scales.data_ptr(), float(alpha), out.data_ptr(), M, N, K,
                                     int(path), int(tile), int(split_k), _stream_handle(stream))
@@ -374,8 +382,8 @@ def gemm_noalloc(a: PackedOperand, b: PackedOperand, alpha: float = 1.0, out=Non
         out = torch.empty((M, N), dtype=torch.bfloat16, device=a.codes.device)
     elif out.dtype != torch.bfloat16 or tuple(out.shape) != (M, N) or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous bfloat16 tensor of shape ({M}, {N})")
-    a.check("a")
-    b.check("b")
+    _check_operand(a, "a")
+    _check_operand(b, "b")
     st = lib().nvfp4_gemm_noalloc(a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(),
                                   b.scales.data_ptr(), float(alpha), out.data_ptr(), M, N, K,
                                   _stream_handle(stream))
@@ -473,8 +481,8 @@ def grouped_gemm(a: PackedOperand, b: PackedGroups, row_offsets, alpha: float = 
         out = torch.empty((M, N), dtype=torch.bfloat16, device=a.codes.device)
     elif out.dtype != torch.bfloat16 or tuple(out.shape) != (M, N) or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous bfloat16 tensor of shape ({M}, {N})")
-    a.check("a")
-    b.check("b")
+    _check_operand(a, "a")
+    _check_operand(b, "b")
     st = lib().nvfp4_grouped_gemm_with_plan(a.codes.data_ptr(), a.scales.data_ptr(),
                                             b.codes.data_ptr(), b.scales.data_ptr(),
                                             row_offsets.data_ptr(), b.groups, float(alpha),
@@ -509,7 +517,7 @@ def quantize(x, out: PackedOperand | None = None, stream=None) -> PackedOperand:
                             torch.empty(sb, dtype=torch.uint8, device=x.device), rows, K)
     elif out.rows != rows or out.K != K:
         raise ValueError("out has the wrong shape")
-    out.check("out")
+    _check_operand(out, "out")
     st = getattr(lib(), fn)(x.data_ptr(), rows, K, x.stride(0), out.codes.data_ptr(),
                             out.scales.data_ptr(), _stream_handle(stream))
     if st:
@@ -531,7 +539,7 @@ def _activation_rows(x, b: PackedOperand, out):
         out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
     elif out.dtype != torch.bfloat16 or tuple(out.shape) != (M, N) or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous bfloat16 tensor of shape ({M}, {N})")
-    b.check("b")
+    _check_operand(b, "b")
     return (INPUT_F32 if x.dtype == torch.float32 else INPUT_BF16), M, N, out
 
 
@@ -614,8 +622,8 @@ class Sequence:
         M, N = a.rows, b.rows
         if out.dtype != torch.bfloat16 or tuple(out.shape) != (M, N) or not out.is_contiguous():
             raise ValueError(f"out must be a contiguous bfloat16 tensor of shape ({M}, {N})")
-        a.check("a")
-        b.check("b")
+        _check_operand(a, "a")
+        _check_operand(b, "b")
         self._keep += [a, b, out]
         self._check(lib().nvfp4_sequence_add_gemm(
             self._h, a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(),
@@ -640,8 +648,8 @@ class Sequence:
             raise ValueError(f"row_offsets must be an int32 tensor of {b.groups + 1} entries")
         if out.dtype != torch.bfloat16 or tuple(out.shape) != (M, N) or not out.is_contiguous():
             raise ValueError(f"out must be a contiguous bfloat16 tensor of shape ({M}, {N})")
-        a.check("a")
-        b.check("b")
+        _check_operand(a, "a")
+        _check_operand(b, "b")
         self._keep += [a, b, row_offsets, out]
         self._check(lib().nvfp4_sequence_add_grouped_gemm(
             self._h, a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(),
@@ -654,7 +662,7 @@ class Sequence:
         rows, K = x.shape
         if out.rows != rows or out.K != K:
             raise ValueError("out has the wrong shape")
-        out.check("out")
+        _check_operand(out, "out")
         self._keep += [x, out]
         self._check(getattr(lib(), fn)(
             self._h, x.data_ptr(), rows, K, x.stride(0), out.codes.data_ptr(),

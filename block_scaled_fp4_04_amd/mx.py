@@ -133,6 +133,7 @@ class MxOperand:
     """One MXFP4 operand in the packed layout, resident on a device.
     ``codes``/``scales`` are uint8 torch tensors; ``rows`` x ``K`` is the
     logical shape."""
+    block = MX_BLOCK  # elements that share a scale (not a field)
     codes: "object"
     scales: "object"
     rows: int
@@ -146,6 +147,7 @@ class MxOperand:
 class MxGroups:
     """The weight operands of a grouped product, each ``rows`` x ``K``, packed
     and concatenated, resident on a device."""
+    block = MX_BLOCK  # elements that share a scale (not a field)
     codes: "object"
     scales: "object"
     groups: int

@@ -300,3 +300,26 @@ def test_linear_takes_leading_dimensions(monkeypatch):
         nv.mx_linear(torch.zeros(64), b)
     with pytest.raises(ValueError, match="mismatch"):
         nv.mx_linear(torch.zeros(2, 5, 96), b)
+
+
+def test_16_element_calls_refuse_mx_operands():
+    """Their scale buffers are half as large: the kernels would read and write past them."""
+    u8 = dict(dtype=torch.uint8)
+    a = nv.MxOperand(torch.zeros(1024, **u8), torch.zeros(256, **u8), 4, 64)
+    w = nv.MxGroups(torch.zeros(3072, **u8), torch.zeros(768, **u8), 3, 4, 64)
+    cb, sb = nv.packed_size(4, 64)
+    p = nv.PackedOperand(torch.zeros(cb, **u8), torch.zeros(sb, **u8), 4, 64)
+    pw = nv.PackedGroups(torch.zeros(3 * cb, **u8), torch.zeros(3 * sb, **u8), 3, 4, 64)
+    x, off = torch.zeros(4, 64), torch.zeros(4, dtype=torch.int32)
+    out = torch.zeros(4, 4, dtype=torch.bfloat16)
+    seq = nv.Sequence()
+    for f in (lambda: nv.gemm(a, p, stream=0), lambda: nv.gemm(p, a, stream=0), lambda: nv.gemm(p, w, stream=0),
+              lambda: nv.gemm_noalloc(a, p, stream=0), lambda: nv.gemm_noalloc(p, a, stream=0),
+              lambda: nv.gemm_quantized(x, a, stream=0), lambda: nv.grouped_gemm(a, pw, off, stream=0),
+              lambda: nv.grouped_gemm(p, w, off, stream=0), lambda: nv.quantize(x, out=a, stream=0),
+              lambda: seq.add_gemm(a, p, out), lambda: seq.add_gemm(p, a, out),
+              lambda: seq.add_gemm_quantized(x, a, 1.0, out), lambda: seq.add_grouped_gemm(a, pw, off, out),
+              lambda: seq.add_grouped_gemm(p, w, off, out), lambda: seq.add_quantize(x, a)):
+        with pytest.raises(ValueError, match="blocks of 16"):
+            f()
+    assert seq.calls == 0 and repr(a).count("block") == 0
