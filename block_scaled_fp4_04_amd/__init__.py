@@ -18,6 +18,7 @@ Reasoning").
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import warnings
@@ -599,7 +600,11 @@ class Sequence:
     """A recorded sequence of NVFP4 calls replayed with one graph launch
     (nvfp4_sequence_*): record with the add_* methods (fixed buffers; the
     plans are chosen then), ``finalize()`` once, then ``launch()`` per step.
-    The tensors passed in are kept referenced for the sequence's lifetime."""
+    The tensors passed in are kept referenced for the sequence's lifetime.
+
+    The MXFP4 and routing calls of a sequence lie on one GPU; finalize and
+    launch run there, as those calls do by themselves (without any of them: on
+    the current GPU)."""
 
     def __init__(self):
         h = _vp()
@@ -608,6 +613,7 @@ class Sequence:
             raise Nvfp4Error(st, "nvfp4_sequence_create")
         self._h = h
         self._keep = []
+        self._gpu = None
         self.calls = 0
 
     def _check(self, st, what):
@@ -668,9 +674,23 @@ class Sequence:
             self._h, x.data_ptr(), rows, K, x.stride(0), out.codes.data_ptr(),
             out.scales.data_ptr()), f"{fn}(rows={rows}, K={K})")
 
-    def _record(self, fn, args: tuple, keep: list) -> None:
+    def _record(self, fn, args: tuple, tensors: tuple, keep: list) -> None:
+        from . import mx
+        gpu = mx._gpu_of(tensors)
+        if self._gpu not in (None, gpu):
+            raise ValueError(f"the sequence's tensors are on GPU {self._gpu}, those of this call on GPU {gpu}")
         self._keep += keep
         self._check(fn(self._h, *args), fn.__name__)
+        self._gpu = gpu
+
+    def _on_gpu(self):
+        """The context of the GPU that the recorded tensors lie on."""
+        if self._gpu is None:
+            return contextlib.nullcontext()
+        from . import mx
+        if self._gpu == mx._current_gpu():
+            return contextlib.nullcontext()
+        return mx.torch.cuda.device(self._gpu)
 
     def add_mx_quantize(self, x, out: "MxOperand") -> None:
         """Records mx_quantize(x, out) for a 2-D x."""
@@ -678,61 +698,61 @@ class Sequence:
         if x.dim() != 2:
             raise ValueError("x must be a 2-D tensor")
         out, a = mx._quantize_args(x, out)
-        mx._gpu_of((x, out.codes, out.scales))
-        self._record(mx.mx_lib().nvfp4_sequence_add_mx_quantize, a[:2] + a[4:], [x, out])
+        self._record(mx.mx_lib().nvfp4_sequence_add_mx_quantize, a[:2] + a[4:],
+                     (x, out.codes, out.scales), [x, out])
 
     def add_mx_gemm(self, a: "MxOperand", b: "MxOperand", out, alpha: float = 1.0) -> None:
         """Records mx_gemm(a, b, alpha, out)."""
         from . import mx
         out, args = mx._gemm_args(a, b, alpha, out, None)
-        mx._gpu_of((a.codes, a.scales, b.codes, b.scales, out))
         self._record(mx.mx_lib().nvfp4_sequence_add_mx_gemm, args,
-                     [a, b, out])
+                     (a.codes, a.scales, b.codes, b.scales, out), [a, b, out])
 
     def add_mx_gemm_quantized(self, x, b: "MxOperand", out, alpha: float = 1.0) -> None:
         """Records mx_gemm_quantized(x, b, alpha, out)."""
         from . import mx
         out, args = mx._gemm_quantized_args(x, b, alpha, out, None)
-        mx._gpu_of((x, b.codes, b.scales, out))
-        self._record(mx.mx_lib().nvfp4_sequence_add_mx_gemm_quantized, args, [x, b, out])
+        self._record(mx.mx_lib().nvfp4_sequence_add_mx_gemm_quantized, args,
+                     (x, b.codes, b.scales, out), [x, b, out])
 
     def add_mx_grouped_gemm(self, a: "MxOperand", b: "MxGroups", row_offsets, out,
                             alpha: float = 1.0, rows=None) -> None:
         """Records mx_grouped_gemm(a, b, row_offsets, alpha, rows, out)."""
         from . import mx
         out, args = mx._grouped_args(a, b, row_offsets, alpha, rows, out, None)
-        mx._gpu_of((a.codes, a.scales, b.codes, b.scales, row_offsets, rows, out))
-        self._record(mx.mx_lib().nvfp4_sequence_add_mx_grouped_gemm, args, [a, b, row_offsets, rows, out])
+        self._record(mx.mx_lib().nvfp4_sequence_add_mx_grouped_gemm, args,
+                     (a.codes, a.scales, b.codes, b.scales, row_offsets, rows, out), [a, b, row_offsets, rows, out])
 
     def add_moe_sort(self, expert_ids, out: "MoeRoute") -> None:
         """Records moe_sort(expert_ids, out.experts, out)."""
-        from . import moe, mx
+        from . import moe
         out, args = moe._sort_args(expert_ids, out.experts, out)
-        mx._gpu_of((expert_ids, out.row_offsets, out.slots, out.tokens))
         self._record(moe.moe_lib().nvfp4_sequence_add_moe_sort, args,
-                     [expert_ids, out])
+                     (expert_ids, out.row_offsets, out.slots, out.tokens), [expert_ids, out])
 
     def add_moe_gather(self, x, route: "MoeRoute", out) -> None:
         """Records moe_gather(x, route, out)."""
-        from . import moe, mx
+        from . import moe
         out, args = moe._gather_args(x, route, out)
-        mx._gpu_of((x, route.slots, out))
-        self._record(moe.moe_lib().nvfp4_sequence_add_moe_gather, args, [x, route, out])
+        self._record(moe.moe_lib().nvfp4_sequence_add_moe_gather, args,
+                     (x, route.slots, out), [x, route, out])
 
     def add_moe_combine(self, y, route: "MoeRoute", weights, out) -> None:
         """Records moe_combine(y, route, weights, out)."""
-        from . import moe, mx
+        from . import moe
         out, args = moe._combine_args(y, route, weights, out)
-        mx._gpu_of((y, route.slots, weights, out))
-        self._record(moe.moe_lib().nvfp4_sequence_add_moe_combine, args, [y, route, weights, out])
+        self._record(moe.moe_lib().nvfp4_sequence_add_moe_combine, args,
+                     (y, route.slots, weights, out), [y, route, weights, out])
 
     def finalize(self) -> None:
-        st = lib().nvfp4_sequence_finalize(self._h)
+        with self._on_gpu():
+            st = lib().nvfp4_sequence_finalize(self._h)
         if st:
             raise Nvfp4Error(st, "nvfp4_sequence_finalize")
 
     def launch(self, stream=None) -> None:
-        st = lib().nvfp4_sequence_launch(self._h, _stream_handle(stream))
+        with self._on_gpu():
+            st = lib().nvfp4_sequence_launch(self._h, _stream_handle(stream))
         if st:
             raise Nvfp4Error(st, "nvfp4_sequence_launch")
 

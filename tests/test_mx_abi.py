@@ -323,3 +323,58 @@ def test_16_element_calls_refuse_mx_operands():
         with pytest.raises(ValueError, match="blocks of 16"):
             f()
     assert seq.calls == 0 and repr(a).count("block") == 0
+
+
+def test_sequence_runs_on_the_gpu_of_its_tensors(monkeypatch):
+    """With the current GPU another one, as the calls by themselves do; a call of another GPU is refused (the GPUs
+    are stood in for)."""
+    seen, now, where = [], [0], [1]
+
+    class On:
+        def __init__(self, gpu):
+            self.gpu = gpu
+
+        def __enter__(self):
+            self.back, now[0] = now[0], self.gpu
+
+        def __exit__(self, *_):
+            now[0] = self.back
+
+    class Lib:
+        def nvfp4_sequence_finalize(self, h):
+            seen.append(("finalize", now[0]))
+            return nv.OK
+
+        def nvfp4_sequence_launch(self, h, stream):
+            seen.append(("launch", now[0], stream))
+            return nv.OK
+
+    u8 = dict(dtype=torch.uint8)
+    a = nv.MxOperand(torch.zeros(1024, **u8), torch.zeros(256, **u8), 4, 64)
+    out = torch.zeros(4, 4, dtype=torch.bfloat16)
+    ids = torch.zeros(4, 2, dtype=torch.int32)
+    i32 = dict(dtype=torch.int32)
+    r = nv.MoeRoute(torch.zeros(9, **i32), torch.zeros(4, 2, **i32), torch.zeros(8, **i32), 8)
+    seq, plain = nv.Sequence(), nv.Sequence()
+    monkeypatch.setattr(nv.mx, "_gpu_of", lambda tensors: where[0])
+    monkeypatch.setattr(nv.mx, "_current_gpu", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "device", On)
+    monkeypatch.setattr(nv, "_stream_handle", lambda stream: 100 + now[0])
+    seq.add_mx_gemm(a, a, out)
+    where[0] = 2
+    with pytest.raises(ValueError, match="GPU 1.*GPU 2"):
+        seq.add_moe_sort(ids, r)
+    assert seq.calls == 1
+    where[0] = 1
+    seq.add_moe_sort(ids, r)
+    monkeypatch.setattr(nv, "lib", Lib)
+    for s in (seq, plain):
+        s.finalize()
+        s.launch()
+    now[0] = 1
+    seq.launch()
+    assert now[0] == 1 and seen == [("finalize", 1), ("launch", 1, 101), ("finalize", 0), ("launch", 0, 100),
+                                    ("launch", 1, 101)]
+    monkeypatch.undo()
+    seq.close()
+    plain.close()
