@@ -683,6 +683,13 @@ class Sequence:
         self._check(fn(self._h, *args), fn.__name__)
         self._gpu = gpu
 
+    @staticmethod
+    def _given(out) -> None:
+        """A call by itself makes its result; nobody could reach one that a
+        sequence made."""
+        if out is None:
+            raise ValueError("a recorded call needs an out")
+
     def _on_gpu(self):
         """The context of the GPU that the recorded tensors lie on."""
         if self._gpu is None:
@@ -695,6 +702,7 @@ class Sequence:
     def add_mx_quantize(self, x, out: "MxOperand") -> None:
         """Records mx_quantize(x, out) for a 2-D x."""
         from . import mx
+        self._given(out)
         if x.dim() != 2:
             raise ValueError("x must be a 2-D tensor")
         out, a = mx._quantize_args(x, out)
@@ -704,6 +712,7 @@ class Sequence:
     def add_mx_gemm(self, a: "MxOperand", b: "MxOperand", out, alpha: float = 1.0) -> None:
         """Records mx_gemm(a, b, alpha, out)."""
         from . import mx
+        self._given(out)
         out, args = mx._gemm_args(a, b, alpha, out, None)
         self._record(mx.mx_lib().nvfp4_sequence_add_mx_gemm, args,
                      (a.codes, a.scales, b.codes, b.scales, out), [a, b, out])
@@ -711,6 +720,7 @@ class Sequence:
     def add_mx_gemm_quantized(self, x, b: "MxOperand", out, alpha: float = 1.0) -> None:
         """Records mx_gemm_quantized(x, b, alpha, out)."""
         from . import mx
+        self._given(out)
         out, args = mx._gemm_quantized_args(x, b, alpha, out, None)
         self._record(mx.mx_lib().nvfp4_sequence_add_mx_gemm_quantized, args,
                      (x, b.codes, b.scales, out), [x, b, out])
@@ -719,6 +729,7 @@ class Sequence:
                             alpha: float = 1.0, rows=None) -> None:
         """Records mx_grouped_gemm(a, b, row_offsets, alpha, rows, out)."""
         from . import mx
+        self._given(out)
         out, args = mx._grouped_args(a, b, row_offsets, alpha, rows, out, None)
         self._record(mx.mx_lib().nvfp4_sequence_add_mx_grouped_gemm, args,
                      (a.codes, a.scales, b.codes, b.scales, row_offsets, rows, out), [a, b, row_offsets, rows, out])
@@ -733,6 +744,7 @@ class Sequence:
     def add_moe_gather(self, x, route: "MoeRoute", out) -> None:
         """Records moe_gather(x, route, out)."""
         from . import moe
+        self._given(out)
         out, args = moe._gather_args(x, route, out)
         self._record(moe.moe_lib().nvfp4_sequence_add_moe_gather, args,
                      (x, route.slots, out), [x, route, out])
@@ -740,6 +752,7 @@ class Sequence:
     def add_moe_combine(self, y, route: "MoeRoute", weights, out) -> None:
         """Records moe_combine(y, route, weights, out)."""
         from . import moe
+        self._given(out)
         out, args = moe._combine_args(y, route, weights, out)
         self._record(moe.moe_lib().nvfp4_sequence_add_moe_combine, args,
                      (y, route.slots, weights, out), [y, route, weights, out])

@@ -378,3 +378,19 @@ def test_sequence_runs_on_the_gpu_of_its_tensors(monkeypatch):
     monkeypatch.undo()
     seq.close()
     plain.close()
+
+
+def test_sequence_refuses_calls_without_an_output(monkeypatch):
+    u8, i32 = dict(dtype=torch.uint8), dict(dtype=torch.int32)
+    a = nv.MxOperand(torch.zeros(1024, **u8), torch.zeros(256, **u8), 4, 64)
+    w = nv.MxGroups(torch.zeros(2048, **u8), torch.zeros(512, **u8), 2, 4, 64)
+    r = nv.MoeRoute(torch.zeros(9, **i32), torch.zeros(4, 2, **i32), torch.zeros(8, **i32), 8)
+    x, y, off = torch.zeros(4, 64), torch.zeros(8, 64), torch.zeros(3, **i32)
+    monkeypatch.setattr(nv.mx, "_gpu_of", lambda tensors: 0)
+    seq = nv.Sequence()
+    for f in (lambda: seq.add_mx_quantize(x, None), lambda: seq.add_mx_gemm(a, a, None),
+              lambda: seq.add_mx_gemm_quantized(x, a, None), lambda: seq.add_mx_grouped_gemm(a, w, off, None),
+              lambda: seq.add_moe_gather(x, r, None), lambda: seq.add_moe_combine(y, r, None, None)):
+        with pytest.raises(ValueError, match="out"):
+            f()
+    assert seq.calls == 0
