@@ -507,3 +507,33 @@ def test_linear_with_leading_dimensions(lead, dtype):
     s.synchronize()
     assert torch.equal(other, want)
     assert nv.mx_linear(x[:0], B).shape == (0, *lead[1:], 72)
+
+
+@pytest.mark.parametrize("G,N,K,rows", [
+    (5000, 40, 160, {0: 1, 17: 2, 4999: 5}),      # 64 x 64 tiles, one team of waves
+    (700, 300, 4128, {3: 1, 4: 1, 698: 3}),       # two teams
+    (300, 16400, 96, {0: 2, 150: 1, 299: 1}),     # 64 x 256
+    (65536, 16, 32, {65535: 1}),
+])
+@pytest.mark.parametrize("tail", [0, 2])
+def test_grouped_few_rows_of_many_groups(G, N, K, rows, tail):
+    """More groups than rows: the few that have some, wherever they are."""
+    say(f"grouped G={G} N={N} K={K} rows={rows} tail={tail}")
+    g = rng(G, N, K)
+    M = sum(rows.values()) + tail
+    sizes = np.zeros(G, np.int64)
+    sizes[list(rows)] = list(rows.values())
+    off = torch.from_numpy(np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)).to(DEV)
+    a = mx_ref.random_operand(g, M, K)
+    cb, sb = nv.mx_packed_size(N, K)
+    B = nv.MxGroups(torch.randint(0, 256, (cb * G,), dtype=torch.uint8, device=DEV),
+                    torch.randint(120, 130, (sb * G,), dtype=torch.uint8, device=DEV), G, N, K)
+    out = torch.full((M, N), 5.0, device=DEV)
+    nv.mx_grouped_gemm(nv.mx_to_device(*a), B, off, out=out)
+    va, at = mx_ref.values(*a), 0
+    for e, n in rows.items():
+        vb = mx_ref.values(*nv.mx_unpack(B.codes[e * cb:(e + 1) * cb].cpu().numpy(),
+                                         B.scales[e * sb:(e + 1) * sb].cpu().numpy(), N, K))
+        check(out[at:at + n], va[at:at + n], vb, 1.0)
+        at += n
+    assert (out[at:] == 5).all()

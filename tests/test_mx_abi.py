@@ -394,3 +394,16 @@ def test_sequence_refuses_calls_without_an_output(monkeypatch):
         with pytest.raises(ValueError, match="out"):
             f()
     assert seq.calls == 0
+
+
+def test_grouped_takes_many_groups():
+    """The grid is as large as the rows need, not as the groups (recorded, so that nothing is launched)."""
+    L = nv.mx.mx_lib()
+    h = ctypes.c_void_p()
+    assert L.nvfp4_sequence_create(ctypes.byref(h)) == nv.OK
+    try:
+        for G, M, N, K in ((2 ** 20, 8, 1024, 64), (2 ** 20, 8, 1024, 8192), (2 ** 22, 1, 65536, 256),
+                           (2 ** 16, 4096, 2048, 6144), (2 ** 30, 3, 100, 32)):
+            assert L.nvfp4_sequence_add_mx_grouped_gemm(h, P, P, M, None, P, P, P, G, 1.0, P, 1, M, N, K) == nv.OK
+    finally:
+        L.nvfp4_sequence_destroy(h)
