@@ -413,3 +413,43 @@ def test_graph_replays_and_sequence():
         kept = int(rr.row_offsets[-1])
         assert torch.equal(xs[:kept], nv.moe_gather(x, rr)[:kept])
     seq.close()
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("k,H", [(1, 1021), (2, 1024), (4, 1021), (8, 1020)])
+def test_rows_beyond_the_cache(k, H, dtype):
+    """Stores with the non-temporal hint, for each number of rows that are read at a time."""
+    say(f"rows beyond the cache k={k} H={H} {dtype}")
+    size = torch.finfo(DT[dtype]).bits // 8
+    T, E = (200 << 20) // (k * H * size) + 1, 11
+    g = torch.Generator(device=DEV)
+    g.manual_seed(k)
+    ids = torch.randint(-1, E, (T, k), device=DEV, generator=g, dtype=torch.int32)      # some dropped
+    r = nv.moe_sort(ids, E)
+    kept = int(r.row_offsets[-1])
+    make = lambda n: torch.randn(n, H, device=DEV, generator=g).to(DT[dtype])  # noqa: E731
+    x, w = make(T), torch.rand(T, k, device=DEV, generator=g)
+    rows = torch.full((T * k + 1, H), 7.0, dtype=DT[dtype], device=DEV)
+    nv.moe_gather(x, r, out=rows[:-1])
+    assert torch.equal(rows[:kept], x[r.tokens[:kept].long()]) and (rows[kept:] == 7).all()
+    y, d = make(T * k), make(T)
+    out, back = nv.moe_combine(y, r, w), nv.moe_gather_grad(y, r)
+    dy = torch.full((T * k + 1, H), 7.0, dtype=DT[dtype], device=DEV)
+    _, dw = nv.moe_combine_grad(d, y, r, w, dy=dy[:-1])
+    assert (dy[kept:] == 7).all()
+    half = torch.finfo(DT[dtype]).eps / 2 * 1.001
+    for t in range(0, T, 4096):
+        at = r.slots[t:t + 4096].long()
+        on = (at >= 0)[:, :, None]
+        wt, gt = w[t:t + 4096, :, None].double(), d[t:t + 4096, None].double()
+        yt = torch.where(on, y[at.clamp(min=0)].double(), 0.0)
+        # k products and k sums rounded to fp32 (2^-24 each), the result once by half a step
+        for got, p in ((out, wt * yt), (back, yt)):
+            want = p.sum(1)
+            assert ((got[t:t + 4096].double() - want).abs()
+                    <= 2 * k * 2.0 ** -24 * p.abs().sum(1) + half * want.abs() + 1e-40).all()
+        want = (wt * gt).expand(-1, -1, H)                    # rounded to fp32, then to the type
+        off = torch.where(on, (dy[at.clamp(min=0)].double() - want).abs(), 0.0)
+        assert (off <= (half + 2.0 ** -24) * want.abs() * 1.001 + 1e-40).all()
+        p = yt * gt                                           # H products and sums of fp32, in any order
+        assert ((dw[t:t + 4096].double() - p.sum(2)).abs() <= (H + 1) * 2.0 ** -24 * p.abs().sum(2)).all()

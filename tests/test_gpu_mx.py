@@ -537,3 +537,105 @@ def test_grouped_few_rows_of_many_groups(G, N, K, rows, tail):
         check(out[at:at + n], va[at:at + n], vb, 1.0)
         at += n
     assert (out[at:] == 5).all()
+
+
+# ---- operands that outgrow the last-level cache (loads and stores with the non-temporal hint) ----
+
+
+@pytest.mark.parametrize("E,N,K,sizes", [
+    (256, 256, 6144, [0, 16, 64, 65, 1, 33, 200, 17]),      # 64 x 256 tiles
+    (256, 260, 6112, [128, 129, 5, 0, 300, 256, 200, 61]),  # 128 x 256
+    (520, 120, 6112, [0, 16, 128, 129, 1, 33, 257, 17]),    # 128 x 128
+    (600, 250, 5216, [1] + [0] * 199),                      # 64 x 64, two teams of waves
+    (1500, 250, 2016, [2] + [0] * 499),                     # one team
+])
+@pytest.mark.parametrize("indirect", [False, True])
+def test_grouped_weights_beyond_the_cache(E, N, K, sizes, indirect):
+    """Groups of no, one and several row blocks side by side."""
+    say(f"grouped E={E} N={N} K={K} sizes={sizes[:8]} indirect={indirect}")
+    g = rng(E, N, K)
+    sizes = (sizes * E)[:E]
+    off = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    M, n = int(off[-1]) + 3, 37
+    cb, sb = nv.mx_packed_size(N, K)
+    assert (cb + sb) * E > 192 << 20
+    B = nv.MxGroups(torch.randint(0, 256, (cb * E,), dtype=torch.uint8, device=DEV),
+                    torch.randint(120, 130, (sb * E,), dtype=torch.uint8, device=DEV), E, N, K)
+    a = mx_ref.random_operand(g, n if indirect else M, K)
+    rows = g.integers(0, n, M).astype(np.int32) if indirect else np.arange(M)
+    va = mx_ref.values(*a)
+    out = torch.full((M, N), 5.0, dtype=torch.bfloat16, device=DEV)
+    nv.mx_grouped_gemm(nv.mx_to_device(*a), B, torch.from_numpy(off).to(DEV), out=out,
+                       rows=torch.from_numpy(rows).to(DEV) if indirect else None)
+    used = [e for e in range(E) if sizes[e]]
+    for e in used[:8] + used[len(used) // 2:len(used) // 2 + 8] + used[-8:]:
+        vb = mx_ref.values(*nv.mx_unpack(B.codes[e * cb:(e + 1) * cb].cpu().numpy(),
+                                         B.scales[e * sb:(e + 1) * sb].cpu().numpy(), N, K))
+        check(out[off[e]:off[e + 1]], va[rows[off[e]:off[e + 1]]], vb, 1.0)
+    assert not torch.isnan(out).any() and (out[off[-1]:] == 5).all()
+
+
+def test_few_packed_rows_by_weights_beyond_the_cache():
+    """The product of packed rows beside the one that quantises them, whose columns test_linear_wide checks."""
+    K, N = 8160, 49_205
+    W = nv.mx_quantize(torch.randn(N, K, device=DEV, dtype=torch.bfloat16))
+    for M in (1, 7, 16):
+        q = nv.mx_quantize(torch.randn(M, K, device=DEV))
+        x = nv.mx_dequantize(q)                              # quantising these again gives the same operand
+        for dtype in DT.values():
+            c = nv.mx_gemm(q, W, dtype=dtype)
+            assert torch.equal(c, nv.mx_gemm_quantized(x, W, dtype=dtype))
+        c1, s1 = nv.mx_packed_size(N % 16 or 16, K)
+        tail = nv.MxOperand(W.codes[-c1:], W.scales[-s1:], N % 16, K)
+        check(c[:, N - N % 16:], host(x).astype(np.float64), host(nv.mx_dequantize(tail)).astype(np.float64), 1.0)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_quantize_and_back_beyond_the_cache(dtype):
+    """The same rows in parts, which take the plain loads and stores."""
+    rows, K = (6205, 8224) if dtype == "fp32" else (12_301, 8224)
+    x = torch.randn(rows, K, device=DEV).to(DT[dtype]) * torch.rand(rows, 1, device=DEV).to(DT[dtype]) * 8
+    assert x.numel() * x.element_size() > 192 << 20
+    q = nv.mx_quantize(x)
+    back = {t: nv.mx_dequantize(q, t) for t in DT.values()}
+    assert torch.equal(back[torch.float32], back[torch.bfloat16].float())
+    for r in range(0, rows, 2048):
+        part = nv.mx_quantize(x[r:r + 2048])
+        cb, sb = nv.mx_packed_size(r, K)
+        assert torch.equal(q.codes[cb:cb + part.codes.numel()], part.codes)
+        assert torch.equal(q.scales[sb:sb + part.scales.numel()], part.scales)
+        for t in DT.values():
+            assert torch.equal(back[t][r:r + 2048], nv.mx_dequantize(part, t))
+    equal_bytes(part, host(x[r:]))
+
+
+# ---- rounding and range ---------------------------------------------------------
+
+
+def test_quantize_fp32_beside_the_borders():
+    """fp32 values one step below, on and above every border between codes, under every scale."""
+    tops = [np.float32(1.5) * np.float32(2.0) ** e for e in range(-140, 127)] + [np.float32(2.0 ** -149)]
+    blocks = []
+    for top in tops:
+        _, e = np.frexp(np.float64(top))
+        scale = 2.0 ** max(e - 3, -127)
+        for sign in (1.0, -1.0):
+            v = np.array([sign * edge * scale for edge in mx_ref.EDGES], np.float64).astype(np.float32)
+            inf = np.float32(np.inf)
+            row = np.concatenate([v, np.nextafter(v, inf), np.nextafter(v, -inf), [top, -top, 0.0, -0.0]])
+            row = np.where(np.abs(row) <= np.float32(top) * np.float32(1.3), row, 0.0)   # (none above the top)
+            blocks.append(np.concatenate([row, np.zeros(32 - row.size)]).astype(np.float32))
+    equal_bytes(nv.mx_quantize(torch.from_numpy(np.stack(blocks)).to(DEV)), np.stack(blocks))
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_dequantize_past_the_largest_value(dtype):
+    """A code times its scale is exact where the type holds it; 2^128 and more are infinities."""
+    codes = np.tile(np.arange(16, dtype=np.uint8), (6, 2))
+    codes = (codes[:, 0::2] | codes[:, 1::2] << 4).astype(np.uint8)
+    scales = np.array([[0], [1], [251], [252], [253], [254]], np.uint8)
+    got = nv.mx_dequantize(nv.mx_to_device(codes, scales), DT[dtype]).double().cpu().numpy()
+    want = mx_ref.values(codes, scales)
+    want = np.where(np.abs(want) >= 2.0 ** 128, np.copysign(np.inf, want), want)
+    assert np.array_equal(got, want) and np.array_equal(np.signbit(got), np.signbit(want))
+    assert np.isinf(want).sum() == 2 * (2 * 2 + 2 * 4)       # +-4, 6 under byte 253; +-2, 3, 4, 6 under 254; twice
