@@ -269,17 +269,19 @@ __global__ void __launch_bounds__(KS * 256, KS > 1 || BM * BN > 128 * 256 ? KS :
     constexpr int STAGE = (AF + BF) * kMxFrag;
     constexpr int SCALES = (AF + BF) * kMxScaleFrag;      // of four steps
     // Step c's place in the ring is filled again, for step c + NS, from the
-    // middle of step c on; a scale word's first step c fills the place of word
-    // c / 4 with the one NQ words on, which is not needed before.
-    constexpr int NQ = (NS + 3) / 4;
+    // middle of step c on; a scale word is in registers before its first step,
+    // from whose middle on the next word's loads fill the buffer.  They have
+    // landed by the middle of the word's last step, where it is read: no more
+    // than two steps' loads are in flight there.
+    static_assert(NS == 3 || NS == 4, "scales are read three steps behind their loads");
     // scale loads among those issued at the `many` steps before step k
     constexpr auto scale_loads = [](int k, int many) {
         int n = 0;
         for (int d = 1; d <= many; ++d) n += ((k - d) & 3) == 0 ? SPW : 0;
         return n;
     };
-    static_assert(AF % 4 == 0 && BF % 4 == 0 && NS >= 2 && (NS + 1) * CPW + NQ * SPW < 64, "ring");
-    constexpr int RING = NS * STAGE + NQ * SCALES;
+    static_assert(AF % 4 == 0 && BF % 4 == 0 && (NS + 1) * CPW + SPW < 64, "ring");
+    constexpr int RING = NS * STAGE + SCALES;
     static_assert(BM * WN * (BN / WN * 2 + 16) <= RING, "the output is staged in the first ring");
     static_assert((KS - 1) * BM * BN * 4 <= KS * RING, "and partial tiles in all");
     __shared__ __attribute__((aligned(1024))) uint8_t lds_all[KS * RING];
@@ -422,15 +424,14 @@ __global__ void __launch_bounds__(KS * 256, KS > 1 || BM * BN > 128 * 256 ? KS :
             mx_dma<16, (AF + i - APW) * kMxFrag, NT.value>(rbc, code_at[i], from,
                                                            lds0 + (uint32_t)(stage * STAGE + wave * BPW * kMxFrag));
     };
-    auto load_scale = [&](auto I, int q, int place) {
+    auto load_scale = [&](auto I, int q) {
         constexpr int i = I.value;
         const uint32_t from = (uint32_t)min(q0 + q, Q - 1) * kMxScaleFrag;
         if constexpr (i < APW)
-            mx_dma<4, NS * STAGE + i * kMxScaleFrag>(ras, scale_at[i], from,
-                                                     lds0 + (uint32_t)(place * SCALES + wave * APW * kMxScaleFrag));
+            mx_dma<4, NS * STAGE + i * kMxScaleFrag>(ras, scale_at[i], from, lds0 + (uint32_t)(wave * APW * kMxScaleFrag));
         else
-            mx_dma<4, NS * STAGE + (AF + i - APW) * kMxScaleFrag>(
-                rbs, scale_at[i], from, lds0 + (uint32_t)(place * SCALES + wave * BPW * kMxScaleFrag));
+            mx_dma<4, NS * STAGE + (AF + i - APW) * kMxScaleFrag>(rbs, scale_at[i], from,
+                                                                  lds0 + (uint32_t)(wave * BPW * kMxScaleFrag));
     };
 
     mx_f16 acc[MI][NI];
@@ -467,14 +468,14 @@ __global__ void __launch_bounds__(KS * 256, KS > 1 || BM * BN > 128 * 256 ? KS :
             h.b[i - MI] = *reinterpret_cast<const mx_u4*>(p + (fb + 2 * (i - MI)) * kMxFrag);
     };
     // the two scale words of 32-row block I
-    auto read_scale = [&](auto I, Scales& s, int place) {
+    auto read_scale = [&](auto I, Scales& s) {
         constexpr int i = I.value;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
             if constexpr (i < MI)
-                s.a[i][h] = *reinterpret_cast<const uint32_t*>(lane_sa + place * SCALES + 2 * i * kMxScaleFrag + h * 8);
+                s.a[i][h] = *reinterpret_cast<const uint32_t*>(lane_sa + 2 * i * kMxScaleFrag + h * 8);
             else
-                s.b[i - MI][h] = *reinterpret_cast<const uint32_t*>(lane_sb + place * SCALES + 2 * (i - MI) * kMxScaleFrag + h * 8);
+                s.b[i - MI][h] = *reinterpret_cast<const uint32_t*>(lane_sb + 2 * (i - MI) * kMxScaleFrag + h * 8);
     };
     Scales sc, sn;
     auto mfma = [&](auto N, auto S, const Half& h, int half) {
@@ -484,26 +485,21 @@ __global__ void __launch_bounds__(KS * 256, KS > 1 || BM * BN > 128 * 256 ? KS :
 
     auto pipeline = [&](auto NT) {
         // fill the ring
-        mx_each<NQ>([&](auto q) {
-            if constexpr (q.value < NQ - NS / 4) mx_each<SPW>([&](auto I) { load_scale(I, q.value, q.value); });
-        });
         mx_each<NS>([&](auto c) {
             mx_each<CPW>([&](auto I) { load_code(I, NT, c.value, c.value); });
-            // (as if at step c - NS)
-            constexpr int q = (c.value - NS) / 4 + NQ;
-            if constexpr ((c.value - NS) % 4 == 0) mx_each<SPW>([&](auto I) { load_scale(I, q, q); });
+            if constexpr (c.value == 0) mx_each<SPW>([&](auto I) { load_scale(I, 0); });
         });
-        wait_vmcnt<(NS - 1) * CPW + scale_loads(0, NS - 1)>();  // step 0 and the first scale word
+        wait_vmcnt<(NS - 1) * CPW>();  // the first scale word and step 0
         wg_barrier();
         Half h0, h1;
-        mx_each<P>([&](auto I) { read_scale(I, sc, 0); });
+        mx_each<P>([&](auto I) { read_scale(I, sc); });
         mx_each<P>([&](auto I) { read(I, h0, 0, 0); });
 
         // One step.  The order is fixed (the scheduling barriers): behind each
         // MFMA one LDS read and its share of the loads, which issue while the
         // MFMA runs; left to itself the compiler moves the reads to their uses
         // and the MFMAs wait for each.
-        int c = 0, stage = 0, place = 0;
+        int c = 0, stage = 0;
         auto step = [&](auto S) {
             constexpr int s = S.value;
             mx_each<MM>([&](auto N) {
@@ -524,19 +520,16 @@ __global__ void __launch_bounds__(KS * 256, KS > 1 || BM * BN > 128 * 256 ? KS :
                 mfma(N, S, h1, 1);
                 mx_each<P>([&](auto I) {
                     if constexpr (slot_of(I.value) == n) read(I, h0, stage, 0);
-                    if constexpr (s == 3 && MM - 1 - slot_of(I.value) == n) read_scale(I, sn, NQ > 1 ? (place + 1) % NQ : 0);
+                    if constexpr (s == 3 && MM - 1 - slot_of(I.value) == n) read_scale(I, sn);
                 });
                 mx_each<(n + 1) * CPW / MM - n * CPW / MM>([&](auto I) {
                     constexpr int i = n * CPW / MM + I.value;
                     load_code(std::integral_constant<int, i>{}, NT, c + NS, freed);
-                    if constexpr (s == 0) load_scale(std::integral_constant<int, i>{}, c / 4 + NQ, place);
+                    if constexpr (s == 0) load_scale(std::integral_constant<int, i>{}, c / 4 + 1);
                 });
                 __builtin_amdgcn_sched_barrier(0);
             });
-            if constexpr (s == 3) {
-                sc = sn;
-                if constexpr (NQ > 1) place = (place + 1) % NQ;
-            }
+            if constexpr (s == 3) sc = sn;
             ++c;
         };
         // whole scale words, then the steps that are left (one loop exit: the
