@@ -15,6 +15,7 @@
  *                          each token's choices
  *   nvfp4_moe_combine_grad gradients of combine
  * The gradient of gather is combine without weights.
+ * In the library from nvfp4_version() 10600 on.
  *
  * Element type of rows: NVFP4_TYPE_F32 or NVFP4_TYPE_BF16 (nvfp4_mx.h);
  * weights are fp32.  Rows are row-major; the rows in the experts' order are

@@ -30,6 +30,8 @@
  * be picked one by one, and the places are such that the lanes of a wave
  * read them from LDS without bank conflicts.
  *
+ * In the library from nvfp4_version() 10600 on.
+ *
  * Status codes, pointers, streams and errors as in nvfp4.h: every entry point
  * returns an nvfp4_status and never aborts, throws or prints; argument errors
  * are detected on the host before any device work; device buffers are

@@ -407,3 +407,10 @@ def test_grouped_takes_many_groups():
             assert L.nvfp4_sequence_add_mx_grouped_gemm(h, P, P, M, None, P, P, P, G, 1.0, P, 1, M, N, K) == nv.OK
     finally:
         L.nvfp4_sequence_destroy(h)
+
+
+def test_version_tells_of_the_operators():
+    """A C caller that looks the functions up at run time can ask for the version first, as the headers say."""
+    assert nv.version() >= 10600
+    for header in ("nvfp4_mx.h", "nvfp4_moe.h"):
+        assert "nvfp4_version() 10600" in open(os.path.join(ROOT, "include", header)).read()
