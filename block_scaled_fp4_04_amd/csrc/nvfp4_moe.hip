@@ -394,7 +394,7 @@ hipError_t run_rows(const MoeArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// With rows that outgrow the last-level cache every store is non-temporal: a
+// With rows of more than kStreamBytes every store is non-temporal: a
 // gather of 65536 rows of 4 KB takes 50 us instead of 59, a combine of them
 // with its gradients 139 instead of 171.  (Non-temporal loads slowed that
 // down: the gradient reads the rows again.)

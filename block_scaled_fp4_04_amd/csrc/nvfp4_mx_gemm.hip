@@ -92,7 +92,7 @@ __device__ __forceinline__ void mx_store4(const MxGemmArgs& a, int row, int col,
 // rows of sixteen blocks at a time, a block to a lane, and hands the codes
 // to the lanes that multiply them through LDS.  (With a lane quantising the
 // four blocks that it multiplies, one row cost as much as sixteen: 5.0 us
-// at 1 x 768 x 6144, where packed operands take 3.7.)  A workgroup then walks
+// at 1 x 768 x 6144, where packed operands take 3.4.)  A workgroup then walks
 // the row blocks of B that its turn comes to: with one scale word to a wave (K
 // up to 8192) the rows are quantised once and the next row block is loaded
 // while the sums of this one are added.
@@ -542,7 +542,7 @@ __global__ void __launch_bounds__(KS * 256, KS > 1 || BM * BN > 128 * 256 ? KS :
         }
     };
     // A group of one row block reads its weights once: non-temporally, if
-    // those of all groups outgrow the last-level cache (256 experts x 256
+    // those of all groups are more than kStreamBytes (256 experts x 256
     // columns, 16 rows: 42.5 -> 38.6 us; groups of several row blocks share theirs
     // in the L2, which keeps such loads for less long: 128 rows 76 -> 80 us).
     if (GROUPED && stream)
@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(KS * 256, KS > 1 || BM * BN > 128 * 256 ? KS :
         }
         __syncthreads();
         if (KS > 1 && team > 0) return;
-        const bool stream_out = 2 * (int64_t)a.M * a.N > kStreamBytes;  // (16384 x 8192 x 8192: 480 -> 475 us)
+        const bool stream_out = 2 * (int64_t)a.M * a.N > kStreamBytes;  // (28672 x 8192 x 2048: 309 -> 308 us)
         constexpr int LPR = PN / 8;        // lanes that store a row's part
         constexpr int RPS = 64 / LPR;      // rows a store covers
         const int r = lane / LPR, col = col0 + (lane % LPR) * 8;
@@ -705,8 +705,9 @@ void choose(Launch& l) {
         // 16 rows each: 13.4 us, 18.1 with 64 x 256 tiles); about even at 64
         // experts x 512 x K 2048 with 16 rows (640 tiles).
         if (tiles(64, 64) <= 640) return run_small_tiles<true>(l);
-        // From 128 rows each, larger tiles read the weights less often (256
-        // experts x 256 columns, 128 rows: 75 against 77 us; 16 x 2048 x K 2048,
+        // From 128 rows each (dropped ones among them), larger tiles read the
+        // weights less often (256 experts x 256 columns, 128 rows: 73 us, 77 with
+        // one token less and 64 x 256 tiles, in three runs; 16 x 2048 x K 2048,
         // 1024 rows: 56 against 64), if they are enough to fill the GPU or the
         // weights come from memory (8 x 2048, 256 rows: 27 against 33; but 4 x
         // 768, 1024 rows: 25 against 20).
@@ -720,15 +721,15 @@ void choose(Launch& l) {
         return run_tile<64, 256, 3, 1, 1, true>(l);
     }
     const int64_t weights = a.RBb * ((int64_t)a.C * kMxFrag + (a.C + 3) / 4 * kMxScaleFrag);
-    if (!a.a_codes) {  // (1 x 131072 x 8192: 103 -> 89 us with the weights non-temporal)
+    if (!a.a_codes) {  // (1 x 131072 x 8192: 98 -> 87 us with the weights non-temporal)
         if (weights > kStreamBytes) return a.x_bf16 ? run_skinny<1, A_BF16, false, true>(l) : run_skinny<1, A_F32, false, true>(l);
         return a.x_bf16 ? run_skinny<1, A_BF16, false>(l) : run_skinny<1, A_F32, false>(l);
     }
     // Up to 16 rows always the kernel that quantises too: the same bits (1 x
     // 768: 3.5 us, 7.3 with 64 x 64 tiles; 16 x 6144: 7.1 and 8.4).
     if (M <= kMxQuantRows) {
-        // (weights beyond the last-level cache: 1 x 131072 x 8192 93 -> 87 us, 16
-        // rows 103 -> 98)
+        // (weights of more than kStreamBytes: 1 x 131072 x 8192 89 -> 81 us, 16 rows
+        // 117 -> 111)
         return weights > kStreamBytes ? run_skinny<1, A_PACKED, false, true>(l) : run_skinny<1, A_PACKED, false>(l);
     }
     // Up to 64 rows while its workgroups fit the GPU at once (64 x 768: 5.3

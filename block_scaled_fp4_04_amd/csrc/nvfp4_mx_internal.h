@@ -19,10 +19,22 @@ constexpr int kMxScaleFrag = 256;  // scale bytes of 16 rows x four steps
 __host__ __device__ constexpr int mx_code_at(int r, int b) { return r * 64 + ((b ^ (r >> 2)) << 4); }
 __host__ __device__ constexpr int mx_scale_at(int r, int b) { return r * 16 + b * 4; }
 
-// Results of more bytes than this are stored non-temporally: they outgrow the
-// 256 MB last-level cache, and whatever reads them next comes from memory
-// anyhow.  (Rows gathered and combined again: 128 MB of them 53 us with plain
-// stores, 61 without; 256 MB 121 and 115.)
+// Results of more bytes than this are stored non-temporally, and inputs and
+// weights of more are loaded so: what is written or read once then does not pass
+// through the 256 MB last-level cache, which a call that uses it again would
+// have found it in.  The border is a compromise of the two.  Used once (three
+// buffers in turn) the hint is the faster one from about 96 MB on; used again by
+// the next call it is from about 256 MB on.  us without and with it:
+//                              128 MB       192 MB       256 MB       320 MB
+//   quantise fp32, once      28.3  26.5   40.9  38.3   53.4  50.0   66.4  62.1
+//   dequantise and quantise  47.1  49.9   69.9  72.8   98.9  95.2   152   119
+//   gather and combine       53.2  59.0   76.3  87.1   124   116    168   147
+//   weights of experts
+//     three sets in turn     31.7  30.3   40.1  37.1   59.8  55.7   70.4  61.5
+//     the same again         23.4  27.0   32.7  35.6   51.8  54.1   66.2  60.6
+//   weights of one row
+//     three sets in turn     25.9  24.3   38.4  35.0   50.5  46.0   62.2  55.9
+//     the same again         22.0  21.1   31.0  32.3   40.4  43.3   57.1  53.3
 constexpr int64_t kStreamBytes = (int64_t)192 << 20;
 
 inline int64_t mx_round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }

@@ -21,8 +21,8 @@ namespace {
 // bytes, 16381 x 8160 fp32 took 122 us, and 269 with non-temporal loads).  The
 // 8 or 4 lanes of a block find its largest magnitude with lane permutes; the
 // codes go through LDS, from where lane l stores bytes 16 l ... of the
-// fragment.  NT: non-temporal loads, for inputs that outgrow the last-level
-// cache (106 us; 116 without; 16384 x 8192 bfloat16 54 and 59 us).
+// fragment.  NT: non-temporal loads, for inputs of more than kStreamBytes
+// (105 us; 116 without; 16384 x 8192 bfloat16 54 and 59 us).
 template <int CTRL>
 __device__ __forceinline__ uint32_t mx_dpp(uint32_t x) {
     return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, CTRL, 0xF, 0xF, true);
@@ -116,7 +116,8 @@ __global__ void __launch_bounds__(256) mx_dequantize_kernel(MxQuantArgs a) {
         const int row = (int)(grb % a.RB) * kMxRows + r;
         const float s = mx_scale(bytes[r * 4 + b]);
         const uint8_t* p = codes + mx_code_at(r, b) + col % kMxBlock / 2;
-        // (a code times a power of two is exact in either type, subnormals included)
+        // (a code times a power of two is exact in either type, subnormals
+        // included, up to the overflow to infinity at 2^128)
         mx_u4 o;
         if constexpr (sizeof(T) == 2) {
             const uint32_t w = *reinterpret_cast<const uint32_t*>(p);

@@ -9,6 +9,12 @@ Argument marshalling only.
 
 or, for a product that reads its rows in order (``grouped_gemm``), with
 ``moe_gather(x, route)`` in front of it.
+
+The gradients are functions of their own (``moe_gather_grad``,
+``moe_combine_grad``): nothing here is recorded by autograd, and results carry
+no history, whatever the inputs require.  A training program calls them from
+the backward of its own ``torch.autograd.Function``; the products between them
+have no backward form here.
 """
 from __future__ import annotations
 
@@ -138,7 +144,8 @@ def moe_gather(x, route: MoeRoute, out=None, stream=None):
     """The rows of x (tokens x hidden, rows may be strided) in the experts'
     order, one for each kept choice (nvfp4_moe_gather): [tokens * topk,
     hidden].  Rows that no choice owns (behind row_offsets[-1]) are left as
-    they were in ``out``."""
+    they were in ``out``: in one that the call makes they hold anything.  Pass a
+    zeroed ``out`` to a product or a sum that reads all rows."""
     if stream is not None:
         with _on(stream, x):
             return moe_gather(x, route, out)
@@ -179,7 +186,9 @@ def moe_combine_grad(dout, y, route: MoeRoute, weights=None, dy=None, dweights=N
     """The gradients (dy, dweights) of moe_combine(y, route, weights) for its
     output's gradient ``dout`` [tokens, hidden] (rows may be strided)
     (nvfp4_moe_combine_grad).  Rows of dy that no choice owns are left as they
-    were; dweights of dropped choices are zero.  ``dy`` may be y itself."""
+    were: in a dy that the call makes they hold anything (their gradient is zero:
+    pass a zeroed ``dy`` to what reads all rows); dweights of dropped choices are
+    zero.  ``dy`` may be y itself."""
     if stream is not None:
         with _on(stream, dout):
             return moe_combine_grad(dout, y, route, weights, dy, dweights)

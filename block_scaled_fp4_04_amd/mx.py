@@ -8,7 +8,9 @@ checkpoint, ``mx_gemm`` multiplies two of them, ``mx_linear`` takes plain
 activations, and ``mx_grouped_gemm`` serves a layer of experts.
 
 Tensors of one call lie on one GPU; the call runs there, on that GPU's current
-stream unless ``stream`` names one.
+stream unless ``stream`` names one.  Results carry no autograd history, whatever
+the inputs require: quantisation has no gradient, and the products here have no
+backward form.
 """
 from __future__ import annotations
 
@@ -302,7 +304,8 @@ def mx_quantize(x, out=None, stream=None):
 
 def mx_dequantize(a, dtype=None, out=None, stream=None):
     """The values of an MxOperand (rows x K) or MxGroups (groups x rows x K)
-    as bfloat16 (default) or float32, exact in both (nvfp4_mx_dequantize)."""
+    as bfloat16 (default) or float32, exact in both but that values from 2^128
+    on are infinities (nvfp4_mx_dequantize)."""
     _kind(a, "a", MxOperand, MxGroups)
     if stream is not None:
         with _on(stream, a.codes):
@@ -421,7 +424,8 @@ def mx_grouped_gemm(a: MxOperand, b: MxGroups, row_offsets, alpha: float = 1.0, 
     row_offsets[g+1]-1 of C belong to group g, whose weights are b's g-th
     operand.  Row r of C takes row rows[r] of A (``MoeRoute.tokens``: the
     activations are quantised once per token and never copied), or row r
-    without ``rows``.  Rows behind the last group are left as they were."""
+    without ``rows``.  Rows behind the last group are left as they were: in an
+    ``out`` that the call makes they hold anything."""
     if stream is not None:
         with _on(stream, a.codes):
             return mx_grouped_gemm(a, b, row_offsets, alpha, rows, out, dtype)

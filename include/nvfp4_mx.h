@@ -42,7 +42,10 @@
  * buffers are on.
  *
  * Sizes: rows and M from 0 (nothing is launched) and N from 1 to 2^30, K a
- * positive multiple of 32 up to 2^30.
+ * positive multiple of 32 up to 2^30.  A call that would take more work-items
+ * than one launch holds (2^32) is refused with NVFP4_ERR_INVALID_VALUE: groups
+ * x row blocks x steps from about 2^26 when quantising, N from about 2^26 in a
+ * product of up to 16 rows.
  */
 #ifndef NVFP4_MX_H
 #define NVFP4_MX_H
@@ -87,8 +90,10 @@ int nvfp4_mx_quantize(const void* x, int x_type, int64_t groups, int64_t group_s
                       int64_t rows, int64_t K, int64_t ld, void* packed_codes,
                       void* packed_scales, void* stream);
 
-/* The values that packed operands stand for, as fp32 or bfloat16 rows (exact
- * in both: a code has two significant bits; NaN for blocks with scale 255).
+/* The values that packed operands stand for, as fp32 or bfloat16 rows.  Exact
+ * in both (a code has two significant bits), but that values from 2^128 on are
+ * infinities: codes of 4 and more under scale byte 253, of 2 and more under 254,
+ * which no finite input is quantised to.  NaN for blocks with scale 255.
  * Buffers and strides as nvfp4_mx_quantize (group_stride >= K: groups must not
  * overlap); writes the rows x K elements of every group and nothing between
  * them. */
@@ -109,7 +114,10 @@ int nvfp4_mx_gemm(const void* a_packed, const void* a_scales, const void* b_pack
                   int64_t N, int64_t K, void* stream);
 
 /* nvfp4_mx_gemm(nvfp4_mx_quantize(X), B) in one launch, bit for bit, for
- * decode steps, where a second launch costs as much as the product.
+ * decode steps, where a second launch costs as much as the product.  Up to K =
+ * 8192 it is the faster form; behind that every 16 columns quantise the rows
+ * again, which takes about N * K * (6 + M) / 2e8 us and pays while that is less
+ * than a launch.
  *   x : DEVICE, M x K values of x_type, row stride ldx elements (as
  *       nvfp4_mx_quantize); M is at most 16 (NVFP4_ERR_UNSUPPORTED above) */
 int nvfp4_mx_gemm_quantized(const void* x, int x_type, int64_t ldx, const void* b_packed,
@@ -133,7 +141,11 @@ int nvfp4_mx_gemm_quantized(const void* x, int x_type, int64_t ldx, const void* 
  * Entries of row_offsets are clamped to [0, M] and of
  * a_rows to A's rows: a malformed table gives wrong rows, no access outside
  * the buffers (overlapping groups may then write the same rows).
- * NVFP4_ERR_MISALIGNED unless the tables are 4-byte aligned. */
+ * NVFP4_ERR_MISALIGNED unless the tables are 4-byte aligned.
+ * Fast while A's packed codes are less than 2 GiB; from there on a kernel
+ * without 32-bit offsets runs, which reads the weights again for every 32 rows
+ * (8 groups x 256 x 8192, 524272 rows: 0.66 ms, 524304 rows: 8.9 ms): split the
+ * groups over calls. */
 int nvfp4_mx_grouped_gemm(const void* a_packed, const void* a_scales, int64_t a_count,
                           const int32_t* a_rows, const void* b_packed, const void* b_scales,
                           const int32_t* row_offsets, int64_t groups, float alpha, void* out,
