@@ -596,6 +596,9 @@ def probe_read(src, blocks: int, out, stream=None) -> None:
         raise Nvfp4Error(st, f"nvfp4_probe_read(blocks={blocks})")
 
 
+_HERE = contextlib.nullcontext()
+
+
 class Sequence:
     """A recorded sequence of NVFP4 calls replayed with one graph launch
     (nvfp4_sequence_*): record with the add_* methods (fixed buffers; the
@@ -613,7 +616,7 @@ class Sequence:
             raise Nvfp4Error(st, "nvfp4_sequence_create")
         self._h = h
         self._keep = []
-        self._gpu = None
+        self._gpu = self._mx = None  # (of the MXFP4 and routing calls)
         self.calls = 0
 
     def _check(self, st, what):
@@ -681,7 +684,7 @@ class Sequence:
             raise ValueError(f"the sequence's tensors are on GPU {self._gpu}, those of this call on GPU {gpu}")
         self._keep += keep
         self._check(fn(self._h, *args), fn.__name__)
-        self._gpu = gpu
+        self._gpu, self._mx = gpu, mx
 
     @staticmethod
     def _given(out) -> None:
@@ -692,12 +695,9 @@ class Sequence:
 
     def _on_gpu(self):
         """The context of the GPU that the recorded tensors lie on."""
-        if self._gpu is None:
-            return contextlib.nullcontext()
-        from . import mx
-        if self._gpu == mx._current_gpu():
-            return contextlib.nullcontext()
-        return mx.torch.cuda.device(self._gpu)
+        if self._gpu is None or self._gpu == self._mx._current_gpu():
+            return _HERE
+        return self._mx.torch.cuda.device(self._gpu)
 
     def add_mx_quantize(self, x, out: "MxOperand") -> None:
         """Records mx_quantize(x, out) for a 2-D x."""

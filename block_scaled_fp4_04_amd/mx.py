@@ -163,7 +163,7 @@ class MxGroups:
 def _kind(x, name: str, *kinds) -> None:
     """Refuses an operand of another class: groups, and the operands of the
     other format, have the same fields."""
-    if not isinstance(x, kinds):
+    if type(x) is not kinds[0] and not isinstance(x, kinds):
         raise ValueError(f"{name} must be {' or '.join(k.__name__ for k in kinds)}, not {type(x).__name__}")
 
 
@@ -380,7 +380,6 @@ def mx_linear(x, b: MxOperand, alpha: float = 1.0, out=None, dtype=None, stream=
     if stream is not None:
         with _on(stream, x):
             return mx_linear(x, b, alpha, out, dtype)
-    _kind(b, "b", MxOperand)
     if x.dim() > 2:
         shape = (*x.shape[:-1], b.rows)
         if out is not None and (tuple(out.shape) != shape or not out.is_contiguous()):
@@ -394,6 +393,7 @@ def mx_linear(x, b: MxOperand, alpha: float = 1.0, out=None, dtype=None, stream=
     if x.dim() == 2 and x.shape[0] <= MX_QUANT_ROWS and (
             b.K <= 8192 or b.rows * b.K * (6 + x.shape[0]) <= 800_000_000):
         return mx_gemm_quantized(x, b, alpha, out, dtype)
+    _kind(b, "b", MxOperand)
     return mx_gemm(mx_quantize(x), b, alpha, out, dtype)
 
 
