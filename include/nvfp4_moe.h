@@ -87,8 +87,9 @@ int nvfp4_moe_combine(const void* y, int type, int64_t tokens, int64_t topk, int
  *   y        : DEVICE (tokens * topk) x hidden, as given to combine
  *   weights  : DEVICE fp32 [tokens][topk], or NULL: ones
  *   dy       : DEVICE (tokens * topk) x hidden; may be y itself (each element
- *              is read before it is written)
- *   dweights : DEVICE fp32 [tokens][topk], overwritten */
+ *              is read before it is written), no other input
+ *   dweights : DEVICE fp32 [tokens][topk], overwritten; must not alias the
+ *              inputs */
 int nvfp4_moe_combine_grad(const void* dout, int64_t ldd, const void* y, int type,
                            int64_t tokens, int64_t topk, int64_t hidden, const int32_t* slots,
                            const float* weights, void* dy, float* dweights, void* stream);

@@ -45,7 +45,7 @@
  * positive multiple of 32 up to 2^30.  A call that would take more work-items
  * than one launch holds (2^32) is refused with NVFP4_ERR_INVALID_VALUE: groups
  * x row blocks x steps from about 2^26 when quantising, N from about 2^26 in a
- * product of up to 16 rows.
+ * product of up to 16 packed rows.
  */
 #ifndef NVFP4_MX_H
 #define NVFP4_MX_H
