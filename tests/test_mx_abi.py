@@ -244,7 +244,7 @@ def test_binding_refuses_operands_of_another_class():
     of the 16-element format, whose buffers have other sizes."""
     u8 = dict(dtype=torch.uint8)
     a = nv.MxOperand(torch.zeros(1024, **u8), torch.zeros(256, **u8), 4, 64)
-    w = nv.MxGroups(torch.zeros(3072, **u8), torch.zeros(768, **u8), 3, 4, 64)
+    w = nv.MxGroups(torch.zeros(3 * 1024, **u8), torch.zeros(768, **u8), 3, 4, 64)
     one = nv.MxGroups(a.codes, a.scales, 1, 4, 64)
     cb, sb = nv.packed_size(4, 64)
     p = nv.PackedOperand(torch.zeros(cb, **u8), torch.zeros(sb, **u8), 4, 64)
@@ -306,7 +306,7 @@ def test_16_element_calls_refuse_mx_operands():
     """Their scale buffers are half as large: the kernels would read and write past them."""
     u8 = dict(dtype=torch.uint8)
     a = nv.MxOperand(torch.zeros(1024, **u8), torch.zeros(256, **u8), 4, 64)
-    w = nv.MxGroups(torch.zeros(3072, **u8), torch.zeros(768, **u8), 3, 4, 64)
+    w = nv.MxGroups(torch.zeros(3 * 1024, **u8), torch.zeros(768, **u8), 3, 4, 64)
     cb, sb = nv.packed_size(4, 64)
     p = nv.PackedOperand(torch.zeros(cb, **u8), torch.zeros(sb, **u8), 4, 64)
     pw = nv.PackedGroups(torch.zeros(3 * cb, **u8), torch.zeros(3 * sb, **u8), 3, 4, 64)
