@@ -6,6 +6,8 @@ import os
 import re
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +20,8 @@ SOURCES = [os.path.join(CSRC, "nvfp4_api.cpp"), os.path.join(CSRC, "nvfp4_plan.c
            os.path.join(CSRC, "nvfp4_noalloc.hip"), os.path.join(CSRC, "nvfp4_mx_api.cpp"),
            os.path.join(CSRC, "nvfp4_mx_quantize.hip"), os.path.join(CSRC, "nvfp4_mx_gemm.hip"),
            os.path.join(CSRC, "nvfp4_moe.hip")]
+# the operators around the products of a layer (include/nvfp4_layer.h)
+LAYER_SOURCES = []
 # what the kernels that a plan table times, and their launches, are built from
 KERNEL_FILES = [os.path.join(CSRC, f) for f in ("nvfp4_kernels.hip", "nvfp4_grouped.hip",
                                                 "nvfp4_quantize.hip", "nvfp4_internal.h",
@@ -56,10 +60,8 @@ def build_id() -> str:
     return h.hexdigest()[:16]
 
 
-def build(verbose: bool = False) -> str:
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [hipcc(), *HIPCC_FLAGS, f"-DNVFP4_BUILD_ID=\"{build_id()}\"", "-I", INCLUDE, "-I", CSRC,
-           "-o", tmp, *SOURCES]
+def _hipcc(args: list[str], verbose: bool) -> None:
+    cmd = [hipcc(), *HIPCC_FLAGS, f"-DNVFP4_BUILD_ID=\"{build_id()}\"", "-I", INCLUDE, "-I", CSRC, *args]
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -69,6 +71,17 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError(f"hipcc failed ({res.returncode}):\n{err}")
     if verbose and err.strip():
         print(err, file=sys.stderr)
+
+
+def build(verbose: bool = False) -> str:
+    """Compiles every source, up to eight side by side, and links the library."""
+    tmp = LIB + f".tmp{os.getpid()}"
+    with tempfile.TemporaryDirectory() as d:
+        sources = SOURCES + LAYER_SOURCES
+        objects = [os.path.join(d, os.path.basename(s) + ".o") for s in sources]
+        with ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+            list(pool.map(lambda so: _hipcc(["-c", "-o", so[1], so[0]], verbose), zip(sources, objects)))
+        _hipcc(["-o", tmp, *objects], verbose)
     os.replace(tmp, LIB)
     return LIB
 
