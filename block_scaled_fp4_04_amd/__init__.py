@@ -686,6 +686,15 @@ class Sequence:
         self._check(fn(self._h, *args), fn.__name__)
         self._gpu, self._mx = gpu, mx
 
+    def _record_product(self, name: str, b, out, args: tuple, tensors: tuple, keep: list, epilogue) -> None:
+        from . import layer, mx
+        if epilogue is None:
+            return self._record(getattr(mx.mx_lib(), "nvfp4_sequence_add_" + name), args, tensors, keep)
+        args, more = epilogue._marshal(b, out, args)
+        # (the tensors themselves: the fields of an epilogue can be set again)
+        self._record(getattr(layer.layer_lib(), f"nvfp4_sequence_add_{name}_fused"), args, tensors + more,
+                     keep + list(more))
+
     @staticmethod
     def _given(out) -> None:
         """A call by itself makes its result; nobody could reach one that a
@@ -709,30 +718,30 @@ class Sequence:
         self._record(mx.mx_lib().nvfp4_sequence_add_mx_quantize, a[:2] + a[4:],
                      (x, out.codes, out.scales), [x, out])
 
-    def add_mx_gemm(self, a: "MxOperand", b: "MxOperand", out, alpha: float = 1.0) -> None:
-        """Records mx_gemm(a, b, alpha, out)."""
+    def add_mx_gemm(self, a: "MxOperand", b: "MxOperand", out, alpha: float = 1.0, epilogue=None) -> None:
+        """Records mx_gemm(a, b, alpha, out, epilogue=epilogue)."""
         from . import mx
         self._given(out)
         out, args = mx._gemm_args(a, b, alpha, out, None)
-        self._record(mx.mx_lib().nvfp4_sequence_add_mx_gemm, args,
-                     (a.codes, a.scales, b.codes, b.scales, out), [a, b, out])
+        self._record_product("mx_gemm", b, out, args, (a.codes, a.scales, b.codes, b.scales, out), [a, b, out],
+                             epilogue)
 
-    def add_mx_gemm_quantized(self, x, b: "MxOperand", out, alpha: float = 1.0) -> None:
-        """Records mx_gemm_quantized(x, b, alpha, out)."""
+    def add_mx_gemm_quantized(self, x, b: "MxOperand", out, alpha: float = 1.0, epilogue=None) -> None:
+        """Records mx_gemm_quantized(x, b, alpha, out, epilogue=epilogue)."""
         from . import mx
         self._given(out)
         out, args = mx._gemm_quantized_args(x, b, alpha, out, None)
-        self._record(mx.mx_lib().nvfp4_sequence_add_mx_gemm_quantized, args,
-                     (x, b.codes, b.scales, out), [x, b, out])
+        self._record_product("mx_gemm_quantized", b, out, args, (x, b.codes, b.scales, out), [x, b, out], epilogue)
 
     def add_mx_grouped_gemm(self, a: "MxOperand", b: "MxGroups", row_offsets, out,
-                            alpha: float = 1.0, rows=None) -> None:
-        """Records mx_grouped_gemm(a, b, row_offsets, alpha, rows, out)."""
+                            alpha: float = 1.0, rows=None, epilogue=None) -> None:
+        """Records mx_grouped_gemm(a, b, row_offsets, alpha, rows, out, epilogue=epilogue)."""
         from . import mx
         self._given(out)
         out, args = mx._grouped_args(a, b, row_offsets, alpha, rows, out, None)
-        self._record(mx.mx_lib().nvfp4_sequence_add_mx_grouped_gemm, args,
-                     (a.codes, a.scales, b.codes, b.scales, row_offsets, rows, out), [a, b, row_offsets, rows, out])
+        self._record_product("mx_grouped_gemm", b, out, args,
+                             (a.codes, a.scales, b.codes, b.scales, row_offsets, rows, out),
+                             [a, b, row_offsets, rows, out], epilogue)
 
     def add_moe_sort(self, expert_ids, out: "MoeRoute") -> None:
         """Records moe_sort(expert_ids, out.experts, out)."""
@@ -790,7 +799,8 @@ _LATER = {"mx": ("mx", "MX_BLOCK", "MX_EXPORTS", "MX_QUANT_ROWS", "TYPE_BF16", "
                  "mx_groups_to_device", "mx_linear", "mx_pack", "mx_packed_size", "mx_quantize",
                  "mx_to_device", "mx_unpack"),
           "moe": ("moe", "INDEX_I32", "INDEX_I64", "MOE_EXPORTS", "MOE_MAX_EXPERTS", "MoeRoute",
-                  "moe_combine", "moe_combine_grad", "moe_gather", "moe_gather_grad", "moe_sort")}
+                  "moe_combine", "moe_combine_grad", "moe_gather", "moe_gather_grad", "moe_sort"),
+          "layer": ("layer", "ACTIVATIONS", "LAYER_EXPORTS", "MxEpilogue")}
 
 
 def __getattr__(name: str):

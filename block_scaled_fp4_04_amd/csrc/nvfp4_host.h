@@ -40,6 +40,7 @@ struct Job {
     MxQuantArgs mx_quant{};
     MxGemmArgs mx_gemm{};
     MoeArgs moe{};
+    MxEpilogueArgs epilogue{};   // with mx_gemm
     bool empty = false;          // nothing to launch (a grouped GEMM with no rows)
 };
 
@@ -56,6 +57,19 @@ int prepare_quantize(const void* x, bool bf16, int64_t rows, int64_t K, int64_t 
 int prepare_gemm_quantized(const void* x, int x_type, int64_t ldx, const void* b_packed,
                            const void* b_scales, float alpha, void* out, int64_t M, int64_t N,
                            int64_t K, Job* job);
+
+int prepare_mx_quantize(bool inverse, const void* x, int x_type, int64_t groups,
+                        int64_t group_stride, int64_t rows, int64_t K, int64_t ld, void* codes,
+                        void* scales, Job* job);
+// x given: from activations; groups > 0: grouped.
+int prepare_mx_gemm(const void* a_packed, const void* a_scales, const void* x, int x_type,
+                    int64_t ldx, int64_t a_count, const int32_t* a_rows, const void* b_packed,
+                    const void* b_scales, const int32_t* row_offsets, int64_t groups, float alpha,
+                    void* out, int out_type, int64_t M, int64_t N, int64_t K, Job* job);
+int prepare_moe_sort(const void* ids, int id_type, int64_t tokens, int64_t topk, int64_t experts,
+                     int32_t* row_offsets, int32_t* slots, int32_t* row_tokens, Job* job);
+int prepare_moe_combine(const void* y, int type, int64_t tokens, int64_t topk, int64_t hidden,
+                        const int32_t* slots, const float* weights, void* out, Job* job);
 
 // The current device, checked to be a gfx950 GPU (status).
 int current_device(int* device);

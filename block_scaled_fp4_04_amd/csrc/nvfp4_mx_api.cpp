@@ -25,6 +25,10 @@ bool valid_rows_k(int64_t rows, int64_t K) {
 bool valid_type(int type) { return type == NVFP4_TYPE_F32 || type == NVFP4_TYPE_BF16; }
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
+}  // namespace
+
+namespace nvfp4 {
+
 int prepare_mx_quantize(bool inverse, const void* x, int x_type, int64_t groups,
                         int64_t group_stride, int64_t rows, int64_t K, int64_t ld, void* codes,
                         void* scales, Job* job) {
@@ -116,6 +120,10 @@ int prepare_mx_gemm(const void* a_packed, const void* a_scales, const void* x, i
     return job->empty || mx_gemm_fits(g) ? NVFP4_OK : NVFP4_ERR_INVALID_VALUE;
 }
 
+}  // namespace nvfp4
+
+namespace {
+
 int prepare_moe(int64_t tokens, int64_t topk, Job* job) {
     if (tokens < 0 || tokens >= ((int64_t)1 << 24) || topk < 1 || topk >= ((int64_t)1 << 24) ||
         tokens * topk > INT32_MAX)
@@ -126,6 +134,10 @@ int prepare_moe(int64_t tokens, int64_t topk, Job* job) {
     job->moe.topk = (int)topk;
     return NVFP4_OK;
 }
+
+}  // namespace
+
+namespace nvfp4 {
 
 int prepare_moe_sort(const void* ids, int id_type, int64_t tokens, int64_t topk, int64_t experts,
                      int32_t* row_offsets, int32_t* slots, int32_t* row_tokens, Job* job) {
@@ -147,6 +159,10 @@ int prepare_moe_sort(const void* ids, int id_type, int64_t tokens, int64_t topk,
     job->launch = +[](const Job& j, hipStream_t s) { return launch_moe_sort(j.moe, s); };
     return NVFP4_OK;
 }
+
+}  // namespace nvfp4
+
+namespace {
 
 // The row operators: x and out, and for the gradient y and dweights.
 int prepare_moe_rows(const void* x, const void* y, int type, int64_t tokens, int64_t topk,
@@ -185,6 +201,10 @@ int prepare_moe_gather(const void* x, int type, int64_t tokens, int64_t topk, in
     return st;
 }
 
+}  // namespace
+
+namespace nvfp4 {
+
 int prepare_moe_combine(const void* y, int type, int64_t tokens, int64_t topk, int64_t hidden,
                         const int32_t* slots, const float* weights, void* out, Job* job) {
     const int st = prepare_moe_rows(y, nullptr, type, tokens, topk, hidden, hidden, slots, weights,
@@ -193,6 +213,10 @@ int prepare_moe_combine(const void* y, int type, int64_t tokens, int64_t topk, i
         job->launch = +[](const Job& j, hipStream_t s) { return launch_moe_combine(j.moe, s); };
     return st;
 }
+
+}  // namespace nvfp4
+
+namespace {
 
 int run(int status, const Job& job, void* stream) {
     return status != NVFP4_OK ? status : run_job(job, stream);

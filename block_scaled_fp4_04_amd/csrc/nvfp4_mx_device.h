@@ -126,6 +126,45 @@ __device__ __forceinline__ mx_f16 mx_mfma32(const mx_u4& a, uint32_t sa, const m
 __device__ __forceinline__ uint16_t mx_to_bf16(float x) {
     return __builtin_bit_cast(uint16_t, (__bf16)x);
 }
+// The low or high bfloat16 of a word.
+__device__ __forceinline__ float mx_widen(uint32_t w, int high) {
+    return __builtin_bit_cast(float, high ? w & 0xFFFF0000u : w << 16);
+}
+
+// Activations (kMxAct*, uniform), in fp32:
+//   silu       z / (1 + exp(-z))
+//   gelu       z (1 + erf(z / sqrt 2)) / 2
+//   gelu_tanh  z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2, which is
+//              z / (1 + exp(-2 sqrt(2 / pi) (z + 0.044715 z^3)))
+// The exponential is the hardware's power of two of a product rounded to fp32,
+// the quotient a product with the hardware's reciprocal: each is off by an
+// ulp or two, and by |z| 2^-24 of the exponential for the rounded product.
+__device__ __forceinline__ float mx_logistic(float z) {  // 1 / (1 + exp(-z))
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * z));
+}
+__device__ __forceinline__ mx_f4 mx_act(mx_f4 z, int act) {
+    switch (act) {
+        case kMxActRelu:
+#pragma unroll
+            for (int v = 0; v < 4; ++v) z[v] = z[v] < 0.0f ? 0.0f : z[v];
+            break;
+        case kMxActSilu:
+#pragma unroll
+            for (int v = 0; v < 4; ++v) z[v] *= mx_logistic(z[v]);
+            break;
+        case kMxActGelu:
+#pragma unroll
+            for (int v = 0; v < 4; ++v) z[v] = 0.5f * z[v] * (1.0f + erff(z[v] * 0.70710678f));
+            break;
+        case kMxActGeluTanh:
+#pragma unroll
+            for (int v = 0; v < 4; ++v) z[v] *= mx_logistic(1.59576912f * z[v] * (1.0f + 0.044715f * z[v] * z[v]));
+            break;
+        default:
+            break;
+    }
+    return z;
+}
 
 }  // namespace
 }  // namespace nvfp4

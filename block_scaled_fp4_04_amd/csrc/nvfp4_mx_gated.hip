@@ -1,0 +1,19 @@
+// nvfp4_mx_gated.hip -- the MXFP4 product with a gate operand, biases, activation and residual
+// (nvfp4_mx_product.h).
+#include "nvfp4_mx_product.h"
+
+namespace nvfp4 {
+
+hipError_t launch_mx_gated(const MxGemmArgs& a, const MxEpilogueArgs& e, hipStream_t stream) {
+    Launch<EPI_GATED> l{a, {e}, stream, false, 0, hipSuccess};
+    choose(l);
+    return l.error;
+}
+
+bool mx_gated_fits(const MxGemmArgs& a) {
+    Launch<EPI_GATED> l{a, {}, nullptr, true, 0, hipSuccess};
+    choose(l);
+    return l.items < ((int64_t)1 << 32);
+}
+
+}  // namespace nvfp4

@@ -75,12 +75,29 @@ struct MxGemmArgs {
     int groups;
     bool x_bf16, out_bf16;
 };
+// What an epilogue adds to the product (include/nvfp4_layer.h).
+enum { kMxActNone = 0, kMxActRelu = 1, kMxActSilu = 2, kMxActGelu = 3, kMxActGeluTanh = 4 };
+struct MxEpilogueArgs {
+    const uint8_t* gate_codes;   // the gate operand(s), like B, or null
+    const uint8_t* gate_scales;
+    const void* bias;            // (groups x) N values, or null
+    const void* gate_bias;
+    const void* residual;        // M x N of the output's type, row stride ldr, or null
+    int64_t ldr;
+    int act;                     // kMxAct*
+    bool bias_bf16;
+};
 // Rows of A up to which the one-launch product from activations runs.
 constexpr int kMxQuantRows = 16;
 hipError_t launch_mx_gemm(const MxGemmArgs& a, hipStream_t stream);
 // Whether the grid of the kernel that the sizes choose stays within the
 // runtime's limit on work-items.
 bool mx_gemm_fits(const MxGemmArgs& a);
+// The same with an epilogue.
+hipError_t launch_mx_fused(const MxGemmArgs& a, const MxEpilogueArgs& e, hipStream_t stream);
+hipError_t launch_mx_gated(const MxGemmArgs& a, const MxEpilogueArgs& e, hipStream_t stream);
+bool mx_fused_fits(const MxGemmArgs& a);
+bool mx_gated_fits(const MxGemmArgs& a);
 
 // Expert routing.
 constexpr int kMoeMaxExperts = 2048;

@@ -15,6 +15,7 @@ backward form.
 from __future__ import annotations
 
 import ctypes
+import dataclasses
 from dataclasses import dataclass
 
 import numpy as np
@@ -324,6 +325,15 @@ def mx_dequantize(a, dtype=None, out=None, stream=None):
     return out
 
 
+def _product(name: str, b, out, args: tuple, tensors: tuple, epilogue) -> None:
+    """Runs a product, with its epilogue if it has one."""
+    if epilogue is None:
+        return _run(getattr(mx_lib(), name), args, tensors)
+    from . import layer
+    args, more = epilogue._marshal(b, out, args)
+    _run(getattr(layer.layer_lib(), name + "_fused"), args, tensors + more)
+
+
 def _gemm_args(a, b, alpha, out, dtype):
     _kind(a, "a", MxOperand)
     _kind(b, "b", MxOperand)
@@ -336,14 +346,16 @@ def _gemm_args(a, b, alpha, out, dtype):
                  float(alpha), out.data_ptr(), kind, a.rows, b.rows, a.K)
 
 
-def mx_gemm(a: MxOperand, b: MxOperand, alpha: float = 1.0, out=None, dtype=None, stream=None):
+def mx_gemm(a: MxOperand, b: MxOperand, alpha: float = 1.0, out=None, dtype=None, stream=None,
+            epilogue=None):
     """C = alpha * (A . B^T) of packed MXFP4 operands (nvfp4_mx_gemm): M x N,
-    bfloat16 unless ``dtype`` or ``out`` says float32."""
+    bfloat16 unless ``dtype`` or ``out`` says float32; with an ``epilogue``
+    (MxEpilogue), nvfp4_mx_gemm_fused."""
     if stream is not None:
         with _on(stream, a.codes):
-            return mx_gemm(a, b, alpha, out, dtype)
+            return mx_gemm(a, b, alpha, out, dtype, epilogue=epilogue)
     out, args = _gemm_args(a, b, alpha, out, dtype)
-    _run(mx_lib().nvfp4_mx_gemm, args, (a.codes, a.scales, b.codes, b.scales, out))
+    _product("nvfp4_mx_gemm", b, out, args, (a.codes, a.scales, b.codes, b.scales, out), epilogue)
     return out
 
 
@@ -359,32 +371,40 @@ def _gemm_quantized_args(x, b, alpha, out, dtype):
                  float(alpha), out.data_ptr(), out_kind, M, b.rows, K)
 
 
-def mx_gemm_quantized(x, b: MxOperand, alpha: float = 1.0, out=None, dtype=None, stream=None):
+def mx_gemm_quantized(x, b: MxOperand, alpha: float = 1.0, out=None, dtype=None, stream=None,
+                      epilogue=None):
     """mx_gemm(mx_quantize(x), b, alpha) in one launch, bit for bit
-    (nvfp4_mx_gemm_quantized): x holds up to MX_QUANT_ROWS rows of fp32 or
+    (nvfp4_mx_gemm_quantized, or with an ``epilogue``
+    nvfp4_mx_gemm_quantized_fused): x holds up to MX_QUANT_ROWS rows of fp32 or
     bfloat16 activations."""
     if stream is not None:
         with _on(stream, x):
-            return mx_gemm_quantized(x, b, alpha, out, dtype)
+            return mx_gemm_quantized(x, b, alpha, out, dtype, epilogue=epilogue)
     out, args = _gemm_quantized_args(x, b, alpha, out, dtype)
-    _run(mx_lib().nvfp4_mx_gemm_quantized, args, (x, b.codes, b.scales, out))
+    _product("nvfp4_mx_gemm_quantized", b, out, args, (x, b.codes, b.scales, out), epilogue)
     return out
 
 
-def mx_linear(x, b: MxOperand, alpha: float = 1.0, out=None, dtype=None, stream=None):
+def mx_linear(x, b: MxOperand, alpha: float = 1.0, out=None, dtype=None, stream=None, epilogue=None):
     """C = alpha * (quantise(x) . B^T) for plain activations x (rows x K,
     fp32 or bfloat16): one launch (mx_gemm_quantized) for few rows, else
     mx_quantize and mx_gemm.  Both give the same bits.  Dimensions in front of
     K (batch x sequence x K) are rows, and C has them in front of N; an x whose
-    rows do not follow each other at one stride is copied first."""
+    rows do not follow each other at one stride is copied first, and so is such a
+    residual of the ``epilogue``."""
     if stream is not None:
         with _on(stream, x):
-            return mx_linear(x, b, alpha, out, dtype)
+            return mx_linear(x, b, alpha, out, dtype, epilogue=epilogue)
     if x.dim() > 2:
         shape = (*x.shape[:-1], b.rows)
         if out is not None and (tuple(out.shape) != shape or not out.is_contiguous()):
             raise ValueError(f"out must be a contiguous tensor of shape {shape}")
-        c = mx_linear(x.flatten(0, -2), b, alpha, None if out is None else out.flatten(0, -2), dtype)
+        if epilogue is not None and epilogue.residual is not None:
+            if tuple(epilogue.residual.shape) != shape:
+                raise ValueError(f"residual must be a tensor of shape {shape}")
+            epilogue = dataclasses.replace(epilogue, residual=epilogue.residual.flatten(0, -2))
+        c = mx_linear(x.flatten(0, -2), b, alpha, None if out is None else out.flatten(0, -2), dtype,
+                      epilogue=epilogue)
         return c.view(shape) if out is None else out
     # (one launch: 16 x 65536 x 8192 52 us, 57 + 2.7 in two; 1 x 6144 x 6144 6.9, 6.4
     # + 2.7.  Behind K = 8192 every 16 columns quantise the rows again, which takes
@@ -392,9 +412,9 @@ def mx_linear(x, b: MxOperand, alpha: float = 1.0, out=None, dtype=None, stream=
     # other call's 8.)
     if x.dim() == 2 and x.shape[0] <= MX_QUANT_ROWS and (
             b.K <= 8192 or b.rows * b.K * (6 + x.shape[0]) <= 800_000_000):
-        return mx_gemm_quantized(x, b, alpha, out, dtype)
+        return mx_gemm_quantized(x, b, alpha, out, dtype, epilogue=epilogue)
     _kind(b, "b", MxOperand)
-    return mx_gemm(mx_quantize(x), b, alpha, out, dtype)
+    return mx_gemm(mx_quantize(x), b, alpha, out, dtype, epilogue=epilogue)
 
 
 def _grouped_args(a, b, row_offsets, alpha, rows, out, dtype):
@@ -419,17 +439,19 @@ def _grouped_args(a, b, row_offsets, alpha, rows, out, dtype):
 
 
 def mx_grouped_gemm(a: MxOperand, b: MxGroups, row_offsets, alpha: float = 1.0, rows=None,
-                    out=None, dtype=None, stream=None):
+                    out=None, dtype=None, stream=None, epilogue=None):
     """Grouped product (nvfp4_mx_grouped_gemm): rows row_offsets[g] ..
     row_offsets[g+1]-1 of C belong to group g, whose weights are b's g-th
     operand.  Row r of C takes row rows[r] of A (``MoeRoute.tokens``: the
     activations are quantised once per token and never copied), or row r
     without ``rows``.  Rows behind the last group are left as they were: in an
-    ``out`` that the call makes they hold anything."""
+    ``out`` that the call makes they hold anything.  With an ``epilogue``,
+    nvfp4_mx_grouped_gemm_fused: its gate is an MxGroups, its biases [groups, N],
+    its residual has C's rows."""
     if stream is not None:
         with _on(stream, a.codes):
-            return mx_grouped_gemm(a, b, row_offsets, alpha, rows, out, dtype)
+            return mx_grouped_gemm(a, b, row_offsets, alpha, rows, out, dtype, epilogue=epilogue)
     out, args = _grouped_args(a, b, row_offsets, alpha, rows, out, dtype)
-    _run(mx_lib().nvfp4_mx_grouped_gemm, args,
-         (a.codes, a.scales, b.codes, b.scales, row_offsets, rows, out))
+    _product("nvfp4_mx_grouped_gemm", b, out, args,
+             (a.codes, a.scales, b.codes, b.scales, row_offsets, rows, out), epilogue)
     return out
