@@ -766,6 +766,18 @@ class Sequence:
         self._record(moe.moe_lib().nvfp4_sequence_add_moe_combine, args,
                      (y, route.slots, weights, out), [y, route, weights, out])
 
+    def add_norm(self, y, residual, h, n=None, **how) -> None:
+        """Records add_norm(y, residual, h=h, n=n, **how); h None: not kept (as rms_norm).  n is an MxOperand with
+        quantize=True."""
+        from . import layer
+        pre = how.setdefault("pre", True)
+        if pre and n is None or not pre and h is None:
+            raise ValueError("a recorded call needs an out")
+        how = {"post_weight": None, "gate": None, "pre_weight": None, "scale": 1.0, "residual_scale": 1.0, "eps": 1e-6,
+               "post": None, "quantize": False, **how}
+        _, _, args, tensors = layer._norm_args(y, residual, h=h, n=n, keep=h is not None, **how)
+        self._record(layer.layer_lib().nvfp4_sequence_add_norm, args, tensors, list(tensors))
+
     def finalize(self) -> None:
         with self._on_gpu():
             st = lib().nvfp4_sequence_finalize(self._h)
@@ -800,7 +812,8 @@ _LATER = {"mx": ("mx", "MX_BLOCK", "MX_EXPORTS", "MX_QUANT_ROWS", "TYPE_BF16", "
                  "mx_to_device", "mx_unpack"),
           "moe": ("moe", "INDEX_I32", "INDEX_I64", "MOE_EXPORTS", "MOE_MAX_EXPERTS", "MoeRoute",
                   "moe_combine", "moe_combine_grad", "moe_gather", "moe_gather_grad", "moe_sort"),
-          "layer": ("layer", "ACTIVATIONS", "LAYER_EXPORTS", "MxEpilogue")}
+          "layer": ("layer", "ACTIVATIONS", "LAYER_EXPORTS", "MxEpilogue", "NORM_MAX_HIDDEN", "NormGrads", "add_norm",
+                    "add_norm_grad", "rms_norm")}
 
 
 def __getattr__(name: str):

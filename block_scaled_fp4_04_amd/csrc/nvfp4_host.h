@@ -41,6 +41,7 @@ struct Job {
     MxGemmArgs mx_gemm{};
     MoeArgs moe{};
     MxEpilogueArgs epilogue{};   // with mx_gemm
+    NormArgs norm{};
     bool empty = false;          // nothing to launch (a grouped GEMM with no rows)
 };
 

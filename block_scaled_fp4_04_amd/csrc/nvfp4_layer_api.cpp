@@ -3,6 +3,8 @@
 // eager entry points run and the sequences record.
 #include <hip/hip_runtime.h>
 
+#include <cstdint>
+
 #include "nvfp4_host.h"
 #include "nvfp4_layer.h"
 
@@ -14,6 +16,9 @@ static_assert((int)NVFP4_ACT_NONE == kMxActNone && (int)NVFP4_ACT_RELU == kMxAct
                   (int)NVFP4_ACT_SILU == kMxActSilu && (int)NVFP4_ACT_GELU == kMxActGelu &&
                   (int)NVFP4_ACT_GELU_TANH == kMxActGeluTanh,
               "the kernels' activations are the header's");
+static_assert((int)NVFP4_GATE_CHANNEL == kGateChannel && (int)NVFP4_GATE_ELEMENT == kGateElement &&
+                  NVFP4_NORM_MAX_HIDDEN == kNormMaxHidden,
+              "and so are the gates and the rows' length");
 
 constexpr int64_t kMaxDim = (int64_t)1 << 30;
 
@@ -84,9 +89,146 @@ int prepare_grouped_fused(const void* a_packed, const void* a_scales, int64_t a_
     return add_epilogue(st, e, out_type, job);
 }
 
+// What forward and gradient share: the operator itself.
+int check_norm(const nvfp4_norm* f, NormArgs* a) {
+    if (!f || !valid_type(f->type) || f->rows < 0 || f->rows > INT32_MAX || f->hidden < 1 ||
+        f->hidden > kNormMaxHidden || f->gate_mode < NVFP4_GATE_NONE || f->gate_mode > NVFP4_GATE_ELEMENT ||
+        (f->gate_mode != NVFP4_GATE_NONE && !f->gate && f->rows > 0) || !(f->eps >= 0.0f))
+        return NVFP4_ERR_INVALID_VALUE;
+    const void* const post_weight = f->post ? f->post_weight : nullptr;
+    const void* const pre_weight = f->pre ? f->pre_weight : nullptr;
+    const bool element = f->gate_mode == NVFP4_GATE_ELEMENT, channel = f->gate_mode == NVFP4_GATE_CHANNEL;
+    if ((post_weight || pre_weight || channel) && !valid_type(f->weight_type)) return NVFP4_ERR_INVALID_VALUE;
+    a->ld_gate = f->rows > 1 ? f->ld_gate : f->hidden;
+    if (element && (a->ld_gate < f->hidden || a->ld_gate > kMaxDim)) return NVFP4_ERR_INVALID_VALUE;
+    const uintptr_t weight_size = size_of(f->weight_type);
+    if (!aligned(post_weight, weight_size) || !aligned(pre_weight, weight_size) ||
+        (channel && !aligned(f->gate, weight_size)) || (element && !aligned(f->gate, size_of(f->type))))
+        return NVFP4_ERR_MISALIGNED;
+    a->bf16 = f->type == NVFP4_TYPE_BF16;
+    a->weight_bf16 = f->weight_type == NVFP4_TYPE_BF16;
+    a->post = f->post != 0;
+    a->pre = f->pre != 0;
+    a->gate_mode = f->gate_mode;
+    a->hidden = (int)f->hidden;
+    a->rows = f->rows;
+    a->post_weight = post_weight;
+    a->pre_weight = pre_weight;
+    a->gate = f->gate;
+    a->scale = f->scale;
+    a->residual_scale = f->residual_scale;
+    a->eps = f->eps;
+    return NVFP4_OK;
+}
+
+// A row stride to read rows of `hidden` elements with; 0 if it is too small.
+int64_t stride_of(const NormArgs& a, int64_t ld) {
+    if (a.rows <= 1) return a.hidden;
+    return ld < a.hidden || ld > kMaxDim ? 0 : ld;
+}
+
+int prepare_norm(const nvfp4_norm* f, const void* y, int64_t ld_y, const void* residual,
+                 int64_t ld_residual, void* h, void* n, void* n_codes, void* n_scales, Job* job) {
+    *job = Job{};
+    NormArgs& a = job->norm;
+    const int st = check_norm(f, &a);
+    if (st != NVFP4_OK) return st;
+    const bool packed = n_codes || n_scales;
+    a.ld_y = stride_of(a, ld_y);
+    a.ld_residual = residual ? stride_of(a, ld_residual) : a.hidden;
+    if ((packed && (!n_codes || !n_scales || n || a.hidden % kMxBlock)) || !a.ld_y || !a.ld_residual)
+        return NVFP4_ERR_INVALID_VALUE;
+    if (a.rows > 0 && (!y || (a.pre ? !n && !packed : n || packed || !h))) return NVFP4_ERR_INVALID_VALUE;
+    const uintptr_t size = size_of(f->type);
+    if (!aligned(y, size) || !aligned(residual, size) || !aligned(h, size) || !aligned(n, size) ||
+        !aligned(n_codes, 16) || !aligned(n_scales, 16))
+        return NVFP4_ERR_MISALIGNED;
+    a.y = y;
+    a.residual = residual;
+    a.h = h;
+    a.n = n;
+    a.codes = static_cast<uint8_t*>(n_codes);
+    a.scales = static_cast<uint8_t*>(n_scales);
+    job->kind = JOB_LAUNCH;
+    job->empty = a.rows == 0;
+    job->launch = +[](const Job& j, hipStream_t s) { return launch_norm(j.norm, s); };
+    return NVFP4_OK;
+}
+
+size_t grad_workspace(const NormArgs& a) {
+    if (a.rows == 0 || !(a.post || a.pre || a.gate_mode == kGateChannel)) return 0;
+    return (size_t)norm_grad_parts(a.bf16, a.rows, a.hidden) * 3 * a.hidden * sizeof(float);
+}
+
 }  // namespace
 
 extern "C" {
+
+int nvfp4_add_norm(const nvfp4_norm* norm, const void* y, int64_t ld_y, const void* residual,
+                   int64_t ld_residual, void* h, void* n, void* n_codes, void* n_scales,
+                   void* stream) {
+    Job job;
+    const int st = prepare_norm(norm, y, ld_y, residual, ld_residual, h, n, n_codes, n_scales, &job);
+    return run(st, job, stream);
+}
+
+int nvfp4_sequence_add_norm(nvfp4_sequence_t seq, const nvfp4_norm* norm, const void* y,
+                            int64_t ld_y, const void* residual, int64_t ld_residual, void* h,
+                            void* n, void* n_codes, void* n_scales) {
+    Job job;
+    const int st = prepare_norm(norm, y, ld_y, residual, ld_residual, h, n, n_codes, n_scales, &job);
+    return sequence_add(seq, st, job);
+}
+
+int nvfp4_add_norm_grad_workspace(const nvfp4_norm* norm, size_t* bytes) {
+    NormArgs a{};
+    const int st = check_norm(norm, &a);
+    if (st != NVFP4_OK || !bytes) return st != NVFP4_OK ? st : NVFP4_ERR_INVALID_VALUE;
+    *bytes = grad_workspace(a);
+    return NVFP4_OK;
+}
+
+int nvfp4_add_norm_grad(const nvfp4_norm* norm, const void* dh, int64_t ld_dh, const void* dn,
+                        int64_t ld_dn, const void* y, int64_t ld_y, const void* h, int64_t ld_h,
+                        void* dy, void* dresidual, void* dgate, float* dpost_weight,
+                        float* dpre_weight, void* workspace, size_t workspace_bytes, void* stream) {
+    Job job;
+    NormArgs& a = job.norm;
+    const int st = check_norm(norm, &a);
+    if (st != NVFP4_OK) return st;
+    const bool channel = a.gate_mode == kGateChannel, reads_y = a.post || a.gate_mode != kGateNone;
+    const bool summed = (channel && dgate) || dpost_weight || dpre_weight;
+    a.ld_dh = dh ? stride_of(a, ld_dh) : a.hidden;
+    a.ld_dn = dn ? stride_of(a, ld_dn) : a.hidden;
+    a.ld_y = reads_y ? stride_of(a, ld_y) : a.hidden;
+    a.ld_h = a.pre ? stride_of(a, ld_h) : a.hidden;
+    if (!a.ld_dh || !a.ld_dn || !a.ld_y || !a.ld_h || (dgate && a.gate_mode == kGateNone) ||
+        (dpost_weight && !a.post) || (dpre_weight && !a.pre) || (dn && !a.pre))
+        return NVFP4_ERR_INVALID_VALUE;
+    // (without rows the sums are zeros all the same)
+    if (a.rows > 0 && ((reads_y && !y) || (a.pre && (!h || !dn)))) return NVFP4_ERR_INVALID_VALUE;
+    if (a.rows > 0 && summed && (!workspace || workspace_bytes < grad_workspace(a))) return NVFP4_ERR_INVALID_VALUE;
+    const uintptr_t size = size_of(norm->type);
+    if (!aligned(dh, size) || !aligned(dn, size) || !aligned(y, size) || !aligned(h, size) || !aligned(dy, size) ||
+        !aligned(dresidual, size) || !aligned(dgate, channel ? 4 : size) || !aligned(dpost_weight, 4) ||
+        !aligned(dpre_weight, 4) || !aligned(workspace, 16))
+        return NVFP4_ERR_MISALIGNED;
+    a.dh = dh;
+    a.dn = dn;
+    a.y = y;
+    a.h_in = h;
+    a.dy = dy;
+    a.dresidual = dresidual;
+    a.dgate = dgate;
+    a.dpost_weight = dpost_weight;
+    a.dpre_weight = dpre_weight;
+    a.partials = summed ? static_cast<float*>(workspace) : nullptr;
+    a.parts = a.rows > 0 ? norm_grad_parts(a.bf16, a.rows, a.hidden) : 0;
+    job.kind = JOB_LAUNCH;
+    job.empty = a.rows == 0 ? !summed : !dy && !dresidual && !dgate && !summed;
+    job.launch = +[](const Job& j, hipStream_t s) { return launch_norm_grad(j.norm, s); };
+    return run_job(job, stream);
+}
 
 int nvfp4_mx_gemm_fused(const void* a_packed, const void* a_scales, const void* b_packed,
                         const void* b_scales, float alpha, const nvfp4_mx_epilogue* epilogue,

@@ -58,6 +58,18 @@ __device__ __forceinline__ uint32_t mx_top(const mx_u4& v) {
         return top;
     }
 }
+// The largest of `top` over the LPB lanes (4 or 8, side by side) of a block.
+template <int CTRL>
+__device__ __forceinline__ uint32_t mx_dpp(uint32_t x) {
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, CTRL, 0xF, 0xF, true);
+}
+template <int LPB>
+__device__ __forceinline__ uint32_t mx_block_top(uint32_t top) {
+    top = max(top, mx_dpp<0xB1>(top));   // lane ^ 1
+    top = max(top, mx_dpp<0x4E>(top));   // lane ^ 2
+    if constexpr (LPB == 8) top = max(top, mx_dpp<0x141>(top));  // 7 - lane, of 8
+    return top;
+}
 // The codes of the same values under scale s: a word from bfloat16 ones, half
 // HALF of word c from fp32 ones.  The conversion divides by the scale exactly
 // (a power of two), rounds to the nearest E2M1 value, ties to the even code,

@@ -122,4 +122,32 @@ hipError_t launch_moe_gather(const MoeArgs& a, hipStream_t stream);
 hipError_t launch_moe_combine(const MoeArgs& a, hipStream_t stream);
 hipError_t launch_moe_combine_grad(const MoeArgs& a, hipStream_t stream);
 
+// Norms around a block's residual (include/nvfp4_layer.h).
+constexpr int kNormMaxHidden = 16384;
+enum { kGateNone = 0, kGateChannel = 1, kGateElement = 2 };
+struct NormArgs {
+    bool bf16, weight_bf16, post, pre;
+    int gate_mode;               // kGate*
+    int hidden;
+    int64_t rows;
+    const void *post_weight, *pre_weight, *gate;
+    const void *y, *residual;    // residual: or null
+    int64_t ld_y, ld_residual, ld_gate;
+    float scale, residual_scale, eps;
+    // forward: results, each or null
+    void *h, *n;
+    uint8_t *codes, *scales;     // n packed
+    // gradients
+    const void *dh, *dn, *h_in;  // dh, dn: or null
+    int64_t ld_dh, ld_dn, ld_h;
+    void *dy, *dresidual, *dgate;
+    float *dpost_weight, *dpre_weight;
+    float* partials;             // [parts][3][hidden]
+    int parts;                   // workgroups that leave partial sums
+};
+hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
+hipError_t launch_norm_grad(const NormArgs& a, hipStream_t stream);
+// Workgroups that launch_norm_grad runs on rows x hidden.
+int norm_grad_parts(bool bf16, int64_t rows, int hidden);
+
 }  // namespace nvfp4

@@ -23,11 +23,6 @@ namespace {
 // codes go through LDS, from where lane l stores bytes 16 l ... of the
 // fragment.  NT: non-temporal loads, for inputs of more than kStreamBytes
 // (105 us; 116 without; 16384 x 8192 bfloat16 54 and 59 us).
-template <int CTRL>
-__device__ __forceinline__ uint32_t mx_dpp(uint32_t x) {
-    return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, CTRL, 0xF, 0xF, true);
-}
-
 template <typename T, bool NT>
 __global__ void __launch_bounds__(256) mx_quantize_kernel(MxQuantArgs a) {
     constexpr int E = 16 / (int)sizeof(T);     // elements of a load
@@ -60,9 +55,7 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(MxQuantArgs a) {
     for (int i = 0; i < L; ++i) {
         if (row0 + i * RPL >= a.rows || k >= a.K) v[i] = mx_u4{0, 0, 0, 0};
         uint32_t top = mx_top<T>(v[i]);
-        top = max(top, mx_dpp<0xB1>(top));   // lane ^ 1
-        top = max(top, mx_dpp<0x4E>(top));   // lane ^ 2
-        if constexpr (LPB == 8) top = max(top, mx_dpp<0x141>(top));  // 7 - lane, of 8
+        top = mx_block_top<LPB>(top);
         const uint32_t byte = mx_scale_byte(top);
         const uint32_t w = byte == 255u ? 0u : mx_codes<T, 0>(0, v[i], mx_scale(byte));
         const int r = i * RPL + lane / LPR;

@@ -10,22 +10,33 @@ the package.
     h = mx_linear(x, w_up, epilogue=gated)
     x = mx_linear(h, w_down, epilogue=MxEpilogue(bias=b, residual=x))
 
-The products have no backward form, with an epilogue as without: results carry
-no autograd history.
+``add_norm`` is what stands between two blocks: the norm behind one, its gate
+and the residual, and the norm before the next, as rows or as a packed MXFP4
+operand; ``rms_norm`` the norm alone.
+
+The products have no backward form, with an epilogue as without.  The gradients
+of ``add_norm`` are a function of their own (``add_norm_grad``): nothing here is
+recorded by autograd, and results carry no history.
 """
 from __future__ import annotations
 
 import ctypes
 from dataclasses import dataclass
 
-from . import _i64, _vp, lib
-from .mx import _GEMM, _GEMM_Q, _GROUPED, _KINDS, _kind
+import torch
+
+from . import Nvfp4Error, _i64, _vp, lib
+from .mx import (MX_BLOCK, _GEMM, _GEMM_Q, _GROUPED, _KINDS, MxOperand, _kind, _on, _packed, _run, _type_of)
 
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}   # NVFP4_ACT_*
 
 LAYER_EXPORTS = ["nvfp4_mx_gemm_fused", "nvfp4_mx_gemm_quantized_fused", "nvfp4_mx_grouped_gemm_fused",
                  "nvfp4_sequence_add_mx_gemm_fused", "nvfp4_sequence_add_mx_gemm_quantized_fused",
-                 "nvfp4_sequence_add_mx_grouped_gemm_fused"]
+                 "nvfp4_sequence_add_mx_grouped_gemm_fused", "nvfp4_add_norm", "nvfp4_sequence_add_norm",
+                 "nvfp4_add_norm_grad", "nvfp4_add_norm_grad_workspace"]
+
+GATE_NONE, GATE_CHANNEL, GATE_ELEMENT = 0, 1, 2   # NVFP4_GATE_*
+NORM_MAX_HIDDEN = 16384
 
 _int, _f32 = ctypes.c_int, ctypes.c_float
 _bound = None
@@ -36,7 +47,15 @@ class _EpilogueT(ctypes.Structure):
                 ("bias_type", _int), ("residual", _vp), ("ld_residual", _i64)]
 
 
-_epi = ctypes.POINTER(_EpilogueT)
+class _NormT(ctypes.Structure):
+    _fields_ = [("type", _int), ("weight_type", _int), ("rows", _i64), ("hidden", _i64), ("post", _int), ("pre", _int),
+                ("post_weight", _vp), ("pre_weight", _vp), ("gate_mode", _int), ("gate", _vp), ("ld_gate", _i64),
+                ("scale", _f32), ("residual_scale", _f32), ("eps", _f32)]
+
+
+_epi, _norm_p, _size = ctypes.POINTER(_EpilogueT), ctypes.POINTER(_NormT), ctypes.c_size_t
+_NORM = [_norm_p, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp]
+_NORM_GRAD = [_norm_p, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _size]
 
 
 def _with_epilogue(types: list) -> list:
@@ -56,6 +75,11 @@ def layer_lib() -> ctypes.CDLL:
             f, g = getattr(L, "nvfp4_" + name), getattr(L, "nvfp4_sequence_add_" + name)
             f.restype = g.restype = _int
             f.argtypes, g.argtypes = types + [_vp], [_vp] + types
+        for name, types in (("nvfp4_add_norm", _NORM + [_vp]), ("nvfp4_sequence_add_norm", [_vp] + _NORM),
+                            ("nvfp4_add_norm_grad", _NORM_GRAD + [_vp]),
+                            ("nvfp4_add_norm_grad_workspace", [_norm_p, ctypes.POINTER(_size)])):
+            f = getattr(L, name)
+            f.restype, f.argtypes = _int, types
         _bound = L
     return L
 
@@ -122,3 +146,189 @@ class MxEpilogue:
         # (alpha is the one float among the arguments)
         at = next(i for i, a in enumerate(args) if type(a) is float) + 1
         return args[:at] + (e,) + args[at:], tensors
+
+
+# ---- norms ------------------------------------------------------------------
+
+
+def _rows_of(name: str, t, shape, dtype):
+    """t (rows may be strided; dimensions in front of the last are rows) as a
+    2-D tensor; None for none.  A t whose rows do not follow each other at one
+    stride, of a row at least, is copied."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)}")
+    t = t if t.dim() == 2 else t.reshape(-1, shape[-1])
+    rows, H = t.shape
+    return t if (t.stride(1) == 1 or H == 1) and (t.stride(0) >= H or rows <= 1) else t.contiguous()
+
+
+def _spec(y, post_weight, gate, pre_weight, scale, residual_scale, eps, post: bool, pre: bool):
+    """(the operator's C description, its gate as rows if it has one for every
+    element, the tensors that it names)."""
+    if y.dim() < 2:
+        raise ValueError("rows must be a tensor of at least two dimensions")
+    H, kind = y.shape[-1], _type_of(y.dtype, "rows")
+    if not 1 <= H <= NORM_MAX_HIDDEN:
+        raise ValueError(f"rows must have 1 to {NORM_MAX_HIDDEN} elements, not {H}")
+    mode, rows = GATE_NONE, None
+    weights = [("post_weight", post_weight), ("pre_weight", pre_weight)]
+    if post_weight is not None and not post or pre_weight is not None and not pre:
+        raise ValueError("a weight without its norm")
+    if gate is not None:
+        if gate.shape == y.shape:
+            mode, rows = GATE_ELEMENT, _rows_of("gate", gate, y.shape, y.dtype)
+        else:
+            mode = GATE_CHANNEL
+            weights.append(("gate", gate))
+    weight_type = None
+    for name, w in weights:
+        if w is None:
+            continue
+        if tuple(w.shape) != (H,) or not w.is_contiguous() or w.dtype not in _KINDS:
+            raise ValueError(f"{name} must be a contiguous float32 or bfloat16 tensor of shape ({H},)"
+                             + (f" or {tuple(y.shape)}" if name == "gate" else ""))
+        if weight_type not in (None, w.dtype):
+            raise ValueError("the weights (and a gate for each channel) must be of one type")
+        weight_type = w.dtype
+    n = y.numel() // H
+    at = rows if mode == GATE_ELEMENT else gate
+    spec = _NormT(kind, 0 if weight_type is None else _KINDS[weight_type], n, H, post, pre,
+                  None if post_weight is None else post_weight.data_ptr(),
+                  None if pre_weight is None else pre_weight.data_ptr(), mode, None if at is None else at.data_ptr(),
+                  0 if rows is None else rows.stride(0), scale, residual_scale, eps)
+    return spec, (post_weight, pre_weight, at)
+
+
+def _at(t):
+    return (None, 0) if t is None else (t.data_ptr(), t.stride(0))
+
+
+def _given(name: str, out, like):
+    """`out`, made like `like` if it is None, checked otherwise."""
+    if out is None:
+        return like.new_empty(like.shape)
+    if out.shape != like.shape or out.dtype != like.dtype or not out.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {like.dtype} tensor of shape {tuple(like.shape)}")
+    return out
+
+
+def _norm_args(y, residual, post_weight, gate, pre_weight, scale, residual_scale, eps, post, pre, quantize, h, n, keep):
+    post = post_weight is not None if post is None else bool(post)
+    spec, named = _spec(y, post_weight, gate, pre_weight, scale, residual_scale, eps, post, bool(pre))
+    rows = _rows_of("y", y, y.shape, y.dtype)
+    res = _rows_of("residual", residual, y.shape, y.dtype)
+    h = _given("h", h, y) if keep else None
+    codes = scales = None
+    if not pre:
+        if quantize or n is not None:
+            raise ValueError("without the norm before the next block there is no n")
+    elif quantize:
+        H = y.shape[-1]
+        if H % MX_BLOCK:
+            raise ValueError(f"packed rows must be a multiple of {MX_BLOCK} long, not {H}")
+        if n is None:
+            cb, sb = _packed(spec.rows, H)
+            n = MxOperand(y.new_empty(cb, dtype=torch.uint8), y.new_empty(sb, dtype=torch.uint8), spec.rows, H)
+        else:
+            _kind(n, "n", MxOperand)
+            if (n.rows, n.K) != (spec.rows, H):
+                raise ValueError("n has the wrong shape")
+            n.check("n")
+        codes, scales = n.codes, n.scales
+    else:
+        n = _given("n", n, y)
+    args = (spec, *_at(rows), *_at(res), None if h is None else h.data_ptr(),
+            None if n is None or quantize else n.data_ptr(), None if codes is None else codes.data_ptr(),
+            None if scales is None else scales.data_ptr())
+    return h, n, args, (rows, res, h, codes if quantize else n, scales, *named)
+
+
+def add_norm(y, residual=None, post_weight=None, gate=None, pre_weight=None, scale: float = 1.0,
+             residual_scale: float = 1.0, eps: float = 1e-6, post=None, pre: bool = True, quantize: bool = False,
+             h=None, n=None, stream=None):
+    """What stands between two blocks of a layer (nvfp4_add_norm), by rows
+    [..., hidden] of float32 or bfloat16, hidden at most NORM_MAX_HIDDEN:
+
+        u = y / rms(y) * post_weight            (``post``; by default if a weight is given; else u = y)
+        h = residual_scale * residual + scale * gate * u
+        n = h / rms(h) * pre_weight             (``pre``; else n is None)
+
+    Returns (h, n).  Weights are [hidden] or None for ones; the gate is [hidden]
+    or has y's shape.  ``quantize``: n as a packed MxOperand of all rows, the bits
+    of mx_quantize(n).  ``h`` and ``n`` take given results; h may be the residual
+    or y itself."""
+    if stream is not None:
+        with _on(stream, y):
+            return add_norm(y, residual, post_weight, gate, pre_weight, scale, residual_scale, eps, post, pre, quantize, h, n)
+    h, n, args, tensors = _norm_args(y, residual, post_weight, gate, pre_weight, scale, residual_scale, eps, post, pre,
+                                     quantize, h, n, True)
+    _run(layer_lib().nvfp4_add_norm, args, tensors)
+    return h, n
+
+
+def rms_norm(x, weight=None, eps: float = 1e-6, quantize: bool = False, out=None, stream=None):
+    """x / rms(x) * weight by rows (nvfp4_add_norm with nothing else), as rows or
+    as a packed MxOperand."""
+    if stream is not None:
+        with _on(stream, x):
+            return rms_norm(x, weight, eps, quantize, out)
+    _, n, args, tensors = _norm_args(x, None, None, None, weight, 1.0, 1.0, eps, False, True, quantize, None, out, False)
+    _run(layer_lib().nvfp4_add_norm, args, tensors)
+    return n
+
+
+@dataclass
+class NormGrads:
+    """Gradients of add_norm by its inputs (None where there is none): rows
+    in the rows' type, those of weights and of a gate for each channel float32."""
+    y: "object"
+    residual: "object"
+    gate: "object"
+    post_weight: "object"
+    pre_weight: "object"
+
+
+def add_norm_grad(dh, dn, y, h, post_weight=None, gate=None, pre_weight=None, scale: float = 1.0,
+                  residual_scale: float = 1.0, eps: float = 1e-6, post=None, pre=None, residual: bool = True, stream=None):
+    """The gradients (NormGrads) of add_norm for those of its results, dh and dn
+    (None: zeros), given y and the h that came out (read only with ``pre``, which
+    is so by default if dn is given).  ``residual``: whether its gradient is
+    wanted.  Weights that are None have no gradient."""
+    like = dh if dh is not None else dn
+    if like is None:
+        raise ValueError("dh or dn must be given")
+    if stream is not None:
+        with _on(stream, like):
+            return add_norm_grad(dh, dn, y, h, post_weight, gate, pre_weight, scale, residual_scale, eps, post, pre, residual)
+    pre = dn is not None if pre is None else bool(pre)
+    post = post_weight is not None if post is None else bool(post)
+    if pre != (dn is not None):
+        raise ValueError("dn must be given with the norm before the next block, and only then")
+    spec, named = _spec(like, post_weight, gate, pre_weight, scale, residual_scale, eps, post, pre)
+    shape, dtype = like.shape, like.dtype
+    rows = {name: _rows_of(name, t, shape, dtype) for name, t in
+            (("dh", dh), ("dn", dn), ("y", y if post or gate is not None else None), ("h", h if pre else None))}
+    for name, used in (("y", post or gate is not None), ("h", pre)):
+        if used and rows[name] is None:
+            raise ValueError(f"{name} must be given")
+    H = shape[-1]
+    out = NormGrads(like.new_empty(shape), like.new_empty(shape) if residual else None, None, None, None)
+    sums = [like.new_empty(H, dtype=torch.float32) if on else None
+            for on in (spec.gate_mode == GATE_CHANNEL, post_weight is not None, pre_weight is not None)]
+    out.gate, out.post_weight, out.pre_weight = sums
+    if spec.gate_mode == GATE_ELEMENT:
+        out.gate = like.new_empty(shape)
+    work, size = None, _size()
+    L = layer_lib()
+    if any(s is not None for s in sums):
+        st = L.nvfp4_add_norm_grad_workspace(ctypes.byref(spec), ctypes.byref(size))
+        if st:
+            raise Nvfp4Error(st, "nvfp4_add_norm_grad_workspace")
+        work = like.new_empty(size.value, dtype=torch.uint8)
+    outs = (out.y, out.residual, out.gate, out.post_weight, out.pre_weight, work)
+    args = (spec, *_at(rows["dh"]), *_at(rows["dn"]), *_at(rows["y"]), *_at(rows["h"]),
+            *(None if t is None else t.data_ptr() for t in outs), size.value)
+    _run(L.nvfp4_add_norm_grad, args, (*(t for t in rows.values()), *outs, *named)[0 if dh is not None else 1:])
+    return out

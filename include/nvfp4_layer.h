@@ -1,6 +1,7 @@
 /*
  * nvfp4_layer.h -- C ABI of the operators that stand around the MXFP4
- * products (nvfp4_mx.h) in a transformer layer: products with an epilogue.
+ * products (nvfp4_mx.h) in a transformer layer: products with an epilogue, and
+ * the norms behind one block and before the next with their gradients.
  *
  * Status codes, pointers, streams, errors, types and sizes as in nvfp4_mx.h.
  * In the library from nvfp4_version() 10700 on.
@@ -80,6 +81,71 @@ int nvfp4_sequence_add_mx_grouped_gemm_fused(nvfp4_sequence_t seq, const void* a
                                              int64_t groups, float alpha,
                                              const nvfp4_mx_epilogue* epilogue, void* out,
                                              int out_type, int64_t M, int64_t N, int64_t K);
+
+/* ---- norms around a block's residual ---------------------------------------
+ *
+ * Behind a block with the result y, and before the next one:
+ *   u = post ? y / rms(y) * post_weight : y        rms(x) = sqrt(mean(x^2) + eps)
+ *   h = residual_scale * residual + scale * gate * u
+ *   n = h / rms(h) * pre_weight                     (pre)
+ * by rows, in fp32; h is rounded to its type once, and n is the norm of the
+ * rounded h, rounded once: the same as that norm of the stored h in a call of
+ * its own.  A mean of squares past fp32's range is an infinity (values of 2^64
+ * and more; such a row's norm is zeros, NaN where an infinity stood). */
+enum { NVFP4_GATE_NONE = 0, NVFP4_GATE_CHANNEL = 1, NVFP4_GATE_ELEMENT = 2 };
+#define NVFP4_NORM_MAX_HIDDEN 16384
+
+typedef struct nvfp4_norm {
+    int type;                /* NVFP4_TYPE_* of all rows */
+    int weight_type;         /* NVFP4_TYPE_* of the weights and of a CHANNEL gate */
+    int64_t rows, hidden;    /* 0 <= rows < 2^31, 1 <= hidden <= NVFP4_NORM_MAX_HIDDEN */
+    int post, pre;           /* whether there is a norm behind the block, before the next */
+    const void* post_weight; /* DEVICE [hidden], or NULL: ones */
+    const void* pre_weight;
+    int gate_mode;           /* NVFP4_GATE_* */
+    const void* gate;        /* DEVICE; CHANNEL: [hidden], the same for every row; ELEMENT: rows x hidden
+                                of `type`, row stride ld_gate */
+    int64_t ld_gate;
+    float scale, residual_scale, eps;   /* eps >= 0 */
+} nvfp4_norm;
+
+/*   y, residual : DEVICE rows x hidden, row strides of at least hidden elements (a single row's
+ *                 is not looked at); residual NULL: zeros
+ *   h           : DEVICE rows x hidden (stride hidden), or NULL if it is not wanted; may be
+ *                 residual or y itself (of stride hidden)
+ *   n           : DEVICE rows x hidden (stride hidden), or NULL
+ *   n_codes, n_scales : n as a packed MXFP4 operand of rows x hidden instead, the bits of
+ *                 nvfp4_mx_quantize(n) (nvfp4_mx_packed_size bytes, 16-byte aligned; hidden a
+ *                 multiple of 32), or both NULL
+ * With `pre` n or the packed operand is wanted, without it neither, and then h is.
+ * Buffers need the alignment of their elements only, but run fastest when rows start on
+ * 16-byte boundaries.  Outputs must not overlap inputs otherwise. */
+int nvfp4_add_norm(const nvfp4_norm* norm, const void* y, int64_t ld_y, const void* residual,
+                   int64_t ld_residual, void* h, void* n, void* n_codes, void* n_scales,
+                   void* stream);
+int nvfp4_sequence_add_norm(nvfp4_sequence_t seq, const nvfp4_norm* norm, const void* y,
+                            int64_t ld_y, const void* residual, int64_t ld_residual, void* h,
+                            void* n, void* n_codes, void* n_scales);
+
+/* Gradients of nvfp4_add_norm, for those of h (dh) and n (dn):
+ *   dh, dn : DEVICE rows x hidden, row strides ld_dh, ld_dn; dh NULL: zeros; dn given exactly if
+ *            `pre`
+ *   y      : as given (read with `post` or a gate); h: as it came out (read with `pre`)
+ * Outputs, each NULL if it is not wanted, none overlapping anything:
+ *   dy, dresidual : DEVICE rows x hidden
+ *   dgate         : DEVICE, CHANNEL: fp32 [hidden]; ELEMENT: rows x hidden of `type`
+ *   dpost_weight, dpre_weight : DEVICE fp32 [hidden] (with `post`, `pre`)
+ *   workspace     : DEVICE, 16-byte aligned, as many bytes as nvfp4_add_norm_grad_workspace
+ *            says (the fp32 sums of groups of rows, which a second launch adds in order);
+ *            may be NULL if that is 0 or none of dgate (CHANNEL), dpost_weight and
+ *            dpre_weight is wanted.  Free again when the call's work is done; calls that may
+ *            run at the same time need one each.
+ * Sums over rows are fp32, in an order that depends on the sizes only. */
+int nvfp4_add_norm_grad_workspace(const nvfp4_norm* norm, size_t* bytes);
+int nvfp4_add_norm_grad(const nvfp4_norm* norm, const void* dh, int64_t ld_dh, const void* dn,
+                        int64_t ld_dn, const void* y, int64_t ld_y, const void* h, int64_t ld_h,
+                        void* dy, void* dresidual, void* dgate, float* dpost_weight,
+                        float* dpre_weight, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -75,3 +75,70 @@ def check(got, want, bound, what=""):
     assert torch.equal(g[~fine & ~w.isnan()], w[~fine & ~w.isnan()]), f"{what}: infinities"
     off = ((g - w).abs() - (bound + eps / 2 * (w.abs() + bound) + 1e-37))[fine]
     assert not off.numel() or off.max() <= 0, f"{what}: {int((off > 0).sum())} elements off, by up to {off.max():.3g} over the bound"
+
+
+# ---- norms: everything in float64, (value, bound before rounding) ---------------
+# A mean of squares adds at most 60 times on its way (pieces of a lane, lanes,
+# waves): off by 62 u with the mean and eps, its root's inverse by half of that
+# and the instruction's error, 40 u in all.
+
+def inverse_rms(x, eps):
+    return (x.square().mean(-1, keepdim=True) + eps).rsqrt()
+
+
+def norm_h(y, residual=None, post=False, post_weight=None, gate=None, scale=1.0, residual_scale=1.0, eps=1e-6):
+    u = y * inverse_rms(y, eps) if post else y
+    if post_weight is not None:
+        u = u * post_weight
+    b = scale * u if gate is None else scale * gate * u
+    r = 0.0 if residual is None else residual_scale * residual
+    return b + r, 48 * U * b.abs() + 4 * U * (b.abs() + abs(r))
+
+
+def norm_n(h, pre_weight=None, eps=1e-6):
+    n = h * inverse_rms(h, eps) * (1.0 if pre_weight is None else pre_weight)
+    return n, 48 * U * n.abs()
+
+
+def _norm_back(d, dd, x, w, eps):
+    """Gradients of x / rms(x) * w for d, which is off by dd: ((dx, bound), (dw, bound) by rows)."""
+    r = inverse_rms(x, eps)
+    v, dv = d * w, dd * abs(w) + 2 * U * (d * w).abs()
+    mean = lambda t: t.mean(-1, keepdim=True)  # noqa: E731
+    along = mean(v * x)
+    dx = r * v - x * r ** 3 * along
+    bound = r * (dv + 50 * U * v.abs()) + x.abs() * r ** 3 * (mean(dv * x.abs()) + 70 * U * mean((v * x).abs())
+                                                              + 130 * U * along.abs()) + 4 * U * dx.abs()
+    dw = d * x * r
+    return (dx, bound), (dw, (dd + 46 * U * d.abs()) * (x * r).abs())
+
+
+def norm_grads(dh, dn, y, h, post=False, post_weight=None, gate=None, pre_weight=None, scale=1.0, residual_scale=1.0,
+               eps=1e-6, channel=False):
+    """{name: (value, bound)}; sums over rows add at most as often as there are rows, plus 40."""
+    rows = (dh if dh is not None else dn).shape[0]
+    total = lambda t, b: (t.sum(0), b.sum(0) + (rows + 40) * U * t.abs().sum(0))  # noqa: E731
+    out = {}
+    d = torch.zeros_like(dn) if dh is None else dh
+    b = torch.zeros_like(d)
+    if dn is not None:
+        w = torch.ones_like(dn[0]) if pre_weight is None else pre_weight
+        (dx, bx), dw = _norm_back(dn, torch.zeros_like(dn), h, w, eps)
+        b = bx + 2 * U * (d.abs() + dx.abs())
+        d = d + dx
+        out["pre_weight"] = total(*dw)
+    out["residual"] = residual_scale * d, abs(residual_scale) * b + 2 * U * (residual_scale * d).abs()
+    d, b = scale * d, abs(scale) * b + U * (scale * d).abs()
+    if gate is not None:
+        u = y
+        if post:
+            u = y * inverse_rms(y, eps) * (1.0 if post_weight is None else post_weight)
+        g, bg = d * u, b * u.abs() + 46 * U * (d * u).abs()
+        out["gate"] = total(g, bg) if channel else (g, bg)
+        d, b = d * gate, b * abs(gate) + U * (d * gate).abs()
+    if post:
+        w = torch.ones_like(y[0]) if post_weight is None else post_weight
+        (d, b), dw = _norm_back(d, b, y, w, eps)
+        out["post_weight"] = total(*dw)
+    out["y"] = d, b
+    return out

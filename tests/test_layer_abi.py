@@ -136,3 +136,109 @@ def test_epilogue_arguments(monkeypatch):
     nv.mx_gemm(operand(4), b, epilogue=nv.MxEpilogue(gate=g, gate_bias=torch.zeros(7, dtype=torch.bfloat16)))
     s = calls[-1][1][5]
     assert (s.bias, s.bias_type) == (None, 1)
+
+
+def norm(**kw):
+    f = dict(type=1, weight_type=0, rows=4, hidden=64, post=1, pre=1, post_weight=P, pre_weight=P, gate_mode=0, gate=None,
+             ld_gate=64, scale=1.0, residual_scale=1.0, eps=1e-6)
+    return nv.layer._NormT(**{**f, **kw})
+
+
+BAD_NORMS = [dict(type=2), dict(weight_type=3), dict(rows=-1), dict(rows=2 ** 31), dict(hidden=0), dict(hidden=16385),
+             dict(gate_mode=3), dict(gate_mode=-1), dict(gate_mode=1), dict(gate_mode=2, gate=P, ld_gate=63),
+             dict(gate_mode=2, gate=P, ld_gate=2 ** 31), dict(eps=-1.0), dict(eps=float("nan")),
+             dict(gate_mode=1, gate=P, post_weight=None, pre_weight=None, weight_type=7)]
+MISALIGNED_NORMS = [dict(post_weight=P + 2), dict(pre_weight=P + 1), dict(weight_type=1, pre_weight=P + 1),
+                    dict(gate_mode=1, gate=P + 2), dict(gate_mode=2, gate=P + 1)]
+
+
+@pytest.mark.parametrize("record", [False, True])
+def test_norm_refusals(record):
+    L = nv.layer.layer_lib()
+    seq = ctypes.c_void_p()
+    assert L.nvfp4_sequence_create(ctypes.byref(seq)) == nv.OK
+
+    def call(f, y=P, ld=64, res=P, ldr=64, h=P, n=P, c=None, s=None):
+        args = (f, y, ld, res, ldr, h, n, c, s)
+        return L.nvfp4_sequence_add_norm(seq, *args) if record else L.nvfp4_add_norm(*args, None)
+
+    assert call(None) == INV
+    for bad in BAD_NORMS:
+        assert call(norm(**bad)) == INV, bad
+    for bad in MISALIGNED_NORMS:
+        assert call(norm(**bad)) == MIS, bad
+    for bad in (dict(y=None), dict(ld=63), dict(ld=-64), dict(ld=2 ** 31), dict(ldr=3), dict(n=None), dict(c=P, s=P),
+                dict(n=None, c=P), dict(n=None, s=P), dict(h=None, n=None)):
+        assert call(norm(), **bad) == INV, bad
+    assert call(norm(pre=0)) == INV and call(norm(pre=0), n=None, c=P, s=P) == INV      # an n without its norm
+    assert call(norm(pre=0), n=None, h=None) == INV
+    assert call(norm(hidden=72), ld=72, ldr=72, n=None, c=P, s=P) == INV                # not whole blocks
+    for bad in (dict(y=P + 1), dict(res=P + 1), dict(h=P + 1), dict(n=P + 1), dict(n=None, c=P + 8, s=P), dict(n=None, c=P, s=P + 4)):
+        assert call(norm(), **bad) == MIS, bad
+    assert call(norm(type=0), y=P + 2) == MIS
+    if record:
+        assert call(norm(rows=1), ld=0, ldr=0) == nv.OK
+        assert call(norm(gate_mode=2, gate=P), h=None, n=None, c=P, s=P) == nv.OK
+        assert call(norm(rows=0), y=None, res=None, h=None, n=None) == nv.OK
+        assert L.nvfp4_sequence_add_norm(None, norm(), P, 64, P, 64, P, P, None, None) == INV
+    L.nvfp4_sequence_destroy(seq)
+
+
+def test_norm_grad_refusals():
+    L = nv.layer.layer_lib()
+    size = ctypes.c_size_t()
+
+    def call(f, dh=P, ldh=64, dn=P, ldn=64, y=P, ldy=64, h=P, ldhh=64, dy=P, dr=P, dg=None, dp=P, dq=P, w=P, n=1 << 30):
+        return L.nvfp4_add_norm_grad(f, dh, ldh, dn, ldn, y, ldy, h, ldhh, dy, dr, dg, dp, dq, w, n, None)
+
+    assert call(None) == INV and L.nvfp4_add_norm_grad_workspace(None, ctypes.byref(size)) == INV
+    assert L.nvfp4_add_norm_grad_workspace(norm(), None) == INV
+    for bad in BAD_NORMS:
+        assert call(norm(**bad)) == INV, bad
+        assert L.nvfp4_add_norm_grad_workspace(norm(**bad), ctypes.byref(size)) == INV, bad
+    for bad in (dict(dn=None), dict(y=None), dict(h=None), dict(ldh=8), dict(ldn=8), dict(ldy=8), dict(ldhh=8), dict(dg=P),
+                dict(w=None), dict(n=16)):
+        assert call(norm(), **bad) == INV, bad
+    assert call(norm(pre=0), dn=None) == INV                                 # a gradient of pre_weight without its norm
+    assert call(norm(pre=0), dq=None) == INV                                 # dn without its norm
+    assert call(norm(post=0)) == INV                                         # a gradient of post_weight without its norm
+    for bad in (dict(dh=P + 1), dict(dn=P + 1), dict(y=P + 1), dict(h=P + 1), dict(dy=P + 1), dict(dr=P + 1), dict(dp=P + 2),
+                dict(dq=P + 2), dict(w=P + 8)):
+        assert call(norm(), **bad) == MIS, bad
+    assert call(norm(gate_mode=1, gate=P), dg=P + 2) == MIS and call(norm(gate_mode=2, gate=P), dg=P + 1) == MIS
+    for f, zero in ((norm(), False), (norm(rows=0), True), (norm(post=0, pre=0), True),
+                    (norm(post=0, pre=0, gate_mode=1, gate=P), False), (norm(post=0, pre=0, gate_mode=2, gate=P), True)):
+        assert L.nvfp4_add_norm_grad_workspace(f, ctypes.byref(size)) == nv.OK and (size.value == 0) == zero
+
+
+def test_norm_binding_refuses():
+    y, w = torch.zeros(4, 64), torch.zeros(64)
+    bf = dict(dtype=torch.bfloat16)
+    for args, kw, match in [((torch.zeros(64),), {}, "two dimensions"), ((y.half(),), {}, "float32 or bfloat16"),
+                            ((torch.zeros(2, 0),), {}, "elements"), ((torch.zeros(2, 16385),), {}, "elements"),
+                            ((y, torch.zeros(4, 65)), {}, "residual"), ((y, torch.zeros(4, 64, **bf)), {}, "residual"),
+                            ((y,), dict(post_weight=torch.zeros(63)), "post_weight"),
+                            ((y,), dict(pre_weight=torch.zeros(64).half()), "pre_weight"),
+                            ((y,), dict(post_weight=w, pre_weight=w.to(torch.bfloat16)), "one type"),
+                            ((y,), dict(post_weight=w, post=False), "without its norm"),
+                            ((y,), dict(pre_weight=w, pre=False), "without its norm"),
+                            ((y,), dict(gate=torch.zeros(4, 1)), "gate"), ((y,), dict(gate=torch.zeros(4, 64, **bf)), "gate"),
+                            ((y,), dict(pre=False, quantize=True), "no n"), ((y,), dict(pre=False, n=y), "no n"),
+                            ((torch.zeros(4, 40),), dict(quantize=True), "multiple"),
+                            ((y,), dict(quantize=True, n=y), "n must be"), ((y,), dict(quantize=True, n=operand(5)), "wrong shape"),
+                            ((y,), dict(h=torch.zeros(4, 63)), "h must be"), ((y,), dict(n=torch.zeros(64, 4).t()), "n must be")]:
+        with pytest.raises(ValueError, match=match):
+            nv.add_norm(*args, **kw)
+    with pytest.raises(ValueError, match="GPU"):
+        nv.rms_norm(y, w)
+    for args, kw, match in [((None, None, y, y), {}, "dh or dn"), ((y, y, y, None), {}, "h must be given"),
+                            ((y, None, None, None), dict(post=True), "y must be given"), ((y, None, y, y), dict(pre=True), "dn must"),
+                            ((y, y, y, y), dict(pre=False), "dn must"), ((y, torch.zeros(4, 65), y, y), {}, "dn"),
+                            ((y, y, torch.zeros(3, 64), y), dict(post=True), "y must be"), ((y, None, y, y), dict(pre_weight=w), "without its norm")]:
+        with pytest.raises(ValueError, match=match):
+            nv.add_norm_grad(*args, **kw)
+    seq = nv.Sequence()
+    for kw in (dict(h=None), dict(h=None, n=None, pre=False), dict(h=y)):
+        with pytest.raises(ValueError, match="out"):
+            seq.add_norm(y, None, **kw)
+    assert seq.calls == 0
