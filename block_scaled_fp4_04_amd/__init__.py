@@ -766,6 +766,16 @@ class Sequence:
         self._record(moe.moe_lib().nvfp4_sequence_add_moe_combine, args,
                      (y, route.slots, weights, out), [y, route, weights, out])
 
+    def add_mx_moe(self, x, expert_ids, weights, up: "MxGroups", down: "MxGroups", out, gate=None, activation="silu",
+                   up_bias=None, gate_bias=None, down_bias=None) -> None:
+        """Records mx_moe(x, expert_ids, weights, up, down, gate, activation, up_bias, gate_bias, down_bias, out).  The
+        sequence keeps the call's workspace: two launches of one sequence must not run at the same time."""
+        from . import layer
+        self._given(out)
+        _, args, tensors = layer._moe_args(x, expert_ids, weights, up, down, gate, activation, up_bias, gate_bias,
+                                           down_bias, out, None)
+        self._record(layer.layer_lib().nvfp4_sequence_add_mx_moe, args, tensors, list(tensors))
+
     def add_norm(self, y, residual, h, n=None, **how) -> None:
         """Records add_norm(y, residual, h=h, n=n, **how); h None: not kept (as rms_norm).  n is an MxOperand with
         quantize=True."""
@@ -813,7 +823,7 @@ _LATER = {"mx": ("mx", "MX_BLOCK", "MX_EXPORTS", "MX_QUANT_ROWS", "TYPE_BF16", "
           "moe": ("moe", "INDEX_I32", "INDEX_I64", "MOE_EXPORTS", "MOE_MAX_EXPERTS", "MoeRoute",
                   "moe_combine", "moe_combine_grad", "moe_gather", "moe_gather_grad", "moe_sort"),
           "layer": ("layer", "ACTIVATIONS", "LAYER_EXPORTS", "MxEpilogue", "NORM_MAX_HIDDEN", "NormGrads", "add_norm",
-                    "add_norm_grad", "rms_norm")}
+                    "add_norm_grad", "mx_moe", "rms_norm")}
 
 
 def __getattr__(name: str):

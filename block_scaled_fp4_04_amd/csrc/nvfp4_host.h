@@ -42,6 +42,7 @@ struct Job {
     MoeArgs moe{};
     MxEpilogueArgs epilogue{};   // with mx_gemm
     NormArgs norm{};
+    MxMoeArgs mx_moe{};
     bool empty = false;          // nothing to launch (a grouped GEMM with no rows)
 };
 

@@ -89,6 +89,140 @@ int prepare_grouped_fused(const void* a_packed, const void* a_scales, int64_t a_
     return add_epilogue(st, e, out_type, job);
 }
 
+// ---- a whole layer of experts -------------------------------------------------
+
+bool few(int64_t tokens, int64_t topk) { return tokens <= kMoeFewTokens && tokens * topk <= kMoeFewChoices; }
+
+int check_experts(const nvfp4_mx_experts* l, int64_t tokens, int64_t topk, int out_type) {
+    auto valid_depth = [](int64_t K) { return K >= kMxBlock && K <= kMaxDim && K % kMxBlock == 0; };
+    if (!l || l->experts < 1 || l->experts > kMoeMaxExperts || !valid_depth(l->hidden) || !valid_depth(l->inner) ||
+        l->hidden > ((int64_t)1 << 22) || !valid_act(l->activation) || !valid_type(out_type) || tokens < 0 ||
+        tokens >= ((int64_t)1 << 24) || topk < 1 || topk >= ((int64_t)1 << 24) || tokens * topk > kMaxDim)
+        return NVFP4_ERR_INVALID_VALUE;
+    return NVFP4_OK;
+}
+
+// The workspace, part by part.
+struct MoeSpace {
+    size_t bytes = 0;
+    size_t take(int64_t n, size_t size) {
+        const size_t at = bytes;
+        bytes += ((size_t)n * size + 255) / 256 * 256;
+        return at;
+    }
+    size_t h = 0, offsets = 0, slots = 0, row_tokens = 0, x_codes = 0, x_scales = 0, h_codes = 0, h_scales = 0, y = 0;
+    MoeSpace(const nvfp4_mx_experts& l, int64_t tokens, int64_t topk, int out_type) {
+        const int64_t pairs = tokens * topk;
+        if (pairs == 0) return;
+        h = take(pairs * l.inner, 2);
+        if (few(tokens, topk)) return;
+        auto packed = [&](int64_t rows, int64_t K, size_t* codes, size_t* scales) {
+            const int64_t rb = mx_row_blocks(rows), c = mx_steps(K);
+            *codes = take(rb * c, kMxFrag);
+            *scales = take(rb * ((c + 3) / 4), kMxScaleFrag);
+        };
+        offsets = take(l.experts + 1, 4);
+        slots = take(pairs, 4);
+        row_tokens = take(pairs, 4);
+        packed(tokens, l.hidden, &x_codes, &x_scales);
+        packed(pairs, l.inner, &h_codes, &h_scales);
+        y = take(pairs * l.hidden, size_of(out_type));
+    }
+};
+
+constexpr int kMoeJobs = 6;
+
+int prepare_mx_moe(const nvfp4_mx_experts* l, const void* x, int x_type, int64_t ldx, const void* ids,
+                   int id_type, const float* weights, int64_t tokens, int64_t topk, void* out, int out_type,
+                   void* workspace, size_t workspace_bytes, Job* jobs, int* count) {
+    *count = 0;
+    int st = check_experts(l, tokens, topk, out_type);
+    if (st != NVFP4_OK) return st;
+    if (!valid_type(x_type) || (id_type != NVFP4_INDEX_I32 && id_type != NVFP4_INDEX_I64) ||
+        !l->gate_packed != !l->gate_scales || !l->up_packed || !l->up_scales || !l->down_packed || !l->down_scales ||
+        (l->gate_bias && !l->gate_packed) ||
+        ((l->gate_bias || l->up_bias || l->down_bias) && !valid_type(l->bias_type)))
+        return NVFP4_ERR_INVALID_VALUE;
+    const int64_t per16 = x_type == NVFP4_TYPE_BF16 ? 8 : 4;
+    if (tokens <= 1) ldx = l->hidden;
+    if (ldx < l->hidden || ldx > kMaxDim || ldx % per16) return NVFP4_ERR_INVALID_VALUE;
+    const MoeSpace at(*l, tokens, topk, out_type);
+    if (tokens > 0 && (!x || !ids || !out || !workspace || workspace_bytes < at.bytes)) return NVFP4_ERR_INVALID_VALUE;
+    const uintptr_t bias_size = size_of(l->bias_type);
+    const void* const whole[] = {x, out, workspace, l->gate_packed, l->gate_scales, l->up_packed,
+                                 l->up_scales, l->down_packed, l->down_scales};
+    for (const void* p : whole)
+        if (!aligned(p, 16)) return NVFP4_ERR_MISALIGNED;
+    if (!aligned(ids, id_type == NVFP4_INDEX_I64 ? 8 : 4) || !aligned(weights, 4) || !aligned(l->gate_bias, bias_size) ||
+        !aligned(l->up_bias, bias_size) || !aligned(l->down_bias, bias_size))
+        return NVFP4_ERR_MISALIGNED;
+    if (tokens == 0) return NVFP4_OK;
+    uint8_t* const w = static_cast<uint8_t*>(workspace);
+    if (few(tokens, topk)) {
+        Job& job = jobs[0];
+        job = Job{};
+        job.kind = JOB_LAUNCH;
+        job.launch = +[](const Job& j, hipStream_t s) { return launch_mx_moe_few(j.mx_moe, s); };
+        MxMoeArgs& a = job.mx_moe;
+        a.x = x;
+        a.x_bf16 = x_type == NVFP4_TYPE_BF16;
+        a.wide = id_type == NVFP4_INDEX_I64;
+        a.bias_bf16 = l->bias_type == NVFP4_TYPE_BF16;
+        a.out_bf16 = out_type == NVFP4_TYPE_BF16;
+        a.ldx = ldx;
+        a.ids = ids;
+        a.weights = weights;
+        a.tokens = (int)tokens;
+        a.topk = (int)topk;
+        a.experts = (int)l->experts;
+        a.hidden = (int)l->hidden;
+        a.inner = (int)l->inner;
+        a.gate_codes = static_cast<const uint8_t*>(l->gate_packed);
+        a.gate_scales = static_cast<const uint8_t*>(l->gate_scales);
+        a.up_codes = static_cast<const uint8_t*>(l->up_packed);
+        a.up_scales = static_cast<const uint8_t*>(l->up_scales);
+        a.down_codes = static_cast<const uint8_t*>(l->down_packed);
+        a.down_scales = static_cast<const uint8_t*>(l->down_scales);
+        a.gate_bias = l->gate_bias;
+        a.up_bias = l->up_bias;
+        a.down_bias = l->down_bias;
+        a.act = l->activation;
+        a.h = reinterpret_cast<uint16_t*>(w + at.h);
+        a.out = out;
+        *count = 1;
+        return NVFP4_OK;
+    }
+    const int64_t pairs = tokens * topk;
+    int32_t* const offsets = reinterpret_cast<int32_t*>(w + at.offsets);
+    int32_t* const slots = reinterpret_cast<int32_t*>(w + at.slots);
+    int32_t* const row_tokens = reinterpret_cast<int32_t*>(w + at.row_tokens);
+    const nvfp4_mx_epilogue up = {l->activation, l->gate_packed, l->gate_scales, l->up_bias,
+                                  l->gate_bias, l->bias_type, nullptr, 0};
+    const nvfp4_mx_epilogue down = {NVFP4_ACT_NONE, nullptr, nullptr, l->down_bias, nullptr, l->bias_type, nullptr, 0};
+    // (rows of h and y behind the last kept choice hold anything: they are read,
+    // but nothing that is used comes of them)
+    st = prepare_moe_sort(ids, id_type, tokens, topk, l->experts, offsets, slots, row_tokens, &jobs[0]);
+    if (st == NVFP4_OK)
+        st = prepare_mx_quantize(false, x, x_type, 1, 0, tokens, l->hidden, ldx, w + at.x_codes, w + at.x_scales, &jobs[1]);
+    if (st == NVFP4_OK)
+        st = prepare_grouped_fused(w + at.x_codes, w + at.x_scales, tokens, row_tokens, l->up_packed, l->up_scales,
+                                   offsets, l->experts, 1.0f, &up, w + at.h, NVFP4_TYPE_BF16, pairs, l->inner,
+                                   l->hidden, &jobs[2]);
+    if (st == NVFP4_OK)
+        st = prepare_mx_quantize(false, w + at.h, NVFP4_TYPE_BF16, 1, 0, pairs, l->inner, l->inner, w + at.h_codes,
+                                 w + at.h_scales, &jobs[3]);
+    if (st == NVFP4_OK)
+        st = prepare_grouped_fused(w + at.h_codes, w + at.h_scales, pairs, nullptr, l->down_packed, l->down_scales,
+                                   offsets, l->experts, 1.0f, &down, w + at.y, out_type, pairs, l->hidden, l->inner,
+                                   &jobs[4]);
+    if (st == NVFP4_OK)
+        st = prepare_moe_combine(w + at.y, out_type, tokens, topk, l->hidden, slots, weights, out, &jobs[5]);
+    if (st == NVFP4_OK) *count = kMoeJobs;
+    return st;
+}
+
+// ---- norms ----------------------------------------------------------------------
+
 // What forward and gradient share: the operator itself.
 int check_norm(const nvfp4_norm* f, NormArgs* a) {
     if (!f || !valid_type(f->type) || f->rows < 0 || f->rows > INT32_MAX || f->hidden < 1 ||
@@ -163,6 +297,44 @@ size_t grad_workspace(const NormArgs& a) {
 }  // namespace
 
 extern "C" {
+
+int nvfp4_mx_moe_workspace(const nvfp4_mx_experts* layer, int64_t tokens, int64_t topk,
+                           int out_type, size_t* bytes) {
+    const int st = check_experts(layer, tokens, topk, out_type);
+    if (st != NVFP4_OK || !bytes) return st != NVFP4_OK ? st : NVFP4_ERR_INVALID_VALUE;
+    *bytes = MoeSpace(*layer, tokens, topk, out_type).bytes;
+    return NVFP4_OK;
+}
+
+int nvfp4_mx_moe(const nvfp4_mx_experts* layer, const void* x, int x_type, int64_t ldx,
+                 const void* expert_ids, int id_type, const float* weights, int64_t tokens,
+                 int64_t topk, void* out, int out_type, void* workspace, size_t workspace_bytes,
+                 void* stream) {
+    Job jobs[kMoeJobs];
+    int count;
+    int st = prepare_mx_moe(layer, x, x_type, ldx, expert_ids, id_type, weights, tokens, topk, out, out_type,
+                            workspace, workspace_bytes, jobs, &count);
+    for (int i = 0; i < count && st == NVFP4_OK; ++i) st = run_job(jobs[i], stream);
+    return st;
+}
+
+int nvfp4_sequence_add_mx_moe(nvfp4_sequence_t seq, const nvfp4_mx_experts* layer, const void* x,
+                              int x_type, int64_t ldx, const void* expert_ids, int id_type,
+                              const float* weights, int64_t tokens, int64_t topk, void* out,
+                              int out_type, void* workspace, size_t workspace_bytes) {
+    Job jobs[kMoeJobs];
+    int count;
+    int st = prepare_mx_moe(layer, x, x_type, ldx, expert_ids, id_type, weights, tokens, topk, out, out_type,
+                            workspace, workspace_bytes, jobs, &count);
+    if (count == 0) {  // refused, or no tokens: a call that does nothing
+        jobs[0] = Job{};
+        jobs[0].kind = JOB_LAUNCH;
+        jobs[0].empty = true;
+        return sequence_add(seq, st, jobs[0]);
+    }
+    for (int i = 0; i < count && st == NVFP4_OK; ++i) st = sequence_add(seq, st, jobs[i]);
+    return st;
+}
 
 int nvfp4_add_norm(const nvfp4_norm* norm, const void* y, int64_t ld_y, const void* residual,
                    int64_t ld_residual, void* h, void* n, void* n_codes, void* n_scales,

@@ -89,26 +89,39 @@ __device__ __forceinline__ uint32_t mx_codes(uint32_t c, const mx_u4& v, float s
     return c;
 }
 
-// A whole block in one lane: the 32 values at p (16-byte aligned) -> 16 bytes
-// of codes and the scale byte.
+// A whole block in one lane: its 32 values as they lie in memory (16-byte
+// aligned) and, of those, 16 bytes of codes and the scale byte.
 template <typename T>
-__device__ __forceinline__ uint32_t mx_quant_load(const T* p, mx_u4& w) {
-    constexpr int L = kMxBlock * (int)sizeof(T) / 16, PER = L / 4;  // loads; of them, to a word of codes
+struct MxRaw {
+    static constexpr int L = kMxBlock * (int)sizeof(T) / 16;
     mx_u4 v[L];
+};
+template <typename T>
+__device__ __forceinline__ MxRaw<T> mx_raw_load(const T* p) {
+    MxRaw<T> r;
 #pragma unroll
-    for (int i = 0; i < L; ++i) v[i] = reinterpret_cast<const mx_u4*>(p)[i];
+    for (int i = 0; i < r.L; ++i) r.v[i] = reinterpret_cast<const mx_u4*>(p)[i];
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t mx_quant_block(const MxRaw<T>& r, mx_u4& w) {
+    constexpr int PER = MxRaw<T>::L / 4;  // loads to a word of codes
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < L; ++i) top = max(top, mx_top<T>(v[i]));
+    for (int i = 0; i < r.L; ++i) top = max(top, mx_top<T>(r.v[i]));
     const uint32_t byte = mx_scale_byte(top);
     const float s = mx_scale(byte);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        uint32_t c = mx_codes<T, 0>(0, v[PER * j], s);
-        if constexpr (PER == 2) c = mx_codes<T, 1>(c, v[PER * j + 1], s);
+        uint32_t c = mx_codes<T, 0>(0, r.v[PER * j], s);
+        if constexpr (PER == 2) c = mx_codes<T, 1>(c, r.v[PER * j + 1], s);
         w[j] = byte == 255u ? 0u : c;
     }
     return byte;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t mx_quant_load(const T* p, mx_u4& w) {
+    return mx_quant_block(mx_raw_load(p), w);
 }
 
 __device__ __forceinline__ mx_v8i mx_operand(const mx_u4& w) {

@@ -150,4 +150,25 @@ hipError_t launch_norm_grad(const NormArgs& a, hipStream_t stream);
 // Workgroups that launch_norm_grad runs on rows x hidden.
 int norm_grad_parts(bool bf16, int64_t rows, int hidden);
 
+// A whole layer of experts for few tokens (include/nvfp4_layer.h).
+constexpr int kMoeFewTokens = 64;   // a wave's lanes
+constexpr int kMoeFewChoices = 512;
+struct MxMoeArgs {
+    const void* x;               // tokens x hidden (fp32, or bfloat16 if x_bf16), row stride ldx
+    bool x_bf16, wide, bias_bf16, out_bf16;
+    int64_t ldx;
+    const void* ids;             // tokens x topk expert numbers (int32, or int64 if wide)
+    const float* weights;        // [tokens][topk], or null: ones
+    int tokens, topk, experts;
+    int hidden, inner;
+    const uint8_t *gate_codes, *gate_scales;   // [experts] of inner x hidden, or null
+    const uint8_t *up_codes, *up_scales;
+    const uint8_t *down_codes, *down_scales;   // [experts] of hidden x inner
+    const void *gate_bias, *up_bias, *down_bias;
+    int act;                     // kMxAct*
+    uint16_t* h;                 // workspace: [tokens * topk][inner] bfloat16
+    void* out;                   // tokens x hidden
+};
+hipError_t launch_mx_moe_few(const MxMoeArgs& a, hipStream_t stream);
+
 }  // namespace nvfp4

@@ -10,6 +10,9 @@ the package.
     h = mx_linear(x, w_up, epilogue=gated)
     x = mx_linear(h, w_down, epilogue=MxEpilogue(bias=b, residual=x))
 
+``mx_moe`` is a whole layer of experts from a router's choices, in two launches
+for few tokens.
+
 ``add_norm`` is what stands between two blocks: the norm behind one, its gate
 and the residual, and the norm before the next, as rows or as a packed MXFP4
 operand; ``rms_norm`` the norm alone.
@@ -26,14 +29,16 @@ from dataclasses import dataclass
 import torch
 
 from . import Nvfp4Error, _i64, _vp, lib
-from .mx import (MX_BLOCK, _GEMM, _GEMM_Q, _GROUPED, _KINDS, MxOperand, _kind, _on, _packed, _run, _type_of)
+from .mx import (MX_BLOCK, _GEMM, _GEMM_Q, _GROUPED, _KINDS, MxGroups, MxOperand, _kind, _on, _out, _packed, _rows_2d,
+                 _run, _type_of)
 
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}   # NVFP4_ACT_*
 
 LAYER_EXPORTS = ["nvfp4_mx_gemm_fused", "nvfp4_mx_gemm_quantized_fused", "nvfp4_mx_grouped_gemm_fused",
                  "nvfp4_sequence_add_mx_gemm_fused", "nvfp4_sequence_add_mx_gemm_quantized_fused",
                  "nvfp4_sequence_add_mx_grouped_gemm_fused", "nvfp4_add_norm", "nvfp4_sequence_add_norm",
-                 "nvfp4_add_norm_grad", "nvfp4_add_norm_grad_workspace"]
+                 "nvfp4_add_norm_grad", "nvfp4_add_norm_grad_workspace", "nvfp4_mx_moe", "nvfp4_mx_moe_workspace",
+                 "nvfp4_sequence_add_mx_moe"]
 
 GATE_NONE, GATE_CHANNEL, GATE_ELEMENT = 0, 1, 2   # NVFP4_GATE_*
 NORM_MAX_HIDDEN = 16384
@@ -53,7 +58,15 @@ class _NormT(ctypes.Structure):
                 ("scale", _f32), ("residual_scale", _f32), ("eps", _f32)]
 
 
-_epi, _norm_p, _size = ctypes.POINTER(_EpilogueT), ctypes.POINTER(_NormT), ctypes.c_size_t
+class _ExpertsT(ctypes.Structure):
+    _fields_ = [("experts", _i64), ("hidden", _i64), ("inner", _i64), ("activation", _int), ("gate_packed", _vp),
+                ("gate_scales", _vp), ("up_packed", _vp), ("up_scales", _vp), ("down_packed", _vp), ("down_scales", _vp),
+                ("bias_type", _int), ("gate_bias", _vp), ("up_bias", _vp), ("down_bias", _vp)]
+
+
+_epi, _norm_p, _experts_p = (ctypes.POINTER(t) for t in (_EpilogueT, _NormT, _ExpertsT))
+_size = ctypes.c_size_t
+_MOE = [_experts_p, _vp, _int, _i64, _vp, _int, _vp, _i64, _i64, _vp, _int, _vp, _size]
 _NORM = [_norm_p, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp]
 _NORM_GRAD = [_norm_p, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _size]
 
@@ -77,7 +90,9 @@ def layer_lib() -> ctypes.CDLL:
             f.argtypes, g.argtypes = types + [_vp], [_vp] + types
         for name, types in (("nvfp4_add_norm", _NORM + [_vp]), ("nvfp4_sequence_add_norm", [_vp] + _NORM),
                             ("nvfp4_add_norm_grad", _NORM_GRAD + [_vp]),
-                            ("nvfp4_add_norm_grad_workspace", [_norm_p, ctypes.POINTER(_size)])):
+                            ("nvfp4_add_norm_grad_workspace", [_norm_p, ctypes.POINTER(_size)]),
+                            ("nvfp4_mx_moe", _MOE + [_vp]), ("nvfp4_sequence_add_mx_moe", [_vp] + _MOE),
+                            ("nvfp4_mx_moe_workspace", [_experts_p, _i64, _i64, _int, ctypes.POINTER(_size)])):
             f = getattr(L, name)
             f.restype, f.argtypes = _int, types
         _bound = L
@@ -146,6 +161,71 @@ class MxEpilogue:
         # (alpha is the one float among the arguments)
         at = next(i for i, a in enumerate(args) if type(a) is float) + 1
         return args[:at] + (e,) + args[at:], tensors
+
+
+# ---- a whole layer of experts --------------------------------------------------
+
+
+def _moe_args(x, ids, weights, up, down, gate, activation, up_bias, gate_bias, down_bias, out, dtype):
+    for name, w in (("up", up), ("down", down), ("gate", gate)):
+        if w is not None or name != "gate":
+            _kind(w, name, MxGroups)
+            w.check(name)
+    E, F, H = up.groups, up.rows, up.K
+    if (down.groups, down.rows, down.K) != (E, H, F):
+        raise ValueError(f"down must be {E} operands of {H} x {F}, not {down.groups} of {down.rows} x {down.K}")
+    if gate is not None and (gate.groups, gate.rows, gate.K) != (E, F, H):
+        raise ValueError(f"the gate must be {E} operands of {F} x {H}, not {gate.groups} of {gate.rows} x {gate.K}")
+    if gate is None and gate_bias is not None:
+        raise ValueError("gate_bias needs a gate")
+    kind = _rows_2d(x)
+    T = x.shape[0]
+    if x.shape[1] != H:
+        raise ValueError(f"x has rows of {x.shape[1]}, the experts of {H}")
+    if ids.dim() != 2 or ids.shape[0] != T or ids.dtype not in (torch.int32, torch.int64) or not ids.is_contiguous():
+        raise ValueError("expert_ids must be a contiguous [tokens, topk] int32 or int64 tensor")
+    if weights is not None and (weights.dtype != torch.float32 or weights.shape != ids.shape or not weights.is_contiguous()):
+        raise ValueError(f"weights must be a contiguous float32 tensor of shape {tuple(ids.shape)}")
+    biases = [_bias(name, b, shape) for name, b, shape in (("gate_bias", gate_bias, (E, F)), ("up_bias", up_bias, (E, F)),
+                                                           ("down_bias", down_bias, (E, H)))]
+    types = {t for _, t in biases if t is not None}
+    if len(types) > 1:
+        raise ValueError("the biases must be of one type")
+    out, out_kind = _out(out, dtype, T, H, x)
+    spec = _ExpertsT(E, H, F, _activation(activation), None if gate is None else gate.codes.data_ptr(),
+                     None if gate is None else gate.scales.data_ptr(), up.codes.data_ptr(), up.scales.data_ptr(),
+                     down.codes.data_ptr(), down.scales.data_ptr(), max(types, default=0), *(b for b, _ in biases))
+    size, k = _size(), ids.shape[1]
+    st = layer_lib().nvfp4_mx_moe_workspace(ctypes.byref(spec), T, k, out_kind, ctypes.byref(size))
+    if st:
+        raise Nvfp4Error(st, f"nvfp4_mx_moe_workspace({T}, {k})")
+    work = x.new_empty(size.value, dtype=torch.uint8)
+    args = (spec, x.data_ptr(), kind, x.stride(0), ids.data_ptr(), 1 if ids.dtype is torch.int64 else 0,
+            None if weights is None else weights.data_ptr(), T, k, out.data_ptr(), out_kind, work.data_ptr(), size.value)
+    tensors = (x, ids, weights, out, work, up.codes, up.scales, down.codes, down.scales, up_bias, gate_bias, down_bias)
+    return out, args, tensors if gate is None else tensors + (gate.codes, gate.scales)
+
+
+def mx_moe(x, expert_ids, weights, up: MxGroups, down: MxGroups, gate: MxGroups | None = None, activation="silu",
+           up_bias=None, gate_bias=None, down_bias=None, out=None, dtype=None, stream=None):
+    """A whole layer of experts (nvfp4_mx_moe): for each token the sum over its
+    choices ``expert_ids`` [tokens, topk] (int32 or int64; numbers outside [0,
+    experts) are dropped) under ``weights`` (float32, None for ones) of the
+    expert's down-projection of
+
+        act(q(x) up^T + up_bias), or act(q(x) gate^T + gate_bias) * (q(x) up^T + up_bias)
+
+    held in bfloat16 and quantised.  x: [tokens, hidden], rows strided as in
+    mx_quantize; ``up`` and ``gate`` are [experts, inner, hidden], ``down``
+    [experts, hidden, inner]; biases [experts, inner] and [experts, hidden].
+    Two launches up to 64 tokens and 512 choices.  The result is bfloat16 unless
+    ``dtype`` or ``out`` says float32."""
+    if stream is not None:
+        with _on(stream, x):
+            return mx_moe(x, expert_ids, weights, up, down, gate, activation, up_bias, gate_bias, down_bias, out, dtype)
+    out, args, tensors = _moe_args(x, expert_ids, weights, up, down, gate, activation, up_bias, gate_bias, down_bias, out, dtype)
+    _run(layer_lib().nvfp4_mx_moe, args, tensors)
+    return out
 
 
 # ---- norms ------------------------------------------------------------------

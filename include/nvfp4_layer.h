@@ -1,7 +1,8 @@
 /*
  * nvfp4_layer.h -- C ABI of the operators that stand around the MXFP4
- * products (nvfp4_mx.h) in a transformer layer: products with an epilogue, and
- * the norms behind one block and before the next with their gradients.
+ * products (nvfp4_mx.h) in a transformer layer: products with an epilogue, a
+ * whole layer of experts, and the norms behind one block and before the next
+ * with their gradients.
  *
  * Status codes, pointers, streams, errors, types and sizes as in nvfp4_mx.h.
  * In the library from nvfp4_version() 10700 on.
@@ -81,6 +82,57 @@ int nvfp4_sequence_add_mx_grouped_gemm_fused(nvfp4_sequence_t seq, const void* a
                                              int64_t groups, float alpha,
                                              const nvfp4_mx_epilogue* epilogue, void* out,
                                              int out_type, int64_t M, int64_t N, int64_t K);
+
+/* ---- a whole layer of experts ------------------------------------------------
+ *
+ * For each token t and its choices e = expert_ids[t][j] (nvfp4_moe.h: numbers
+ * outside [0, experts) are dropped choices),
+ *   z         = q(x[t]) . U_e^T + up_bias[e]
+ *   h[t][j]   = act(z), or with gate operands act(q(x[t]) . G_e^T + gate_bias[e]) * z,
+ *               rounded to bfloat16
+ *   out[t]    = sum over j of weights[t][j] * (q(h[t][j]) . D_e^T + down_bias[e])
+ * with q() the rounding of nvfp4_mx_quantize; sums in fp32, out rounded once
+ * (zeros for a token without a kept choice).
+ *
+ * Up to 64 tokens and 512 choices the layer runs in two launches, bound by
+ * reading the chosen experts' weights once.  Above that it is nvfp4_moe_sort,
+ * nvfp4_mx_quantize, nvfp4_mx_grouped_gemm_fused, and the same two again with
+ * nvfp4_moe_combine behind them, in one call; each choice's result is then also
+ * rounded to the output's type before the sum.  Deterministic either way. */
+typedef struct nvfp4_mx_experts {
+    int64_t experts;         /* 1 to 2048 */
+    int64_t hidden, inner;   /* row lengths of x and out, and of h: multiples of 32 */
+    int activation;          /* NVFP4_ACT_* */
+    const void* gate_packed; /* DEVICE, `experts` packed operands of inner x hidden, or both NULL */
+    const void* gate_scales;
+    const void* up_packed;   /* DEVICE, `experts` packed operands of inner x hidden */
+    const void* up_scales;
+    const void* down_packed; /* DEVICE, `experts` packed operands of hidden x inner */
+    const void* down_scales;
+    int bias_type;           /* NVFP4_TYPE_* of the biases */
+    const void* gate_bias;   /* DEVICE [experts][inner], or NULL */
+    const void* up_bias;     /* DEVICE [experts][inner], or NULL */
+    const void* down_bias;   /* DEVICE [experts][hidden], or NULL */
+} nvfp4_mx_experts;
+
+/* Bytes of workspace for so many tokens of so many choices (0 for none). */
+int nvfp4_mx_moe_workspace(const nvfp4_mx_experts* layer, int64_t tokens, int64_t topk,
+                           int out_type, size_t* bytes);
+/*   x          : DEVICE tokens x hidden of x_type, row stride ldx (as nvfp4_mx_quantize)
+ *   expert_ids : DEVICE [tokens][topk] of id_type (NVFP4_INDEX_*)
+ *   weights    : DEVICE fp32 [tokens][topk], or NULL: ones; those of dropped choices are ignored
+ *   out        : DEVICE tokens x hidden, overwritten; must not alias the inputs
+ *   workspace  : DEVICE, 16-byte aligned, needs no initial value; free again when the call's
+ *                work is done, so calls that may run at the same time need one each
+ * Sizes as nvfp4_moe_sort and the products. */
+int nvfp4_mx_moe(const nvfp4_mx_experts* layer, const void* x, int x_type, int64_t ldx,
+                 const void* expert_ids, int id_type, const float* weights, int64_t tokens,
+                 int64_t topk, void* out, int out_type, void* workspace, size_t workspace_bytes,
+                 void* stream);
+int nvfp4_sequence_add_mx_moe(nvfp4_sequence_t seq, const nvfp4_mx_experts* layer, const void* x,
+                              int x_type, int64_t ldx, const void* expert_ids, int id_type,
+                              const float* weights, int64_t tokens, int64_t topk, void* out,
+                              int out_type, void* workspace, size_t workspace_bytes);
 
 /* ---- norms around a block's residual ---------------------------------------
  *

@@ -142,3 +142,24 @@ def norm_grads(dh, dn, y, h, post=False, post_weight=None, gate=None, pre_weight
         out["post_weight"] = total(*dw)
     out["y"] = d, b
     return out
+
+
+# ---- a layer of experts ------------------------------------------------------------
+
+def moe_hidden(x, ids, w, act_name, gate=None, bias=None, gate_bias=None):
+    """{(t, e): (h, bound)} before its rounding; x, w, gate: float64 values that MXFP4 holds."""
+    out = {}
+    for e in sorted(set(ids.flatten().tolist())):
+        if 0 <= e < w.shape[0]:
+            t = sorted(set(torch.nonzero(ids == e)[:, 0].tolist()))
+            more = {}
+            if bias is not None:
+                more["bias"] = bias[e]
+            if gate is not None:
+                more["gate"] = product(x[t], gate[e])
+                if gate_bias is not None:
+                    more["gate_bias"] = gate_bias[e]
+            h, d = epilogue(*product(x[t], w[e]), activation=act_name, **more)
+            for i, token in enumerate(t):
+                out[token, e] = h[i], d[i]
+    return out

@@ -242,3 +242,77 @@ def test_norm_binding_refuses():
         with pytest.raises(ValueError, match="out"):
             seq.add_norm(y, None, **kw)
     assert seq.calls == 0
+
+
+def layer(**kw):
+    f = dict(experts=8, hidden=64, inner=96, activation=2, gate_packed=P, gate_scales=P, up_packed=P, up_scales=P,
+             down_packed=P, down_scales=P, bias_type=0, gate_bias=P, up_bias=P, down_bias=P)
+    return nv.layer._ExpertsT(**{**f, **kw})
+
+
+@pytest.mark.parametrize("tokens", [4, 500])
+@pytest.mark.parametrize("record", [False, True])
+def test_moe_refusals(record, tokens):
+    L = nv.layer.layer_lib()
+    seq = ctypes.c_void_p()
+    assert L.nvfp4_sequence_create(ctypes.byref(seq)) == nv.OK
+
+    def call(f, x=P, kind=1, ld=64, ids=P, idt=0, w=P, T=tokens, k=2, out=P, ok=1, ws=P, n=1 << 40):
+        args = (f, x, kind, ld, ids, idt, w, T, k, out, ok, ws, n)
+        return L.nvfp4_sequence_add_mx_moe(seq, *args) if record else L.nvfp4_mx_moe(*args, None)
+
+    assert call(None) == INV
+    for bad in (dict(experts=0), dict(experts=2049), dict(hidden=0), dict(hidden=48), dict(inner=40), dict(inner=-32),
+                dict(hidden=2 ** 23), dict(activation=9), dict(gate_packed=None), dict(gate_scales=None), dict(up_packed=None),
+                dict(up_scales=None), dict(down_packed=None), dict(down_scales=None), dict(bias_type=2),
+                dict(gate_packed=None, gate_scales=None)):                       # (a bias of no gate)
+        assert call(layer(**bad)) == INV, bad
+    for bad in (dict(x=None), dict(kind=2), dict(ld=32), dict(ld=68), dict(ids=None), dict(idt=2), dict(T=-1), dict(T=2 ** 24),
+                dict(k=0), dict(k=2 ** 24), dict(T=2 ** 20, k=2 ** 11), dict(out=None), dict(ok=5), dict(ws=None), dict(n=100)):
+        assert call(layer(), **bad) == INV, bad
+    for bad in (dict(x=P + 8), dict(ids=P + 2), dict(ids=P + 4, idt=1), dict(w=P + 2), dict(out=P + 8), dict(ws=P + 8)):
+        assert call(layer(), **bad) == MIS, bad
+    for bad in (dict(gate_packed=P + 8), dict(up_scales=P + 4), dict(down_packed=P + 1), dict(up_bias=P + 2),
+                dict(bias_type=1, down_bias=P + 1)):
+        assert call(layer(**bad)) == MIS, bad
+    size = ctypes.c_size_t()
+    assert L.nvfp4_mx_moe_workspace(None, 4, 2, 1, ctypes.byref(size)) == INV
+    assert L.nvfp4_mx_moe_workspace(layer(), 4, 2, 1, None) == INV and L.nvfp4_mx_moe_workspace(layer(), -1, 2, 1, ctypes.byref(size)) == INV
+    assert L.nvfp4_mx_moe_workspace(layer(), tokens, 2, 1, ctypes.byref(size)) == nv.OK
+    need = size.value
+    assert call(layer(), n=need - 1) == INV
+    assert L.nvfp4_mx_moe_workspace(layer(), 0, 2, 1, ctypes.byref(size)) == nv.OK and size.value == 0
+    if record:
+        assert call(layer(), n=need) == nv.OK
+        assert call(layer(gate_packed=None, gate_scales=None, gate_bias=None), w=None, n=need) == nv.OK
+        assert call(layer(), T=0, x=None, ids=None, out=None, ws=None, n=0) == nv.OK
+        assert L.nvfp4_sequence_add_mx_moe(None, layer(), P, 1, 64, P, 0, P, 4, 2, P, 1, P, 1 << 40) == INV
+    L.nvfp4_sequence_destroy(seq)
+
+
+def test_moe_binding_refuses():
+    up, down, gate = groups(3, 96, 64), groups(3, 64, 96), groups(3, 96, 64)
+    x, ids, p = torch.zeros(4, 64), torch.zeros(4, 2, dtype=torch.int64), torch.zeros(4, 2)
+    seq, out = nv.Sequence(), torch.zeros(4, 64, dtype=torch.bfloat16)
+    for args, kw, match in [((x, ids, p, operand(96), down), {}, "up must be"), ((x, ids, p, up, operand(64, 96)), {}, "down must be"),
+                            ((x, ids, p, up, down), dict(gate=operand(96)), "gate must be"), ((x, ids, p, up, up), {}, "down must be 3"),
+                            ((x, ids, p, up, groups(2, 64, 96)), {}, "down must be 3"), ((x, ids, p, up, down), dict(gate=down), "gate must be 3"),
+                            ((x, ids, p, up, down), dict(gate_bias=torch.zeros(3, 96)), "needs a gate"),
+                            ((x[:, :32], ids, p, up, down), {}, "rows of 32"), ((x.half(), ids, p, up, down), {}, "float32 or bfloat16"),
+                            ((x, ids[:3], p, up, down), {}, "expert_ids"), ((x, ids.float(), p, up, down), {}, "expert_ids"),
+                            ((x, ids.t().contiguous().t(), p, up, down), {}, "expert_ids"), ((x, ids, p[:, :1], up, down), {}, "weights"),
+                            ((x, ids, p.double(), up, down), {}, "weights"), ((x, ids, p, up, down), dict(activation="elu"), "activation"),
+                            ((x, ids, p, up, down), dict(up_bias=torch.zeros(96)), "up_bias"),
+                            ((x, ids, p, up, down), dict(down_bias=torch.zeros(3, 96)), "down_bias"),
+                            ((x, ids, p, up, down), dict(up_bias=torch.zeros(3, 96), down_bias=torch.zeros(3, 64).bfloat16()), "one type"),
+                            ((x, ids, p, nv.MxGroups(up.codes[:-1], up.scales, 3, 96, 64), down), {}, "up.codes")]:
+        with pytest.raises(ValueError, match=match):
+            nv.mx_moe(*args, **kw)
+        with pytest.raises(ValueError, match=match):
+            seq.add_mx_moe(*args, out, **kw)
+    for kw, match in ((dict(out=torch.zeros(4, 63)), "out"), (dict(dtype=torch.float16), "out"), ({}, "GPU")):
+        with pytest.raises(ValueError, match=match):
+            nv.mx_moe(x, ids, p, up, down, gate, **kw)
+    with pytest.raises(ValueError, match="out"):
+        seq.add_mx_moe(x, ids, p, up, down, None)
+    assert seq.calls == 0

@@ -21,6 +21,7 @@ bool mx_fused_fits(const MxGemmArgs&) { return true; }
 bool mx_gated_fits(const MxGemmArgs&) { return true; }
 hipError_t launch_norm(const NormArgs&, hipStream_t) { return hipErrorInvalidValue; }
 hipError_t launch_norm_grad(const NormArgs&, hipStream_t) { return hipErrorInvalidValue; }
+hipError_t launch_mx_moe_few(const MxMoeArgs&, hipStream_t) { return hipErrorInvalidValue; }
 int norm_grad_parts(bool, int64_t, int) { return 3; }
 }
 """
