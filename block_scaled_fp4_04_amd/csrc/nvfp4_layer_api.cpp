@@ -91,8 +91,6 @@ int prepare_grouped_fused(const void* a_packed, const void* a_scales, int64_t a_
 
 // ---- a whole layer of experts -------------------------------------------------
 
-bool few(int64_t tokens, int64_t topk) { return tokens <= kMoeFewTokens && tokens * topk <= kMoeFewChoices; }
-
 int check_experts(const nvfp4_mx_experts* l, int64_t tokens, int64_t topk, int out_type) {
     auto valid_depth = [](int64_t K) { return K >= kMxBlock && K <= kMaxDim && K % kMxBlock == 0; };
     if (!l || l->experts < 1 || l->experts > kMoeMaxExperts || !valid_depth(l->hidden) || !valid_depth(l->inner) ||
@@ -115,17 +113,17 @@ struct MoeSpace {
         const int64_t pairs = tokens * topk;
         if (pairs == 0) return;
         h = take(pairs * l.inner, 2);
-        if (few(tokens, topk)) return;
+        if (mx_moe_few(tokens, topk, l.hidden, l.inner)) return;
         auto packed = [&](int64_t rows, int64_t K, size_t* codes, size_t* scales) {
             const int64_t rb = mx_row_blocks(rows), c = mx_steps(K);
             *codes = take(rb * c, kMxFrag);
             *scales = take(rb * ((c + 3) / 4), kMxScaleFrag);
         };
+        packed(tokens, l.hidden, &x_codes, &x_scales);
+        packed(pairs, l.inner, &h_codes, &h_scales);
         offsets = take(l.experts + 1, 4);
         slots = take(pairs, 4);
         row_tokens = take(pairs, 4);
-        packed(tokens, l.hidden, &x_codes, &x_scales);
-        packed(pairs, l.inner, &h_codes, &h_scales);
         y = take(pairs * l.hidden, size_of(out_type));
     }
 };
@@ -158,7 +156,7 @@ int prepare_mx_moe(const nvfp4_mx_experts* l, const void* x, int x_type, int64_t
         return NVFP4_ERR_MISALIGNED;
     if (tokens == 0) return NVFP4_OK;
     uint8_t* const w = static_cast<uint8_t*>(workspace);
-    if (few(tokens, topk)) {
+    if (mx_moe_few(tokens, topk, l->hidden, l->inner)) {
         Job& job = jobs[0];
         job = Job{};
         job.kind = JOB_LAUNCH;
@@ -215,6 +213,9 @@ int prepare_mx_moe(const nvfp4_mx_experts* l, const void* x, int x_type, int64_t
         st = prepare_grouped_fused(w + at.h_codes, w + at.h_scales, pairs, nullptr, l->down_packed, l->down_scales,
                                    offsets, l->experts, 1.0f, &down, w + at.y, out_type, pairs, l->hidden, l->inner,
                                    &jobs[4]);
+    // (up to about a tile of rows to an expert; the kernel is right for more)
+    if (st == NVFP4_OK && mx_steps(l->inner) <= 4 && pairs <= 16 * l->experts)
+        jobs[4].launch = +[](const Job& j, hipStream_t s) { return launch_mx_short(j.mx_gemm, j.epilogue, s); };
     if (st == NVFP4_OK)
         st = prepare_moe_combine(w + at.y, out_type, tokens, topk, l->hidden, slots, weights, out, &jobs[5]);
     if (st == NVFP4_OK) *count = kMoeJobs;

@@ -138,6 +138,18 @@ __device__ __forceinline__ mx_f4 mx_mfma16(const mx_u4& a, uint32_t sa, const mx
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(a), mx_operand(b), acc, 4, 4, S,
                                                             (int)sa, S, (int)sb);
 }
+// Keeps the matrix instructions that made x out of a branch that alone uses
+// it: the compiler moves them there, but they work on every lane of the wave
+// whoever takes the branch.  (A lane permute, here of each lane to itself, is
+// not moved.)
+__device__ __forceinline__ mx_f4 mx_pin(mx_f4 x) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+        const float f = x[v];  // (by value, as mx_pair)
+        x[v] = __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, f), 0xE4, 0xF, 0xF, true));
+    }
+    return x;
+}
 // The same for 32 x 32 rows over 64 elements: lane l brings row l % 32,
 // elements 32 * (l / 32) ...; result: row l % 32 of the second operand, rows
 // 8 * (v / 4) + 4 * (l / 32) + v % 4 of the first.

@@ -96,6 +96,8 @@ bool mx_gemm_fits(const MxGemmArgs& a);
 // The same with an epilogue.
 hipError_t launch_mx_fused(const MxGemmArgs& a, const MxEpilogueArgs& e, hipStream_t stream);
 hipError_t launch_mx_gated(const MxGemmArgs& a, const MxEpilogueArgs& e, hipStream_t stream);
+// Grouped, rows of A in order, up to four steps and kMoeMaxExperts groups, a bias at most.
+hipError_t launch_mx_short(const MxGemmArgs& a, const MxEpilogueArgs& e, hipStream_t stream);
 bool mx_fused_fits(const MxGemmArgs& a);
 bool mx_gated_fits(const MxGemmArgs& a);
 
@@ -151,8 +153,9 @@ hipError_t launch_norm_grad(const NormArgs& a, hipStream_t stream);
 int norm_grad_parts(bool bf16, int64_t rows, int hidden);
 
 // A whole layer of experts for few tokens (include/nvfp4_layer.h).
-constexpr int kMoeFewTokens = 64;   // a wave's lanes
+constexpr int kMoeFewTokens = 4;
 constexpr int kMoeFewChoices = 512;
+constexpr int64_t kMoeImageBytes = 48 << 10;  // of quantised rows in LDS
 struct MxMoeArgs {
     const void* x;               // tokens x hidden (fp32, or bfloat16 if x_bf16), row stride ldx
     bool x_bf16, wide, bias_bf16, out_bf16;
@@ -169,6 +172,8 @@ struct MxMoeArgs {
     uint16_t* h;                 // workspace: [tokens * topk][inner] bfloat16
     void* out;                   // tokens x hidden
 };
+// Whether it takes a layer of these sizes.
+bool mx_moe_few(int64_t tokens, int64_t topk, int64_t hidden, int64_t inner);
 hipError_t launch_mx_moe_few(const MxMoeArgs& a, hipStream_t stream);
 
 }  // namespace nvfp4

@@ -1,13 +1,17 @@
 // nvfp4_mx_moe.hip -- gfx950 kernels of a whole layer of experts for few
-// tokens (include/nvfp4_layer.h), in two launches:
+// tokens (include/nvfp4_layer.h):
 //   h[t][e]  = bf16(act(q(x[t]) . Wg_e^T + bg_e) * (q(x[t]) . Wu_e^T + bu_e))
 //   out[t]   = sum over t's experts e of p[t][e] * (q(h[t][e]) . Wd_e^T + bd_e)
 // with q() the MXFP4 quantisation and p the router's weight.
 //
 // Bound by the weights of the experts that were chosen, which are read once:
-// every workgroup finds those experts itself from the router's choices, the
-// rows are quantised where they are multiplied, and the sum over a token's
-// experts stays in registers, so nothing but h is written on the way.
+// every workgroup finds those experts itself from the router's choices, and
+// the sum over a token's experts stays in registers, so that nothing but h is
+// written on the way.  The weights go straight to the registers of the lanes
+// that multiply them, a scale word (four steps, 4 KB of a row block) ahead of
+// the one that is multiplied, also past the end of a task.
+// x, and in the second launch h, are quantised by every workgroup into an
+// image in its LDS, while its first weights are on their way.
 #include "nvfp4_mx_parts.h"
 
 #include <algorithm>
@@ -15,356 +19,258 @@
 namespace nvfp4 {
 namespace {
 
-constexpr int kMoeWaves = 4;
-constexpr int kMoeWG = kMoeWaves * 64;
-constexpr int kMoeTiles = kMoeFewTokens / 16;  // of 16 rows
-
-// LDS of a workgroup.  Three of them fit a CU.
-struct MoeLds {
-    uint8_t b[kMoeWaves][2][4 * kMxFrag];              // a wave's weights: this item's and the next one's
-    uint8_t a[kMoeWaves][4 * kMxFrag + kMxScaleFrag];  // its quantised rows; the sums at the end of a task
-    uint32_t list[kMoeWaves][2][kMoeFewTokens];        // rows of this item's and the next one's expert
-    int16_t id[kMoeFewChoices], expert[kMoeFewChoices];
+// A workgroup's view of the router's choices.
+struct MoeChoices {
+    int16_t id[kMoeFewChoices];      // expert of each choice, -1: dropped
+    int16_t expert[kMoeFewChoices];  // the experts among them, by their first choice
+    int count;
 };
-static_assert(sizeof(MoeLds) <= 160 * 1024 / 3, "three workgroups to a CU");
-static_assert(kMoeMaxExperts * 4 <= sizeof(MoeLds::b) && kMoeMaxExperts < 32768, "the table of the experts' first choices");
 
-// Reads the choices and numbers the experts among them in the order of their
-// first choice: lds.id (-1: dropped), lds.expert; returns how many there are.
-__device__ __forceinline__ int moe_experts(const MxMoeArgs& a, MoeLds& lds) {
+// Fills it; `first`: LDS for kMoeMaxExperts integers.  Ends with a barrier.
+__device__ __forceinline__ void moe_choices(const MxMoeArgs& a, MoeChoices& c, int* first) {
     const int tid = threadIdx.x, lane = tid & 63, n = a.tokens * a.topk;
-    int* const first = reinterpret_cast<int*>(lds.b);
-    __shared__ int count;
-    for (int i = tid; i < n; i += kMoeWG) {
+    for (int i = tid; i < n; i += blockDim.x) {
         const int64_t e = a.wide ? static_cast<const int64_t*>(a.ids)[i] : static_cast<const int32_t*>(a.ids)[i];
         const bool kept = e >= 0 && e < a.experts;
-        lds.id[i] = (int16_t)(kept ? e : -1);
+        c.id[i] = (int16_t)(kept ? e : -1);
         if (kept) first[e] = n;
     }
     __syncthreads();
-    for (int i = tid; i < n; i += kMoeWG)
-        if (lds.id[i] >= 0) atomicMin(&first[lds.id[i]], i);
+    for (int i = tid; i < n; i += blockDim.x)
+        if (c.id[i] >= 0) atomicMin(&first[c.id[i]], i);
     __syncthreads();
     if (tid < 64) {
         int found = 0;
         for (int i0 = 0; i0 < n; i0 += 64) {
-            const int i = i0 + lane, e = i < n ? lds.id[i] : -1;
+            const int i = i0 + lane, e = i < n ? c.id[i] : -1;
             const bool leads = e >= 0 && first[e] == i;
             const uint64_t who = __ballot(leads);
-            if (leads) lds.expert[found + __popcll(who & ((1ull << lane) - 1))] = (int16_t)e;
+            if (leads) c.expert[found + __popcll(who & ((1ull << lane) - 1))] = (int16_t)e;
             found += __popcll(who);
         }
-        if (lane == 0) count = found;
+        if (lane == 0) c.count = found;
     }
     __syncthreads();
-    return count;
 }
 
-// The tokens of expert e, a bit each, and a row of the wave's list for each:
-// token | number of its first choice of e << 16.  weight: the lane's token's,
-// over all its choices of e.
-__device__ __forceinline__ uint64_t moe_rows(const MxMoeArgs& a, MoeLds& lds, int e, int slot, float& weight) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int at = -1, times = 0;
-    if (lane < a.tokens)
-        for (int j = a.topk - 1; j >= 0; --j)
-            if (lds.id[lane * a.topk + j] == e) {
-                at = lane * a.topk + j;
-                ++times;
-            }
-    const uint64_t who = __ballot(at >= 0);
-    weight = at < 0 ? 0.0f : a.weights ? a.weights[at] : 1.0f;
-    for (int j = at + 1; times > 1; ++j)  // the same expert more than once
-        if (lds.id[j] == e) {
-            weight += a.weights ? a.weights[j] : 1.0f;
-            --times;
-        }
-    if (at >= 0) lds.list[wave][slot][__popcll(who & ((1ull << lane) - 1))] = (uint32_t)(lane | at << 16);
-    mx_wave_fence();
-    return who;
-}
-
-// Four steps (a scale word) of a row block of 16 rows of a weight, or of eight
-// rows of each of two weights (PAIR: half `half` of row block rb of both), to
-// LDS; returns the lane's scales.  Steps past the last one are past the
-// buffer's range; what they leave in LDS is multiplied by zeros of the rows,
-// under scale bytes of zero.
-template <bool PAIR>
-__device__ __forceinline__ uint32_t moe_load(const uint8_t* codes0, const uint8_t* codes1, const uint8_t* scales0,
-                                             const uint8_t* scales1, int64_t rb, int half, int q, int C, uint32_t lds) {
-    const int lane = threadIdx.x & 63, r16 = lane & 15, kg = lane >> 4, Q = (C + 3) / 4;
-    const int64_t at = (rb * C + 4 * q) * kMxFrag;
-    const uint32_t bytes = (uint32_t)min(4, C - 4 * q) * kMxFrag;
-    const __amdgpu_buffer_rsrc_t r0 = make_rsrc(codes0 + at, bytes);
-    const uint8_t* s = scales0;
-    int row = r16;
-    if constexpr (PAIR) {
-        const __amdgpu_buffer_rsrc_t r1 = make_rsrc(codes1 + at, bytes);
-        const uint32_t from = (uint32_t)((lane >> 5) * kMxFrag + half * (kMxFrag / 2) + (lane & 31) * 16);
-        mx_each<4>([&](auto I) {  // two steps of one weight, then of the other
-            constexpr int i = I.value;
-            if constexpr (i % 2 == 0)
-                mx_dma<16, i * kMxFrag>(r0, from + i / 2 * 2 * kMxFrag, 0, lds);
-            else
-                mx_dma<16, i * kMxFrag>(r1, from + i / 2 * 2 * kMxFrag, 0, lds);
-        });
-        if (r16 >= 8) s = scales1;
-        row = half * 8 + (r16 & 7);
-    } else {
-        mx_each<4>([&](auto I) { mx_dma<16, I.value * kMxFrag>(r0, lane * 16 + I.value * kMxFrag, 0, lds); });
-    }
-    return *reinterpret_cast<const uint32_t*>(s + (rb * Q + q) * kMxScaleFrag + mx_scale_at(row, kg));
-}
-// Where the lane's 16 bytes of step S of what moe_load brought lie.
-template <bool PAIR, int S>
-__device__ __forceinline__ int moe_code_at(int half) {
-    const int lane = threadIdx.x & 63, r16 = lane & 15, kg = lane >> 4;
-    if constexpr (PAIR) {
-        const int row = half * 8 + (r16 & 7);
-        return S / 2 * 2 * kMxFrag + (r16 >> 3) * kMxFrag + (S & 1) * (kMxFrag / 2) + (r16 & 7) * 64 + ((kg ^ (row >> 2)) << 4);
-    }
-    return S * kMxFrag + mx_code_at(r16, kg);
-}
-
-// A row's block for the lane, if it has one: lane l takes block l % 16 of scale
-// word q of row l / 16 of four.
-template <typename T>
-__device__ __forceinline__ MxRaw<T> moe_raw(const T* rows, int64_t ld, int row, bool live, int q, int K) {
-    const int k = q * 4 * kMxStep + (threadIdx.x & 15) * kMxBlock;
-    MxRaw<T> r;
+// A token's first choice of expert e, as a row of h; -1: none, or no token.
+__device__ __forceinline__ int moe_row(const MxMoeArgs& a, const MoeChoices& c, int e, int token) {
+    const int16_t* const id = c.id + min(token, a.tokens - 1) * a.topk;
+    int at = -1;
+    for (int j0 = 0; j0 < a.topk; j0 += 8) {
+        int x[8];
 #pragma unroll
-    for (int i = 0; i < r.L; ++i) r.v[i] = mx_u4{0, 0, 0, 0};
-    if (live && k < K) r = mx_raw_load(rows + row * ld + k);
-    return r;
+        for (int j = 0; j < 8; ++j) x[j] = id[min(j0 + j, a.topk - 1)];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (x[j] == e && at < 0) at = j0 + j;  // (the last choice again: found before)
+    }
+    return token < a.tokens && at >= 0 ? token * a.topk + at : -1;
 }
-// Quantises it to row `to` of the wave's operand.
-template <typename T>
-__device__ __forceinline__ void moe_quantize(const MxRaw<T>& r, uint8_t* a_lds, int to, bool live) {
-    if (!live) return;
-    const int s = (threadIdx.x & 15) >> 2, b = threadIdx.x & 3;
-    mx_u4 w;
-    const uint32_t byte = mx_quant_block(r, w);
-    *reinterpret_cast<mx_u4*>(a_lds + s * kMxFrag + mx_code_at(to, b)) = w;
-    a_lds[4 * kMxFrag + mx_scale_at(to, b) + s] = (uint8_t)byte;
+// The router's weight of the token for the expert, over all its choices of it.
+// `weights`: in LDS.
+__device__ __forceinline__ float moe_weight(const MxMoeArgs& a, const MoeChoices& c, int e, int at, int token, const float* weights) {
+    if (at < 0) return 0.0f;
+    float w = weights[at];
+    for (int j = at + 1; j < (token + 1) * a.topk; ++j)
+        if (c.id[j] == e) w += weights[j];
+    return w;
 }
 
-// acc += the weights in b_lds by the rows in a_lds, four steps.  Rows of a_lds
-// that nothing was written to give whatever LDS held: not used.
-template <bool PAIR>
-__device__ __forceinline__ mx_f4 moe_multiply(const uint8_t* b_lds, uint32_t sb, int half, const uint8_t* a_lds, mx_f4 acc) {
-    const int lane = threadIdx.x & 63, r16 = lane & 15, kg = lane >> 4;
-    const uint32_t sa = *reinterpret_cast<const uint32_t*>(a_lds + 4 * kMxFrag + mx_scale_at(r16, kg));
-    mx_each<4>([&](auto S) {
-        const mx_u4 wb = *reinterpret_cast<const mx_u4*>(b_lds + moe_code_at<PAIR, S.value>(half));
-        const mx_u4 wa = *reinterpret_cast<const mx_u4*>(a_lds + S.value * kMxFrag + mx_code_at(r16, kg));
-        acc = mx_mfma16<S.value>(wb, sb, wa, sa, acc);
-    });
+// What a wave multiplies at a time: four steps of 16 rows of a weight and of
+// its rows of activations (in one tile), a lane's share.
+struct MoeFrag {
+    mx_u4 b[4], a[4];
+    uint32_t sb, sa;
+};
+
+// The lane's 16 code bytes of each step of scale word q: `codes` points to its
+// place in the row block's step 0.  Steps past the last one: zeros.
+__device__ __forceinline__ void moe_steps(const uint8_t* codes, int q, int C, mx_u4 (&w)[4]) {
+    const uint8_t* p = codes + (int64_t)q * 4 * kMxFrag;
+    const int n = C - 4 * q;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        w[s] = mx_u4{0, 0, 0, 0};
+        if (s < n) w[s] = *reinterpret_cast<const mx_u4*>(p + s * kMxFrag);
+    }
+}
+__device__ __forceinline__ uint32_t moe_word(const uint8_t* scales, int q) {
+    return *reinterpret_cast<const uint32_t*>(scales + (int64_t)q * kMxScaleFrag);
+}
+__device__ __forceinline__ mx_f4 moe_multiply(const MoeFrag& f, mx_f4 acc) {
+    mx_each<4>([&](auto S) { acc = mx_mfma16<S.value>(f.b[S.value], f.sb, f.a[S.value], f.sa, acc); });
     return acc;
 }
 
+// ---- quantised rows in LDS ------------------------------------------------
+// Rows of K, padded to whole scale words with zeros: [row][word][step][block]
+// of 16 code bytes, and a word of scale bytes for each [row][word][block].
+__host__ __device__ constexpr int64_t moe_image_bytes(int64_t rows, int64_t K) {
+    return rows * ((K + 4 * kMxStep - 1) / (4 * kMxStep)) * (16 * 16 + 16);
+}
+template <typename T>
+__device__ __forceinline__ void moe_image(const T* x, int64_t ld, int rows, int K, uint8_t* image) {
+    const int Q = (K + 4 * kMxStep - 1) / (4 * kMxStep), blocks = Q * 16;
+    uint8_t* const scales = image + rows * blocks * 16;
+    for (int i = threadIdx.x; i < rows * blocks; i += blockDim.x) {
+        const int row = i / blocks, b = i % blocks;
+        mx_u4 w = {0, 0, 0, 0};
+        uint32_t byte = 0;
+        if (b * kMxBlock < K) byte = mx_quant_load(x + row * ld + b * kMxBlock, w);
+        *reinterpret_cast<mx_u4*>(image + i * 16) = w;
+        scales[((row * Q + (b >> 4)) * 4 + (b & 3)) * 4 + (b >> 2 & 3)] = (uint8_t)byte;
+    }
+}
+// The lane's share of word q of a row (its block l / 16 of each step).
+__device__ __forceinline__ void moe_from_image(const uint8_t* image, int rows, int Q, int row, int q, MoeFrag& f) {
+    const int kg = (threadIdx.x & 63) >> 4;
+    const uint8_t* const p = image + ((row * Q + q) * 16 + kg) * 16;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) f.a[s] = *reinterpret_cast<const mx_u4*>(p + s * 64);
+    f.sa = *reinterpret_cast<const uint32_t*>(image + rows * Q * 256 + ((row * Q + q) * 4 + kg) * 4);
+}
+
 // ---------------------------------------------------------------------------
-// First kernel.  A task is eight columns of h of one expert (with a gate: eight
-// rows of each weight make the 16 of one matrix instruction) or 16 (without),
-// for all its tokens; the workgroups walk the tasks, and a task's waves split K,
-// a scale word (512 elements) at a time.  While a wave multiplies one word, the
-// weights and the rows of the next are on their way, also past the end of the
-// task.
+// First kernel.  A task is eight columns of h of one expert (with a gate:
+// eight rows of each weight make the 16 of a matrix instruction) or 16
+// (without), for all tokens; its waves split K.  h: [choice][inner] bfloat16.
 // ---------------------------------------------------------------------------
+constexpr int kUpWaves = 8;
+
 template <typename T, bool GATED>
-__global__ void __launch_bounds__(kMoeWG) moe_up_kernel(MxMoeArgs a) {
+__global__ void __launch_bounds__(kUpWaves * 64) moe_up_few_kernel(MxMoeArgs a) {
     constexpr int COLS = GATED ? 8 : 16;
-    __shared__ __attribute__((aligned(1024))) MoeLds lds;
+    extern __shared__ __attribute__((aligned(1024))) uint8_t image[];
+    __shared__ MoeChoices choices;
+    __shared__ __attribute__((aligned(16))) union { int first[kMoeMaxExperts]; mx_f4 red[kUpWaves][64]; } u;
     const int lane = threadIdx.x & 63, r16 = lane & 15, kg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int C = (a.hidden + kMxStep - 1) / kMxStep, Q = (C + 3) / 4;
-    const int units = a.inner / COLS, RB = a.inner / 16;
-    const int total = __builtin_amdgcn_readfirstlane(moe_experts(a, lds)) * units, turn = gridDim.x;
-    const T* const x = static_cast<const T*>(a.x);
-    uint8_t* const a_lds = lds.a[wave];
-    float unused;
-
-    auto expert_of = [&](int task) { return __builtin_amdgcn_readfirstlane((int)lds.expert[task / units]); };
-    auto load = [&](int task, int q, int slot) {
-        const int u = task % units;
-        const int64_t rb = (int64_t)expert_of(task) * RB + (GATED ? u >> 1 : u);
-        return moe_load<GATED>(GATED ? a.gate_codes : a.up_codes, a.up_codes, GATED ? a.gate_scales : a.up_scales, a.up_scales,
-                               rb, u & 1, q, C, lds_addr(lds.b[wave][slot]));
-    };
-    // rows first .. first + 3 of a list
-    auto raw_of = [&](int slot, int rows, int first, int q) {
-        const int n = first + (lane >> 4);
-        const int token = n < rows ? (int)(lds.list[wave][slot][n] & 0xFFFF) : 0;
-        return moe_raw<T>(x, a.ldx, token, n < rows, q, a.hidden);
-    };
-
+    const int units = a.inner / COLS, RB = a.inner / 16, turn = gridDim.x;
+    moe_choices(a, choices, u.first);
+    const int total = __builtin_amdgcn_readfirstlane(choices.count) * units;
     int task = blockIdx.x;
     if (task >= total) return;
-    int k = 0, slot = 0;  // places of the list and of the weights
-    int rows = __popcll(moe_rows(a, lds, expert_of(task), 0, unused));
-    uint32_t sb = 0;
-    MxRaw<T> raw;
-    if (wave < Q) {
-        raw = raw_of(0, rows, 0, wave);
-        sb = load(task, wave, 0);
-    }
+
+    const bool second = GATED && r16 >= 8;  // (the lane's row is one of the up weight)
+    const uint8_t* const codes = GATED && !second ? a.gate_codes : a.up_codes;
+    const uint8_t* const scales = GATED && !second ? a.gate_scales : a.up_scales;
+    auto expert_of = [&](int t) { return __builtin_amdgcn_readfirstlane((int)choices.expert[t / units]); };
+    auto load = [&](int t, int q) {
+        const int unit = t % units, row = GATED ? (unit & 1) * 8 + (r16 & 7) : r16;
+        const int64_t rb = (int64_t)expert_of(t) * RB + (GATED ? unit >> 1 : unit);
+        MoeFrag f;
+        moe_steps(codes + rb * C * kMxFrag + mx_code_at(row, kg), q, C, f.b);
+        f.sb = moe_word(scales + rb * Q * kMxScaleFrag + mx_scale_at(row, kg), q);
+        return f;
+    };
+    MoeFrag next;
+    if (wave < Q) next = load(task, wave);
+    moe_image(static_cast<const T*>(a.x), a.ldx, a.tokens, a.hidden, image);
+    __syncthreads();
     for (; task < total; task += turn) {
-        const int e = expert_of(task), u = task % units, tiles = (rows + 15) / 16;
-        const bool more = task + turn < total;
-        int next_rows = 0;
-        if (more) next_rows = __popcll(moe_rows(a, lds, expert_of(task + turn), k ^ 1, unused));
-        mx_f4 acc[kMoeTiles];
-#pragma unroll
-        for (int t = 0; t < kMoeTiles; ++t) acc[t] = mx_f4{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int q = wave; q < Q; q += kMoeWaves) {
-            wait_vmcnt<0>();
-            asm volatile("" ::: "memory");  // the weights have landed
-            const MxRaw<T> now = raw;
-            const uint32_t sb_now = sb;
-            const uint8_t* const b_lds = lds.b[wave][slot];
-            slot ^= 1;
-            if (q + kMoeWaves < Q) {
-                raw = raw_of(k, rows, 0, q + kMoeWaves);
-                sb = load(task, q + kMoeWaves, slot);
-            } else if (more) {
-                raw = raw_of(k ^ 1, next_rows, 0, wave);
-                sb = load(task + turn, wave, slot);
-            }
-#pragma unroll
-            for (int t = 0; t < kMoeTiles; ++t) {
-                if (t >= tiles) break;
-                const int live = min(rows - t * 16, 16);
-                moe_quantize(t == 0 ? now : raw_of(k, rows, t * 16, q), a_lds, lane >> 4, (lane >> 4) < live);
-                for (int p = 4; p < live; p += 4)
-                    moe_quantize(raw_of(k, rows, t * 16 + p, q), a_lds, p + (lane >> 4), p + (lane >> 4) < live);
-                mx_wave_fence();
-                acc[t] = moe_multiply<GATED>(b_lds, sb_now, u & 1, a_lds, acc[t]);
-                mx_wave_fence();
-            }
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // LDS is read before it is filled again
+        const int e = expert_of(task), unit = task % units;
+        mx_f4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int q = wave; q < Q; q += kUpWaves) {
+            MoeFrag f = next;
+            if (q + kUpWaves < Q)
+                next = load(task, q + kUpWaves);
+            else if (task + turn < total)
+                next = load(task + turn, wave);
+            moe_from_image(image, a.tokens, Q, min(r16, a.tokens - 1), q, f);
+            acc = moe_multiply(f, acc);
         }
-        // the waves' sums, added in their order, a tile to a wave
-#pragma unroll
-        for (int t = 0; t < kMoeTiles; ++t)
-            if (t < tiles) reinterpret_cast<mx_f4*>(a_lds)[t * 64 + lane] = acc[t];
+        u.red[wave][lane] = acc;
         __syncthreads();
-        if (wave < tiles) {
+        if (wave == 0) {
+            const int at = moe_row(a, choices, e, r16);
             auto sum_of = [&](int from) {
-                mx_f4 s = reinterpret_cast<const mx_f4*>(lds.a[0])[wave * 64 + from];
+                mx_f4 s = u.red[0][from];
 #pragma unroll
-                for (int w = 1; w < kMoeWaves; ++w) s += reinterpret_cast<const mx_f4*>(lds.a[w])[wave * 64 + from];
+                for (int w = 1; w < kUpWaves; ++w) s += u.red[w][from];
                 return s;
             };
-            const int n = wave * 16 + r16;
-            if (n < rows && (!GATED || kg < 2)) {
-                const int col = u * COLS + 4 * kg;
-                const int64_t at = (int64_t)e * a.inner + col;
+            if (at >= 0 && (!GATED || kg < 2)) {
+                const int col = unit * COLS + 4 * kg;
+                const int64_t b = (int64_t)e * a.inner + col;
                 mx_f4 z = sum_of(lane);
-                const mx_f4 bias = mx_row4(a.up_bias, a.bias_bf16, at, col, a.inner);
+                const mx_f4 bias = mx_row4(a.up_bias, a.bias_bf16, b, col, a.inner);
                 if constexpr (GATED)
-                    z = mx_act(z + mx_row4(a.gate_bias, a.bias_bf16, at, col, a.inner), a.act) * (sum_of(lane + 32) + bias);
+                    z = mx_act(z + mx_row4(a.gate_bias, a.bias_bf16, b, col, a.inner), a.act) * (sum_of(lane + 32) + bias);
                 else
                     z = mx_act(z + bias, a.act);
-                mx_put4(a.h, true, (int64_t)(lds.list[wave][k][n] >> 16) * a.inner + col, col, a.inner, z);
+                mx_put4(a.h, true, (int64_t)at * a.inner + col, col, a.inner, z);
             }
         }
         __syncthreads();
-        rows = next_rows;
-        k ^= 1;
     }
 }
 
 // ---------------------------------------------------------------------------
 // Second kernel.  A task is 16 columns of the result, for all tokens and all
 // experts: the waves split the pairs of (expert, scale word of its inner
-// dimension), multiply the expert's rows of h, and add them under the router's
-// weights in registers; the waves' sums are added in their order at the end of
-// the task.
+// dimension), multiply the rows of h, and add them under the router's weights
+// in registers; the waves' sums are added in their order at the end of the
+// task.  h is quantised into LDS first.
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(kMoeWG) moe_down_kernel(MxMoeArgs a) {
-    __shared__ __attribute__((aligned(1024))) MoeLds lds;
+constexpr int kDownWaves = 8;
+
+__global__ void __launch_bounds__(kDownWaves * 64) moe_down_few_kernel(MxMoeArgs a) {
+    extern __shared__ __attribute__((aligned(1024))) uint8_t image[];
+    __shared__ MoeChoices choices;
+    __shared__ float weights[kMoeFewChoices];
+    __shared__ __attribute__((aligned(16))) union { int first[kMoeMaxExperts]; mx_f4 red[kDownWaves][64]; } u;
     const int lane = threadIdx.x & 63, r16 = lane & 15, kg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int C = (a.inner + kMxStep - 1) / kMxStep, Q = (C + 3) / 4;
-    const int RB = (a.hidden + 15) / 16, turn = gridDim.x;
-    const int items = __builtin_amdgcn_readfirstlane(moe_experts(a, lds)) * Q;
-    const int tiles = (a.tokens + 15) / 16;
-    uint8_t* const a_lds = lds.a[wave];
+    const int RB = (a.hidden + 15) / 16, turn = gridDim.x, pairs = a.tokens * a.topk;
+    for (int i = threadIdx.x; i < pairs; i += kDownWaves * 64) weights[i] = a.weights ? a.weights[i] : 1.0f;
+    moe_choices(a, choices, u.first);
+    const int items = __builtin_amdgcn_readfirstlane(choices.count) * Q;
 
     struct Item {
-        int e, q;
-        uint64_t who;      // its tokens
-        float weight;      // of the lane's token
-        uint32_t sb;
-        MxRaw<uint16_t> raw;
+        int e, q, at;      // at: the lane's row of h, of token l % 16 (-1: none)
+        float weight;      // of that token
+        MoeFrag f;
     };
-    auto raw_of = [&](int slot, uint64_t who, int t, int p, int q) {
-        const int before = __popcll(who & ((1ull << (t * 16)) - 1)), live = __popc((uint32_t)(who >> (t * 16)) & 0xFFFF);
-        const int n = p + (lane >> 4);
-        const int row = n < live ? (int)(lds.list[wave][slot][before + n] >> 16) : 0;
-        return moe_raw<uint16_t>(a.h, a.inner, row, n < live, q, a.inner);
-    };
-    auto first_tile = [&](uint64_t who) { return (__ffsll((unsigned long long)who) - 1) >> 4; };
-    auto fetch = [&](int cb, int i, int slot) {
+    auto fetch = [&](int cb, int i) {
         Item n;
-        n.e = __builtin_amdgcn_readfirstlane((int)lds.expert[i / Q]);
+        n.e = __builtin_amdgcn_readfirstlane((int)choices.expert[i / Q]);
         n.q = i % Q;
-        n.who = moe_rows(a, lds, n.e, slot, n.weight);
-        n.raw = raw_of(slot, n.who, first_tile(n.who), 0, n.q);
-        n.sb = moe_load<false>(a.down_codes, nullptr, a.down_scales, nullptr, (int64_t)n.e * RB + cb, 0, n.q, C,
-                               lds_addr(lds.b[wave][slot]));
+        const int64_t rb = (int64_t)n.e * RB + cb;
+        moe_steps(a.down_codes + rb * C * kMxFrag + mx_code_at(r16, kg), n.q, C, n.f.b);
+        n.f.sb = moe_word(a.down_scales + rb * Q * kMxScaleFrag + mx_scale_at(r16, kg), n.q);
+        n.at = moe_row(a, choices, n.e, r16);
+        n.weight = moe_weight(a, choices, n.e, n.at, r16, weights);
         return n;
     };
-
-    int slot = 0;
-    Item next{};
-    if (wave < items && (int)blockIdx.x < RB) next = fetch(blockIdx.x, wave, 0);
+    Item next;
+    if (wave < items && (int)blockIdx.x < RB) next = fetch(blockIdx.x, wave);
+    moe_image(a.h, a.inner, pairs, a.inner, image);
+    __syncthreads();
     for (int cb = blockIdx.x; cb < RB; cb += turn) {
         const int col = cb * 16 + 4 * kg;
-        mx_f4 sum[kMoeTiles];
-#pragma unroll
-        for (int t = 0; t < kMoeTiles; ++t) sum[t] = mx_f4{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int i = wave; i < items; i += kMoeWaves) {
-            wait_vmcnt<0>();
-            asm volatile("" ::: "memory");  // the weights have landed
-            const Item now = next;
-            const int here = slot;
-            slot ^= 1;
-            if (i + kMoeWaves < items)
-                next = fetch(cb, i + kMoeWaves, slot);
+        mx_f4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = wave; i < items; i += kDownWaves) {
+            Item now = next;
+            if (i + kDownWaves < items)
+                next = fetch(cb, i + kDownWaves);
             else if (cb + turn < RB)
-                next = fetch(cb + turn, wave, slot);
-            const int t0 = first_tile(now.who);
+                next = fetch(cb + turn, wave);
             mx_f4 bias = {0.0f, 0.0f, 0.0f, 0.0f};
             if (now.q == 0) bias = mx_row4(a.down_bias, a.bias_bf16, (int64_t)now.e * a.hidden + col, col, a.hidden);
-#pragma unroll
-            for (int t = 0; t < kMoeTiles; ++t) {
-                if (t >= tiles) break;
-                const uint32_t who = (uint32_t)(now.who >> (t * 16)) & 0xFFFF;
-                if (who == 0) continue;
-                const int live = __popc(who), before = __popcll(now.who & ((1ull << (t * 16)) - 1));
-                for (int p = 0; p < live; p += 4) {
-                    const int n = p + (lane >> 4);
-                    const int to = n < live ? (int)(lds.list[wave][here][before + n] & 15) : 0;
-                    moe_quantize(p == 0 && t == t0 ? now.raw : raw_of(here, now.who, t, p, now.q), a_lds, to, n < live);
-                }
-                mx_wave_fence();
-                const mx_f4 y = moe_multiply<false>(lds.b[wave][here], now.sb, 0, a_lds, bias);
-                mx_wave_fence();
-                const float w = __shfl(now.weight, t * 16 + r16);
-                if (who >> r16 & 1) sum[t] += w * y;
-            }
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // LDS is read before it is filled again
+            moe_from_image(image, pairs, Q, max(now.at, 0), now.q, now.f);
+            const mx_f4 y = mx_pin(moe_multiply(now.f, bias));
+            if (now.at >= 0) sum += now.weight * y;
         }
-#pragma unroll
-        for (int t = 0; t < kMoeTiles; ++t)
-            if (t < tiles) reinterpret_cast<mx_f4*>(a_lds)[t * 64 + lane] = sum[t];
+        u.red[wave][lane] = sum;
         __syncthreads();
-        if (wave < tiles) {
-            mx_f4 s = reinterpret_cast<const mx_f4*>(lds.a[0])[wave * 64 + lane];
+        if (wave == 0) {
+            mx_f4 s = u.red[0][lane];
 #pragma unroll
-            for (int w = 1; w < kMoeWaves; ++w) s += reinterpret_cast<const mx_f4*>(lds.a[w])[wave * 64 + lane];
-            const int token = wave * 16 + r16;
-            if (token < a.tokens) mx_put4(a.out, a.out_bf16, (int64_t)token * a.hidden + col, col, a.hidden, s);
+            for (int w = 1; w < kDownWaves; ++w) s += u.red[w][lane];
+            if (r16 < a.tokens) mx_put4(a.out, a.out_bf16, (int64_t)r16 * a.hidden + col, col, a.hidden, s);
         }
         __syncthreads();
     }
@@ -372,26 +278,32 @@ __global__ void __launch_bounds__(kMoeWG) moe_down_kernel(MxMoeArgs a) {
 
 }  // namespace
 
+bool mx_moe_few(int64_t tokens, int64_t topk, int64_t hidden, int64_t inner) {
+    return tokens <= kMoeFewTokens && tokens * topk <= kMoeFewChoices && moe_image_bytes(tokens, hidden) <= kMoeImageBytes &&
+           moe_image_bytes(tokens * topk, inner) <= kMoeImageBytes;
+}
+
 hipError_t launch_mx_moe_few(const MxMoeArgs& a, hipStream_t stream) {
-    constexpr int kResident = 3 * 256;  // workgroups that the GPU holds at once
+    constexpr int kResident = 2 * 256;  // workgroups that the GPU holds at once
     const bool gated = a.gate_codes != nullptr;
-    const int units = a.inner / (gated ? 8 : 16);
-    const int most = std::min<int64_t>((int64_t)std::min(a.tokens * a.topk, a.experts) * units, kResident);
-    const dim3 up((unsigned)most), down((unsigned)std::min((a.hidden + 15) / 16, kResident)), block(kMoeWG);
+    const int64_t experts = std::min(a.tokens * a.topk, a.experts);
+    const size_t image = (size_t)moe_image_bytes(a.tokens, a.hidden);
+    const dim3 up((unsigned)std::min<int64_t>(experts * (a.inner / (gated ? 8 : 16)), kResident)), block(kUpWaves * 64);
     if (gated) {
         if (a.x_bf16)
-            hipLaunchKernelGGL((moe_up_kernel<uint16_t, true>), up, block, 0, stream, a);
+            hipLaunchKernelGGL((moe_up_few_kernel<uint16_t, true>), up, block, image, stream, a);
         else
-            hipLaunchKernelGGL((moe_up_kernel<float, true>), up, block, 0, stream, a);
+            hipLaunchKernelGGL((moe_up_few_kernel<float, true>), up, block, image, stream, a);
     } else {
         if (a.x_bf16)
-            hipLaunchKernelGGL((moe_up_kernel<uint16_t, false>), up, block, 0, stream, a);
+            hipLaunchKernelGGL((moe_up_few_kernel<uint16_t, false>), up, block, image, stream, a);
         else
-            hipLaunchKernelGGL((moe_up_kernel<float, false>), up, block, 0, stream, a);
+            hipLaunchKernelGGL((moe_up_few_kernel<float, false>), up, block, image, stream, a);
     }
     const hipError_t error = hipGetLastError();
     if (error != hipSuccess) return error;
-    hipLaunchKernelGGL(moe_down_kernel, down, block, 0, stream, a);
+    hipLaunchKernelGGL(moe_down_few_kernel, dim3((unsigned)std::min((a.hidden + 15) / 16, kResident)), dim3(kDownWaves * 64),
+                       (size_t)moe_image_bytes((int64_t)a.tokens * a.topk, a.inner), stream, a);
     return hipGetLastError();
 }
 

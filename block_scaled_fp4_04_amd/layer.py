@@ -218,7 +218,7 @@ def mx_moe(x, expert_ids, weights, up: MxGroups, down: MxGroups, gate: MxGroups 
     held in bfloat16 and quantised.  x: [tokens, hidden], rows strided as in
     mx_quantize; ``up`` and ``gate`` are [experts, inner, hidden], ``down``
     [experts, hidden, inner]; biases [experts, inner] and [experts, hidden].
-    Two launches up to 64 tokens and 512 choices.  The result is bfloat16 unless
+    Two launches for up to 4 tokens.  The result is bfloat16 unless
     ``dtype`` or ``out`` says float32."""
     if stream is not None:
         with _on(stream, x):

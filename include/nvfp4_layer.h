@@ -94,11 +94,12 @@ int nvfp4_sequence_add_mx_grouped_gemm_fused(nvfp4_sequence_t seq, const void* a
  * with q() the rounding of nvfp4_mx_quantize; sums in fp32, out rounded once
  * (zeros for a token without a kept choice).
  *
- * Up to 64 tokens and 512 choices the layer runs in two launches, bound by
- * reading the chosen experts' weights once.  Above that it is nvfp4_moe_sort,
- * nvfp4_mx_quantize, nvfp4_mx_grouped_gemm_fused, and the same two again with
- * nvfp4_moe_combine behind them, in one call; each choice's result is then also
- * rounded to the output's type before the sum.  Deterministic either way. */
+ * For few tokens (up to 4, with rows that fit a workgroup's LDS when they are
+ * quantised) the layer runs in two launches, bound by reading the chosen
+ * experts' weights once.  Above that it is nvfp4_moe_sort, nvfp4_mx_quantize,
+ * nvfp4_mx_grouped_gemm_fused, and the same two again with nvfp4_moe_combine
+ * behind them, in one call; each choice's result is then also rounded to the
+ * output's type before the sum.  Deterministic either way. */
 typedef struct nvfp4_mx_experts {
     int64_t experts;         /* 1 to 2048 */
     int64_t hidden, inner;   /* row lengths of x and out, and of h: multiples of 32 */

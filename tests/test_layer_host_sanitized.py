@@ -17,11 +17,13 @@ LAYER_STUBS = r"""
 namespace nvfp4 {
 hipError_t launch_mx_fused(const MxGemmArgs&, const MxEpilogueArgs&, hipStream_t) { return hipErrorInvalidValue; }
 hipError_t launch_mx_gated(const MxGemmArgs&, const MxEpilogueArgs&, hipStream_t) { return hipErrorInvalidValue; }
+hipError_t launch_mx_short(const MxGemmArgs&, const MxEpilogueArgs&, hipStream_t) { return hipErrorInvalidValue; }
 bool mx_fused_fits(const MxGemmArgs&) { return true; }
 bool mx_gated_fits(const MxGemmArgs&) { return true; }
 hipError_t launch_norm(const NormArgs&, hipStream_t) { return hipErrorInvalidValue; }
 hipError_t launch_norm_grad(const NormArgs&, hipStream_t) { return hipErrorInvalidValue; }
 hipError_t launch_mx_moe_few(const MxMoeArgs&, hipStream_t) { return hipErrorInvalidValue; }
+bool mx_moe_few(int64_t tokens, int64_t, int64_t, int64_t) { return tokens <= 4; }
 int norm_grad_parts(bool, int64_t, int) { return 3; }
 }
 """
