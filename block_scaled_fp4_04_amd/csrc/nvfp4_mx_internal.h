@@ -149,6 +149,10 @@ struct NormArgs {
 };
 hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
 hipError_t launch_norm_grad(const NormArgs& a, hipStream_t stream);
+hipError_t launch_norm_bf16(const NormArgs& a, hipStream_t stream);
+hipError_t launch_norm_f32(const NormArgs& a, hipStream_t stream);
+hipError_t launch_norm_grad_bf16(const NormArgs& a, hipStream_t stream);  // without the last step
+hipError_t launch_norm_grad_f32(const NormArgs& a, hipStream_t stream);
 // Workgroups that launch_norm_grad runs on rows x hidden.
 int norm_grad_parts(bool bf16, int64_t rows, int hidden);
 
