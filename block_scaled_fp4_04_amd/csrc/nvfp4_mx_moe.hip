@@ -194,12 +194,12 @@ __global__ void __launch_bounds__(kUpWaves * 64) moe_up_few_kernel(MxMoeArgs a) 
             if (at >= 0 && (!GATED || kg < 2)) {
                 const int col = unit * COLS + 4 * kg;
                 const int64_t b = (int64_t)e * a.inner + col;
-                mx_f4 z = sum_of(lane);
-                const mx_f4 bias = mx_row4(a.up_bias, a.bias_bf16, b, col, a.inner);
-                if constexpr (GATED)
-                    z = mx_act(z + mx_row4(a.gate_bias, a.bias_bf16, b, col, a.inner), a.act) * (sum_of(lane + 32) + bias);
-                else
-                    z = mx_act(z + bias, a.act);
+                mx_f4 z = sum_of(GATED ? lane + 32 : lane) + mx_row4(a.up_bias, a.bias_bf16, b, col, a.inner), gate = z;
+                if constexpr (GATED) gate = sum_of(lane) + mx_row4(a.gate_bias, a.bias_bf16, b, col, a.inner);
+                mx_by_act(a.act, [&](auto ACT) {
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) z[v] = GATED ? mx_act<ACT.value>(gate[v]) * z[v] : mx_act<ACT.value>(z[v]);
+                });
                 mx_put4(a.h, true, (int64_t)at * a.inner + col, col, a.inner, z);
             }
         }

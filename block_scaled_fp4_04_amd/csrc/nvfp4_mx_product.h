@@ -45,13 +45,59 @@ struct MxEpi : MxEpilogueArgs {};
 template <>
 struct MxEpi<EPI_NONE> {};
 
-// The epilogue's columns col .. col + 3 before the residual: from the sums of
-// B and of the gate operand, and the biases.
-template <int EPI>
-__device__ __forceinline__ mx_f4 mx_epilogue(float alpha, int act, mx_f4 up, mx_f4 gate, mx_f4 bias, mx_f4 gate_bias) {
-    mx_f4 z = up * alpha + bias;
-    if constexpr (EPI == EPI_GATED) return mx_act(gate * alpha + gate_bias, act) * z;
-    return mx_act(z, act);
+// A value of the epilogue before the residual: from the sums of B and of the
+// gate operand, and the biases.
+template <int EPI, int ACT>
+__device__ __forceinline__ float mx_epilogue(float alpha, float up, float gate, float bias, float gate_bias) {
+    const float z = up * alpha + bias;
+    if constexpr (EPI == EPI_GATED) return mx_act<ACT>(gate * alpha + gate_bias) * z;
+    return mx_act<ACT>(z);
+}
+
+// Eight values of a row, as they lie in memory: at(.., v) is zero without a row.
+struct MxRow8 {
+    mx_u4 w[2];
+    __device__ __forceinline__ void load(const void* p, bool bf16, int64_t at, int col, int N) {
+        w[0] = w[1] = mx_u4{0, 0, 0, 0};
+        if (!p) return;
+        if (bf16) {
+            const uint16_t* x = static_cast<const uint16_t*>(p) + at;
+            if (col + 8 <= N) {
+                w[0] = *reinterpret_cast<const mx_u4_any*>(x);
+            } else {
+#pragma unroll
+                for (int v = 0; v < 7; ++v)
+                    if (col + v < N) w[0][v >> 1] |= (uint32_t)x[v] << (v & 1) * 16;
+            }
+        } else {
+            typedef unsigned int u4_word __attribute__((ext_vector_type(4), aligned(4)));
+            const uint32_t* x = static_cast<const uint32_t*>(p) + at;
+            if (col + 8 <= N) {
+                w[0] = *reinterpret_cast<const u4_word*>(x);
+                w[1] = *reinterpret_cast<const u4_word*>(x + 4);
+            } else {
+#pragma unroll
+                for (int v = 0; v < 7; ++v)
+                    if (col + v < N) w[v >> 2][v & 3] = x[v];
+            }
+        }
+    }
+    __device__ __forceinline__ float at(bool bf16, int v) const {
+        const uint32_t narrow = w[0][v >> 1], wide = w[v >> 2][v & 3];
+        return bf16 ? mx_widen(narrow, v & 1) : __builtin_bit_cast(float, wide);
+    }
+};
+
+// Stores eight consecutive columns of C, rounded.
+__device__ __forceinline__ void mx_store8(const MxGemmArgs& a, int row, int col, const float (&z)[8]) {
+    const int64_t at = (int64_t)row * a.N + col;
+    if (col + 8 <= a.N && a.out_bf16) {
+        *reinterpret_cast<mx_u4_any*>(static_cast<uint16_t*>(a.out) + at) =
+            mx_u4_any{mx_bf16_pair(z[0], z[1]), mx_bf16_pair(z[2], z[3]), mx_bf16_pair(z[4], z[5]), mx_bf16_pair(z[6], z[7])};
+    } else {
+        mx_put4(a.out, a.out_bf16, at, col, a.N, mx_f4{z[0], z[1], z[2], z[3]});
+        mx_put4(a.out, a.out_bf16, at + 4, col + 4, a.N, mx_f4{z[4], z[5], z[6], z[7]});
+    }
 }
 
 // A: packed, or fp32 / bfloat16 rows.
@@ -232,9 +278,15 @@ __global__ void __launch_bounds__(1024) mx_skinny_kernel(MxGemmArgs a, MxEpi<EPI
                     gate = sum;
                 } else if (row < r1) {
                     const int64_t at = (GROUPED ? (int64_t)tm * a.N : 0) + col;
-                    const mx_f4 z = mx_epilogue<EPI>(a.alpha, e.act, sum, gate, mx_row4(e.bias, e.bias_bf16, at, col, a.N),
-                                                     mx_row4(e.gate_bias, e.bias_bf16, at, col, a.N));
-                    mx_store4(a, row, col, z + mx_row4(e.residual, a.out_bf16, row * e.ldr + col, col, a.N));
+                    const mx_f4 bias = mx_row4(e.bias, e.bias_bf16, at, col, a.N);
+                    const mx_f4 gate_bias = mx_row4(e.gate_bias, e.bias_bf16, at, col, a.N);
+                    mx_f4 z = mx_row4(e.residual, a.out_bf16, row * e.ldr + col, col, a.N);
+                    mx_by_act(e.act, [&](auto ACT) {
+#pragma unroll
+                        for (int v = 0; v < 4; ++v)
+                            z[v] += mx_epilogue<EPI, ACT.value>(a.alpha, sum[v], gate[v], bias[v], gate_bias[v]);
+                    });
+                    mx_store4(a, row, col, z);
                 }
             }
         }
@@ -288,7 +340,7 @@ __global__ void __launch_bounds__(KS * 256, KS > 1 || BM * BN > 128 * 256 ? KS :
     };
     static_assert(AF % 4 == 0 && BF % 4 == 0 && (NS + 1) * CPW + SPW < 64, "ring");
     constexpr int RING = NS * STAGE + SCALES;
-    static_assert(BM * WN * (ON / WN * 2 + 16) <= RING, "the output is staged in the first ring");
+    static_assert(BM * WN * (BN / WN * 2 + 16) <= RING, "the output is staged in the first ring");
     static_assert((KS - 1) * BM * BN * 4 <= KS * RING, "and partial tiles in all");
     __shared__ __attribute__((aligned(1024))) uint8_t lds_all[KS * RING];
 
@@ -601,86 +653,108 @@ __global__ void __launch_bounds__(KS * 256, KS > 1 || BM * BN > 128 * 256 ? KS :
         __syncthreads();
     }
 
-    // Epilogue.  Block (i, j) of lane l: row 32 i + l % 32, columns 32 j +
-    // 8 (v / 4) + 4 (l / 32) + v % 4; or, gated, 16 j + ... of the gate operand
-    // for v < 8 and of B for those from 8 on.
-    constexpr int PM = BM / WM, PN = ON / WN;  // the wave's part
-    constexpr int VN = GATED ? 8 : 16;         // values of a block in a lane
-    const int row0 = m0 + wm * PM, col0 = n0 + wn * PN;
-    // Calls put(i, column in the part, four values) for everything in acc.
-    auto finish = [&](auto put) {
-        auto column = [&](auto J, auto V) { return J.value * 2 * VN + 8 * V.value + 4 * kgl; };
-        if constexpr (EPI == EPI_NONE) {
-            mx_each<MI>([&](auto I) { mx_each<NI>([&](auto J) { mx_each<VN / 4>([&](auto V) {
-                const mx_f16& x = acc[I.value][J.value];
-                constexpr int v = 4 * V.value;
-                put(I.value, column(J, V), a.alpha * mx_f4{x[v], x[v + 1], x[v + 2], x[v + 3]});
-            }); }); });
-        } else {  // (a column's biases serve all its rows)
-            mx_each<NI>([&](auto J) { mx_each<VN / 4>([&](auto V) {
-                const int pc = column(J, V), col = col0 + pc;
-                const int64_t at = (int64_t)group * a.N + col;
-                const mx_f4 bias = mx_row4(e.bias, e.bias_bf16, at, col, a.N);
-                mx_f4 gate_bias = bias;
-                if constexpr (GATED) gate_bias = mx_row4(e.gate_bias, e.bias_bf16, at, col, a.N);
-                mx_each<MI>([&](auto I) {
-                    const mx_f16& x = acc[I.value][J.value];
-                    constexpr int v = 4 * V.value, u = GATED ? v + 8 : v;
-                    put(I.value, pc, mx_epilogue<EPI>(a.alpha, e.act, mx_f4{x[u], x[u + 1], x[u + 2], x[u + 3]},
-                                                      mx_f4{x[v], x[v + 1], x[v + 2], x[v + 3]}, bias, gate_bias));
-                });
-            }); });
-        }
-    };
-    if (a.out_bf16) {
-        // through LDS, a wave's part each, so that whole lines are stored (and
-        // read: the residual goes the same way, and the lane that holds an
-        // element adds its residual where it lies before it is rounded)
-        constexpr int ROW = PN * 2 + 16;  // bytes, 16 of them padding
-        constexpr int LPR = PN / 8;        // lanes that store a row's part
-        constexpr int RPS = 64 / LPR;      // rows a store covers
-        uint8_t* part = lds_all + wave * PM * ROW;
-        const int r = lane / LPR, col = col0 + (lane % LPR) * 8;
-        if (KS == 1 || team == 0) {
-            bool add = false;
-            if constexpr (EPI != EPI_NONE) {
-                add = e.residual != nullptr;
-                if (add) {
-#pragma unroll 4
-                    for (int k = 0; k < PM; k += RPS) {
-                        const int row = row0 + k + r;
-                        mx_u4 o = {0, 0, 0, 0};
-                        if (row < row_end && col < a.N) {
-                            const uint16_t* d = static_cast<const uint16_t*>(e.residual) + row * e.ldr + col;
-                            if (col + 8 <= a.N) {
-                                o = *reinterpret_cast<const mx_u4_any*>(d);
-                            } else {
+    // Block (i, j) of lane l: row 32 i + l % 32, columns 32 j + 8 (v / 4) +
+    // 4 (l / 32) + v % 4.
+    constexpr int PM = BM / WM;  // the wave's rows
+    const int row0 = m0 + wm * PM;
+    if constexpr (EPI != EPI_NONE) {
+        // Through LDS in fp32, as many rows of the wave's part at a time as
+        // fit; from there a lane takes eight columns of a row after row, so that
+        // its biases stay in registers, rows of the residual and of C are read
+        // and written whole, and the code is a short loop.  (With the epilogue
+        // written out for every accumulator 16384 x 4096 x 8192 took 326 us
+        // without a part and 403 with all, against 252 of the plain product.)
+        constexpr int PW = BN / WN, PO = ON / WN;  // columns of the wave: of the operands, of C
+        constexpr int ROW = PW * 4 + 16;           // bytes, 16 of them padding
+        constexpr auto rows_that_fit = [](int pm) {
+            while (4 * pm * ROW > KS * RING) pm /= 2;
+            return pm;
+        };
+        constexpr int PR = rows_that_fit(PM);
+        static_assert(PR % 32 == 0, "whole blocks at a time");
+        constexpr int LPR = PO / 8, RPS = 64 / LPR;  // lanes to a row, rows at a time
+        constexpr int BATCH = PR / RPS < 8 ? PR / RPS : 8;
+        if (KS > 1 && team > 0) return;
+        uint8_t* const part = lds_all + wave * PR * ROW;
+        const int r = lane / LPR, oc = lane % LPR * 8, col = n0 + wn * PO + oc;
+        const int at = GATED ? oc / 16 * 32 + oc % 16 : oc;  // of the columns in a row of LDS
+        float bias[8], gate_bias[8];
 #pragma unroll
-                                for (int v = 0; v < 7; ++v)
-                                    if (col + v < a.N) o[v >> 1] |= (uint32_t)d[v] << (v & 1) * 16;
+        for (int h = 0; h < 8; h += 4) {
+            const int64_t b = (int64_t)group * a.N + col + h;
+            const mx_f4 x = mx_row4(e.bias, e.bias_bf16, b, col + h, a.N), y = mx_row4(e.gate_bias, e.bias_bf16, b, col + h, a.N);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                bias[h + v] = x[v];
+                gate_bias[h + v] = y[v];
+            }
+        }
+        auto rows = [&](auto ACT) {
+            mx_each<PM / PR>([&](auto PASS) {
+                if constexpr (PASS.value > 0) mx_wave_fence();  // the rows before are read
+                mx_each<PR / 32>([&](auto I) { mx_each<NI>([&](auto J) { mx_each<4>([&](auto V) {
+                    const mx_f16& x = acc[PASS.value * (PR / 32) + I.value][J.value];
+                    constexpr int v = 4 * V.value;
+                    *reinterpret_cast<mx_f4*>(part + (I.value * 32 + q32) * ROW + (J.value * 32 + 2 * v + 4 * kgl) * 4) =
+                        mx_f4{x[v], x[v + 1], x[v + 2], x[v + 3]};
+                }); }); });
+                mx_wave_fence();
+#pragma unroll 1
+                for (int k0 = 0; k0 < PR; k0 += RPS * BATCH) {
+                    MxRow8 res[BATCH];
+#pragma unroll
+                    for (int k = 0; k < BATCH; ++k) {
+                        const int row = min(row0 + PASS.value * PR + k0 + k * RPS + r, row_end - 1);
+                        res[k].load(e.residual, a.out_bf16, row * e.ldr + col, col, a.N);
+                    }
+#pragma unroll
+                    for (int k = 0; k < BATCH; ++k) {
+                        const int in = k0 + k * RPS + r, row = row0 + PASS.value * PR + in;
+                        const float* const p = reinterpret_cast<const float*>(part + in * ROW) + at;
+                        float z[8];
+#pragma unroll
+                        for (int h = 0; h < 8; h += 4) {
+                            const mx_f4 up = *reinterpret_cast<const mx_f4*>(p + h + (GATED ? 16 : 0));
+                            mx_f4 gate = up;
+                            if constexpr (GATED) gate = *reinterpret_cast<const mx_f4*>(p + h);
+#pragma unroll
+                            for (int v = 0; v < 4; ++v) {
+                                z[h + v] = mx_epilogue<EPI, ACT.value>(a.alpha, up[v], gate[v], bias[h + v], gate_bias[h + v]);
+                                if (e.residual) z[h + v] += res[k].at(a.out_bf16, h + v);
                             }
                         }
-                        __builtin_memcpy(__builtin_assume_aligned(part + (k + r) * ROW + (lane % LPR) * 16, 16), &o, 16);
+                        if (row < row_end) mx_store8(a, row, col, z);
                     }
-                    mx_wave_fence();
                 }
-            }
-            finish([&](int i, int pc, mx_f4 f) {
-                uint8_t* d = part + (i * 32 + q32) * ROW + pc * 2;
-                uint32_t o[2];
-                if (EPI != EPI_NONE && add) {
-                    __builtin_memcpy(o, __builtin_assume_aligned(d, 8), 8);
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) f[v] += mx_widen(o[v >> 1], v & 1);
-                }
-                o[0] = mx_bf16_pair(f[0], f[1]);
-                o[1] = mx_bf16_pair(f[2], f[3]);
-                __builtin_memcpy(__builtin_assume_aligned(d, 8), o, 8);
             });
+        };
+        mx_by_act(e.act, rows);
+        return;
+    }
+    constexpr int PN = BN / WN;  // the wave's columns
+    const int col0 = n0 + wn * PN;
+    if (a.out_bf16) {
+        // through LDS, a wave's part each, so that whole lines are stored
+        constexpr int ROW = PN * 2 + 16;  // bytes, 16 of them padding
+        uint8_t* part = lds_all + wave * PM * ROW;
+        if (KS == 1 || team == 0) {
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int j = 0; j < NI; ++j)
+#pragma unroll
+                    for (int v = 0; v < 16; v += 4) {
+                        const uint32_t o[2] = {mx_bf16_pair(a.alpha * acc[i][j][v], a.alpha * acc[i][j][v + 1]),
+                                               mx_bf16_pair(a.alpha * acc[i][j][v + 2], a.alpha * acc[i][j][v + 3])};
+                        __builtin_memcpy(__builtin_assume_aligned(part + (i * 32 + q32) * ROW + (j * 32 + 2 * v + 4 * kgl) * 2, 8), o, 8);
+                    }
         }
         __syncthreads();
         if (KS > 1 && team > 0) return;
         const bool stream_out = 2 * (int64_t)a.M * a.N > kStreamBytes;  // (28672 x 8192 x 2048: 309 -> 308 us)
+        constexpr int LPR = PN / 8;        // lanes that store a row's part
+        constexpr int RPS = 64 / LPR;      // rows a store covers
+        const int r = lane / LPR, col = col0 + (lane % LPR) * 8;
 #pragma unroll 4
         for (int k = 0; k < PM; k += RPS) {
             const int row = row0 + k + r;
@@ -699,12 +773,17 @@ __global__ void __launch_bounds__(KS * 256, KS > 1 || BM * BN > 128 * 256 ? KS :
             }
         }
     } else if (KS == 1 || team == 0) {
-        finish([&](int i, int pc, mx_f4 f) {
-            const int row = row0 + i * 32 + q32, col = col0 + pc;
-            if (row >= row_end) return;
-            if constexpr (EPI != EPI_NONE) f += mx_row4(e.residual, false, row * e.ldr + col, col, a.N);
-            mx_store4(a, row, col, f);
-        });
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            const int row = row0 + i * 32 + q32;
+#pragma unroll
+            for (int j = 0; j < NI; ++j)
+#pragma unroll
+                for (int v = 0; v < 16; v += 4) {
+                    const mx_f4 f = {acc[i][j][v], acc[i][j][v + 1], acc[i][j][v + 2], acc[i][j][v + 3]};
+                    if (row < row_end) mx_store4(a, row, col0 + j * 32 + 2 * v + 4 * kgl, f * a.alpha);
+                }
+        }
     }
 }
 
