@@ -197,28 +197,46 @@ int prepare_mx_moe(const nvfp4_mx_experts* l, const void* x, int x_type, int64_t
     const nvfp4_mx_epilogue up = {l->activation, l->gate_packed, l->gate_scales, l->up_bias,
                                   l->gate_bias, l->bias_type, nullptr, 0};
     const nvfp4_mx_epilogue down = {NVFP4_ACT_NONE, nullptr, nullptr, l->down_bias, nullptr, l->bias_type, nullptr, 0};
-    // (rows of h and y behind the last kept choice hold anything: they are read,
-    // but nothing that is used comes of them)
-    st = prepare_moe_sort(ids, id_type, tokens, topk, l->experts, offsets, slots, row_tokens, &jobs[0]);
+    // (rows of h and y behind the last kept choice hold anything: they may be
+    // read, but nothing that is used comes of them)
+    Job sort, quantize;
+    st = prepare_moe_sort(ids, id_type, tokens, topk, l->experts, offsets, slots, row_tokens, &sort);
     if (st == NVFP4_OK)
-        st = prepare_mx_quantize(false, x, x_type, 1, 0, tokens, l->hidden, ldx, w + at.x_codes, w + at.x_scales, &jobs[1]);
-    if (st == NVFP4_OK)
-        st = prepare_grouped_fused(w + at.x_codes, w + at.x_scales, tokens, row_tokens, l->up_packed, l->up_scales,
-                                   offsets, l->experts, 1.0f, &up, w + at.h, NVFP4_TYPE_BF16, pairs, l->inner,
-                                   l->hidden, &jobs[2]);
-    if (st == NVFP4_OK)
+        st = prepare_mx_quantize(false, x, x_type, 1, 0, tokens, l->hidden, ldx, w + at.x_codes, w + at.x_scales, &quantize);
+    if (st != NVFP4_OK) return st;
+    Job* next = jobs;
+    if (pairs <= kMoeRouteChoices) {
+        *next = sort;
+        next->mx_quant = quantize.mx_quant;
+        next->launch = +[](const Job& j, hipStream_t s) { return launch_moe_route(j.moe, j.mx_quant, s); };
+        ++next;
+    } else {
+        *next++ = sort;
+        *next++ = quantize;
+    }
+    st = prepare_grouped_fused(w + at.x_codes, w + at.x_scales, tokens, row_tokens, l->up_packed, l->up_scales, offsets,
+                               l->experts, 1.0f, &up, w + at.h, NVFP4_TYPE_BF16, pairs, l->inner, l->hidden, next);
+    if (st != NVFP4_OK) return st;
+    const bool packs = l->gate_packed ? mx_gated_packs(next->mx_gemm) : mx_fused_packs(next->mx_gemm);
+    if (packs) {
+        next->epilogue.q_codes = w + at.h_codes;
+        next->epilogue.q_scales = w + at.h_scales;
+    }
+    ++next;
+    if (!packs) {
         st = prepare_mx_quantize(false, w + at.h, NVFP4_TYPE_BF16, 1, 0, pairs, l->inner, l->inner, w + at.h_codes,
-                                 w + at.h_scales, &jobs[3]);
-    if (st == NVFP4_OK)
-        st = prepare_grouped_fused(w + at.h_codes, w + at.h_scales, pairs, nullptr, l->down_packed, l->down_scales,
-                                   offsets, l->experts, 1.0f, &down, w + at.y, out_type, pairs, l->hidden, l->inner,
-                                   &jobs[4]);
+                                 w + at.h_scales, next++);
+        if (st != NVFP4_OK) return st;
+    }
+    st = prepare_grouped_fused(w + at.h_codes, w + at.h_scales, pairs, nullptr, l->down_packed, l->down_scales, offsets,
+                               l->experts, 1.0f, &down, w + at.y, out_type, pairs, l->hidden, l->inner, next);
+    if (st != NVFP4_OK) return st;
     // (up to about a tile of rows to an expert; the kernel is right for more)
-    if (st == NVFP4_OK && mx_steps(l->inner) <= 4 && pairs <= 16 * l->experts)
-        jobs[4].launch = +[](const Job& j, hipStream_t s) { return launch_mx_short(j.mx_gemm, j.epilogue, s); };
-    if (st == NVFP4_OK)
-        st = prepare_moe_combine(w + at.y, out_type, tokens, topk, l->hidden, slots, weights, out, &jobs[5]);
-    if (st == NVFP4_OK) *count = kMoeJobs;
+    if (mx_steps(l->inner) <= 4 && pairs <= 16 * l->experts)
+        next->launch = +[](const Job& j, hipStream_t s) { return launch_mx_short(j.mx_gemm, j.epilogue, s); };
+    ++next;
+    st = prepare_moe_combine(w + at.y, out_type, tokens, topk, l->hidden, slots, weights, out, next++);
+    if (st == NVFP4_OK) *count = (int)(next - jobs);
     return st;
 }
 

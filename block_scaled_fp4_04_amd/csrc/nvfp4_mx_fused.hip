@@ -16,4 +16,10 @@ bool mx_fused_fits(const MxGemmArgs& a) {
     return l.items < ((int64_t)1 << 32);
 }
 
+bool mx_fused_packs(const MxGemmArgs& a) {
+    Launch<EPI_ONE> l{a, {}, nullptr, true, 0, hipSuccess};
+    choose(l);
+    return l.packs;
+}
+
 }  // namespace nvfp4

@@ -16,4 +16,10 @@ bool mx_gated_fits(const MxGemmArgs& a) {
     return l.items < ((int64_t)1 << 32);
 }
 
+bool mx_gated_packs(const MxGemmArgs& a) {
+    Launch<EPI_GATED> l{a, {}, nullptr, true, 0, hipSuccess};
+    choose(l);
+    return l.packs;
+}
+
 }  // namespace nvfp4

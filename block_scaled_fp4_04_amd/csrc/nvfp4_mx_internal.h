@@ -84,6 +84,7 @@ struct MxEpilogueArgs {
     const void* gate_bias;
     const void* residual;        // M x N of the output's type, row stride ldr, or null
     int64_t ldr;
+    uint8_t *q_codes, *q_scales; // C as a packed operand instead of out, or null (mx_packs)
     int act;                     // kMxAct*
     bool bias_bf16;
 };
@@ -100,6 +101,9 @@ hipError_t launch_mx_gated(const MxGemmArgs& a, const MxEpilogueArgs& e, hipStre
 hipError_t launch_mx_short(const MxGemmArgs& a, const MxEpilogueArgs& e, hipStream_t stream);
 bool mx_fused_fits(const MxGemmArgs& a);
 bool mx_gated_fits(const MxGemmArgs& a);
+// Whether the kernel that the sizes choose writes C packed.
+bool mx_fused_packs(const MxGemmArgs& a);
+bool mx_gated_packs(const MxGemmArgs& a);
 
 // Expert routing.
 constexpr int kMoeMaxExperts = 2048;
@@ -179,5 +183,8 @@ struct MxMoeArgs {
 // Whether it takes a layer of these sizes.
 bool mx_moe_few(int64_t tokens, int64_t topk, int64_t hidden, int64_t inner);
 hipError_t launch_mx_moe_few(const MxMoeArgs& a, hipStream_t stream);
+// Few choices sorted (as launch_moe_sort) and x quantised (as launch_mx_quantize) in one launch.
+constexpr int kMoeRouteChoices = 256;
+hipError_t launch_moe_route(const MoeArgs& s, const MxQuantArgs& q, hipStream_t stream);
 
 }  // namespace nvfp4

@@ -88,6 +88,24 @@ struct MxRow8 {
     }
 };
 
+// Rounds eight consecutive columns to bfloat16 and stores them as a quarter of a
+// block of the packed row, whose four lanes, side by side, call this together.
+__device__ __forceinline__ void mx_pack8(const MxEpilogueArgs& e, int row, int col, int N, bool live, const float (&z)[8]) {
+    const mx_u4 v = {mx_bf16_pair(z[0], z[1]), mx_bf16_pair(z[2], z[3]), mx_bf16_pair(z[4], z[5]), mx_bf16_pair(z[6], z[7])};
+    const uint32_t byte = mx_scale_byte(mx_block_top<4>(mx_top<uint16_t>(v)));
+    const uint32_t q = byte == 255u ? 0u : mx_codes<uint16_t, 0>(0, v, mx_scale(byte));
+    if (!live) return;
+    const int C = (N + kMxStep - 1) / kMxStep, Q = (C + 3) / 4, c = col / kMxStep, b = col % kMxStep / kMxBlock;
+    *reinterpret_cast<uint32_t*>(e.q_codes + ((int64_t)(row >> 4) * C + c) * kMxFrag + mx_code_at(row & 15, b) + col % kMxBlock / 2) = q;
+    if (col % kMxBlock == 0) e.q_scales[((int64_t)(row >> 4) * Q + c / 4) * kMxScaleFrag + mx_scale_at(row & 15, b) + (c & 3)] = (uint8_t)byte;
+}
+// Zeros in block `block` of the packed row, behind its last column.
+__device__ __forceinline__ void mx_pack_zeros(const MxEpilogueArgs& e, int row, int block, int N) {
+    const int C = (N + kMxStep - 1) / kMxStep, Q = (C + 3) / 4, c = block >> 2, b = block & 3;
+    if (c < C) *reinterpret_cast<mx_u4*>(e.q_codes + ((int64_t)(row >> 4) * C + c) * kMxFrag + mx_code_at(row & 15, b)) = mx_u4{0, 0, 0, 0};
+    e.q_scales[((int64_t)(row >> 4) * Q + c / 4) * kMxScaleFrag + mx_scale_at(row & 15, b) + (c & 3)] = 0;
+}
+
 // Stores eight consecutive columns of C, rounded.
 __device__ __forceinline__ void mx_store8(const MxGemmArgs& a, int row, int col, const float (&z)[8]) {
     const int64_t at = (int64_t)row * a.N + col;
@@ -723,12 +741,24 @@ __global__ void __launch_bounds__(KS * 256, KS > 1 || BM * BN > 128 * 256 ? KS :
                                 if (e.residual) z[h + v] += res[k].at(a.out_bf16, h + v);
                             }
                         }
+                        if constexpr (PO % 32 == 0) {
+                            if (e.q_codes) {  // (N is a multiple of 32: a block's four lanes are all inside or none)
+                                mx_pack8(e, row, col, a.N, row < row_end && col < a.N, z);
+                                continue;
+                            }
+                        }
                         if (row < row_end) mx_store8(a, row, col, z);
                     }
                 }
             });
         };
         mx_by_act(e.act, rows);
+        // packed rows are filled up to whole steps and scale words
+        if (e.q_codes && tn == tiles_n - 1 && wn == 0) {
+            const int Qn = (a.N + 4 * kMxStep - 1) / (4 * kMxStep), more = Qn * 16 - a.N / kMxBlock;
+            for (int k = lane; k < PM * more; k += 64)
+                if (row0 + k / more < row_end) mx_pack_zeros(e, row0 + k / more, a.N / kMxBlock + k % more, a.N);
+        }
         return;
     }
     constexpr int PN = BN / WN;  // the wave's columns
@@ -801,6 +831,7 @@ struct Launch {
     bool dry;
     int64_t items;
     hipError_t error;
+    bool packs = false;  // whether the kernel can write C packed
 };
 
 template <int MI, int AT, bool GROUPED, bool NT = false, int EPI>
@@ -824,6 +855,7 @@ void run_tile(Launch<EPI>& l) {
     // x 6144 took 24.2 us, now 13.1; and many groups were refused)
     const int64_t tiles_m = ((int64_t)a.M + BM - 1) / BM + (GROUPED ? std::min(a.groups, a.M) : 0), tiles_n = ((int64_t)a.N * l.kWeights + BN - 1) / BN;
     l.items = tiles_m * tiles_n * KS * 256;
+    l.packs = BN * WM / 4 / l.kWeights % 32 == 0;  // (a wave has whole blocks of its columns)
     if (l.dry) return;
     hipLaunchKernelGGL((mx_tile_kernel<BM, BN, NS, WM, KS, GROUPED, EPI>), dim3((unsigned)(tiles_m * tiles_n)), dim3(KS * 256), 0,
                        l.stream, a, (int)tiles_m, (int)tiles_n, l.e);

@@ -18,6 +18,9 @@ namespace nvfp4 {
 hipError_t launch_mx_fused(const MxGemmArgs&, const MxEpilogueArgs&, hipStream_t) { return hipErrorInvalidValue; }
 hipError_t launch_mx_gated(const MxGemmArgs&, const MxEpilogueArgs&, hipStream_t) { return hipErrorInvalidValue; }
 hipError_t launch_mx_short(const MxGemmArgs&, const MxEpilogueArgs&, hipStream_t) { return hipErrorInvalidValue; }
+bool mx_fused_packs(const MxGemmArgs&) { return true; }
+bool mx_gated_packs(const MxGemmArgs&) { return false; }
+hipError_t launch_moe_route(const MoeArgs&, const MxQuantArgs&, hipStream_t) { return hipErrorInvalidValue; }
 bool mx_fused_fits(const MxGemmArgs&) { return true; }
 bool mx_gated_fits(const MxGemmArgs&) { return true; }
 hipError_t launch_norm(const NormArgs&, hipStream_t) { return hipErrorInvalidValue; }
