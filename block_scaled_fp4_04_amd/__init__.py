@@ -690,7 +690,7 @@ class Sequence:
         from . import layer, mx
         if epilogue is None:
             return self._record(getattr(mx.mx_lib(), "nvfp4_sequence_add_" + name), args, tensors, keep)
-        args, more = epilogue._marshal(b, out, args)
+        args, more = epilogue._marshal(b, out, args, layer._EPILOGUE_AT["nvfp4_" + name])
         # (the tensors themselves: the fields of an epilogue can be set again)
         self._record(getattr(layer.layer_lib(), f"nvfp4_sequence_add_{name}_fused"), args, tensors + more,
                      keep + list(more))

@@ -109,7 +109,7 @@ struct MoeSpace {
         return at;
     }
     size_t h = 0, offsets = 0, slots = 0, row_tokens = 0, x_codes = 0, x_scales = 0, h_codes = 0, h_scales = 0, y = 0;
-    MoeSpace(const nvfp4_mx_experts& l, int64_t tokens, int64_t topk, int out_type) {
+    MoeSpace(const nvfp4_mx_experts& l, int64_t tokens, int64_t topk) {
         const int64_t pairs = tokens * topk;
         if (pairs == 0) return;
         h = take(pairs * l.inner, 2);
@@ -124,7 +124,7 @@ struct MoeSpace {
         offsets = take(l.experts + 1, 4);
         slots = take(pairs, 4);
         row_tokens = take(pairs, 4);
-        y = take(pairs * l.hidden, size_of(out_type));
+        y = take(pairs * l.hidden, 4);
     }
 };
 
@@ -144,7 +144,7 @@ int prepare_mx_moe(const nvfp4_mx_experts* l, const void* x, int x_type, int64_t
     const int64_t per16 = x_type == NVFP4_TYPE_BF16 ? 8 : 4;
     if (tokens <= 1) ldx = l->hidden;
     if (ldx < l->hidden || ldx > kMaxDim || ldx % per16) return NVFP4_ERR_INVALID_VALUE;
-    const MoeSpace at(*l, tokens, topk, out_type);
+    const MoeSpace at(*l, tokens, topk);
     if (tokens > 0 && (!x || !ids || !out || !workspace || workspace_bytes < at.bytes)) return NVFP4_ERR_INVALID_VALUE;
     const uintptr_t bias_size = size_of(l->bias_type);
     const void* const whole[] = {x, out, workspace, l->gate_packed, l->gate_scales, l->up_packed,
@@ -229,15 +229,19 @@ int prepare_mx_moe(const nvfp4_mx_experts* l, const void* x, int x_type, int64_t
         if (st != NVFP4_OK) return st;
     }
     st = prepare_grouped_fused(w + at.h_codes, w + at.h_scales, pairs, nullptr, l->down_packed, l->down_scales, offsets,
-                               l->experts, 1.0f, &down, w + at.y, out_type, pairs, l->hidden, l->inner, next);
+                               l->experts, 1.0f, &down, w + at.y, NVFP4_TYPE_F32, pairs, l->hidden, l->inner, next);
     if (st != NVFP4_OK) return st;
     // (up to about a tile of rows to an expert; the kernel is right for more)
     if (mx_steps(l->inner) <= 4 && pairs <= 16 * l->experts)
         next->launch = +[](const Job& j, hipStream_t s) { return launch_mx_short(j.mx_gemm, j.epilogue, s); };
     ++next;
-    st = prepare_moe_combine(w + at.y, out_type, tokens, topk, l->hidden, slots, weights, out, next++);
-    if (st == NVFP4_OK) *count = (int)(next - jobs);
-    return st;
+    st = prepare_moe_combine(w + at.y, NVFP4_TYPE_F32, tokens, topk, l->hidden, slots, weights, out, next);
+    if (st != NVFP4_OK) return st;
+    if (out_type == NVFP4_TYPE_BF16)
+        next->launch = +[](const Job& j, hipStream_t s) { return launch_moe_combine_narrow(j.moe, s); };
+    ++next;
+    *count = (int)(next - jobs);
+    return NVFP4_OK;
 }
 
 // ---- norms ----------------------------------------------------------------------
@@ -321,7 +325,7 @@ int nvfp4_mx_moe_workspace(const nvfp4_mx_experts* layer, int64_t tokens, int64_
                            int out_type, size_t* bytes) {
     const int st = check_experts(layer, tokens, topk, out_type);
     if (st != NVFP4_OK || !bytes) return st != NVFP4_OK ? st : NVFP4_ERR_INVALID_VALUE;
-    *bytes = MoeSpace(*layer, tokens, topk, out_type).bytes;
+    *bytes = MoeSpace(*layer, tokens, topk).bytes;
     return NVFP4_OK;
 }
 
@@ -450,6 +454,28 @@ int nvfp4_mx_grouped_gemm_fused(const void* a_packed, const void* a_scales, int6
                                          row_offsets, groups, alpha, epilogue, out, out_type, M, N,
                                          K, &job);
     return run(st, job, stream);
+}
+
+int nvfp4_mx_linear_fused(const void* x, int x_type, int64_t ldx, const void* b_packed,
+                          const void* b_scales, float alpha, const nvfp4_mx_epilogue* epilogue,
+                          void* out, int out_type, int64_t M, int64_t N, int64_t K,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+    // (one launch: 16 x 65536 x 8192 52 us, 57 + 2.7 in two.  Behind K = 8192 every
+    // 16 columns quantise the rows again, about N K (6 + M) / 2e8 us)
+    if (M <= kMxQuantRows && (K <= 8192 || (double)N * K * (6 + M) <= 8e8))
+        return nvfp4_mx_gemm_quantized_fused(x, x_type, ldx, b_packed, b_scales, alpha, epilogue, out, out_type,
+                                             M, N, K, stream);
+    size_t codes = 0, scales = 0;
+    int st = nvfp4_mx_packed_size(M, K, &codes, &scales);
+    if (st != NVFP4_OK) return st;
+    if (!workspace || workspace_bytes < codes + scales) return NVFP4_ERR_INVALID_VALUE;
+    uint8_t* const w = static_cast<uint8_t*>(workspace);
+    Job quantize, product;
+    st = prepare_mx_quantize(false, x, x_type, 1, 0, M, K, ldx, w, w + codes, &quantize);
+    if (st == NVFP4_OK)
+        st = prepare_gemm_fused(w, w + codes, b_packed, b_scales, alpha, epilogue, out, out_type, M, N, K, &product);
+    if (st == NVFP4_OK) st = run_job(quantize, stream);
+    return run(st, product, stream);
 }
 
 int nvfp4_sequence_add_mx_gemm_fused(nvfp4_sequence_t seq, const void* a_packed,

@@ -259,7 +259,9 @@ __global__ void __launch_bounds__(256) moe_gather_kernel(MoeArgs a) {
 
 // out[t] = sum_j w[t][j] * x[slot(t, j)], in fp32 and in the order of j.  B
 // rows are read at a time (row 0 in the place of a dropped choice's, unused).
-template <typename T, int V, int B, bool NT>
+// O: the type of the result, T but for fp32 rows that a layer of experts adds
+// up to bfloat16.
+template <typename T, typename O, int V, int B, bool NT>
 __global__ void __launch_bounds__(256) moe_combine_kernel(MoeArgs a) {
     const int64_t t = blockIdx.x;
     int64_t col = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * V;
@@ -280,10 +282,10 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(MoeArgs a) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) sum[i] += c.weight[b] * widen(r[b].v[i]);
     }
-    Piece<T, V> o;
+    Piece<O, V> o;
 #pragma unroll
     for (int i = 0; i < V; ++i) narrow(sum[i], o.v[i]);
-    if (in) store_piece<NT, T, V>(static_cast<T*>(a.out) + t * a.hidden + col, o);
+    if (in) store_piece<NT, O, V>(static_cast<O*>(a.out) + t * a.hidden + col, o);
 }
 
 // dy[slot(t, j)] = w[t][j] * dout[t];  dw[t][j] = <dout[t], y[slot(t, j)]>.
@@ -349,7 +351,7 @@ __global__ void __launch_bounds__(256) moe_combine_grad_kernel(MoeArgs a) {
     }
 }
 
-enum RowKernel { GATHER, COMBINE, COMBINE_GRAD };
+enum RowKernel { GATHER, COMBINE, COMBINE_NARROW, COMBINE_GRAD };
 
 template <RowKernel K, typename T, int V, int B, bool NT>
 hipError_t run_rows(const MoeArgs& a, hipStream_t stream) {
@@ -361,7 +363,9 @@ hipError_t run_rows(const MoeArgs& a, hipStream_t stream) {
     if constexpr (K == GATHER)
         hipLaunchKernelGGL((moe_gather_kernel<T, V, B, NT>), grid, dim3(threads), 0, stream, a);
     else if constexpr (K == COMBINE)
-        hipLaunchKernelGGL((moe_combine_kernel<T, V, B, NT>), grid, dim3(threads), 0, stream, a);
+        hipLaunchKernelGGL((moe_combine_kernel<T, T, V, B, NT>), grid, dim3(threads), 0, stream, a);
+    else if constexpr (K == COMBINE_NARROW)
+        hipLaunchKernelGGL((moe_combine_kernel<T, uint16_t, V, B, NT>), grid, dim3(threads), 0, stream, a);
     else
         hipLaunchKernelGGL((moe_combine_grad_kernel<T, V, B, NT>), grid, dim3(threads), 0, stream, a);
     return hipGetLastError();
@@ -373,6 +377,8 @@ hipError_t run_rows(const MoeArgs& a, hipStream_t stream) {
 // down: the gradient reads the rows again.)
 template <RowKernel K, typename T, int V, int B>
 hipError_t pick_stores(const MoeArgs& a, hipStream_t stream) {
+    // (stores of 8 bytes have no such form)
+    if constexpr (K == COMBINE_NARROW) return run_rows<K, T, V, B, false>(a, stream);
     return a.tokens * a.topk * a.hidden * (int64_t)sizeof(T) > kStreamBytes ? run_rows<K, T, V, B, true>(a, stream)
                                                              : run_rows<K, T, V, B, false>(a, stream);
 }
@@ -425,6 +431,9 @@ hipError_t launch_moe_sort(const MoeArgs& a, hipStream_t stream) {
 }
 hipError_t launch_moe_gather(const MoeArgs& a, hipStream_t stream) { return pick<GATHER>(a, stream); }
 hipError_t launch_moe_combine(const MoeArgs& a, hipStream_t stream) { return pick<COMBINE>(a, stream); }
+hipError_t launch_moe_combine_narrow(const MoeArgs& a, hipStream_t stream) {
+    return pick_batch<COMBINE_NARROW, float, 4>(a, stream);
+}
 hipError_t launch_moe_combine_grad(const MoeArgs& a, hipStream_t stream) { return pick<COMBINE_GRAD>(a, stream); }
 
 }  // namespace nvfp4

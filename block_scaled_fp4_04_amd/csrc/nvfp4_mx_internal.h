@@ -126,6 +126,7 @@ struct MoeArgs {
 hipError_t launch_moe_sort(const MoeArgs& a, hipStream_t stream);
 hipError_t launch_moe_gather(const MoeArgs& a, hipStream_t stream);
 hipError_t launch_moe_combine(const MoeArgs& a, hipStream_t stream);
+hipError_t launch_moe_combine_narrow(const MoeArgs& a, hipStream_t stream);  // fp32 rows to bfloat16, hidden >= 4
 hipError_t launch_moe_combine_grad(const MoeArgs& a, hipStream_t stream);
 
 // Norms around a block's residual (include/nvfp4_layer.h).

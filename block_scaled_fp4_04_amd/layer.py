@@ -30,12 +30,13 @@ from dataclasses import dataclass
 import torch
 
 from . import Nvfp4Error, _i64, _vp, lib
-from .mx import (MX_BLOCK, _GEMM, _GEMM_Q, _GROUPED, _KINDS, MxGroups, MxOperand, _kind, _on, _out, _packed, _rows_2d,
-                 _run, _type_of)
+from .mx import (MX_BLOCK, MX_QUANT_ROWS, _GEMM, _GEMM_Q, _GROUPED, _KINDS, MxGroups, MxOperand, _gemm_quantized_args, _kind, _on, _out,
+                 _packed, _rows_2d, _run, _type_of)
 
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}   # NVFP4_ACT_*
 
-LAYER_EXPORTS = ["nvfp4_mx_gemm_fused", "nvfp4_mx_gemm_quantized_fused", "nvfp4_mx_grouped_gemm_fused",
+LAYER_EXPORTS = ["nvfp4_mx_linear_fused", "nvfp4_mx_gemm_fused", "nvfp4_mx_gemm_quantized_fused",
+                 "nvfp4_mx_grouped_gemm_fused",
                  "nvfp4_sequence_add_mx_gemm_fused", "nvfp4_sequence_add_mx_gemm_quantized_fused",
                  "nvfp4_sequence_add_mx_grouped_gemm_fused", "nvfp4_add_norm", "nvfp4_sequence_add_norm",
                  "nvfp4_add_norm_grad", "nvfp4_add_norm_grad_workspace", "nvfp4_mx_moe", "nvfp4_mx_moe_workspace",
@@ -89,7 +90,8 @@ def layer_lib() -> ctypes.CDLL:
             f, g = getattr(L, "nvfp4_" + name), getattr(L, "nvfp4_sequence_add_" + name)
             f.restype = g.restype = _int
             f.argtypes, g.argtypes = types + [_vp], [_vp] + types
-        for name, types in (("nvfp4_add_norm", _NORM + [_vp]), ("nvfp4_sequence_add_norm", [_vp] + _NORM),
+        for name, types in (("nvfp4_mx_linear_fused", _with_epilogue(_GEMM_Q) + [_vp, _size, _vp]),
+                            ("nvfp4_add_norm", _NORM + [_vp]), ("nvfp4_sequence_add_norm", [_vp] + _NORM),
                             ("nvfp4_add_norm_grad", _NORM_GRAD + [_vp]),
                             ("nvfp4_add_norm_grad_workspace", [_norm_p, ctypes.POINTER(_size)]),
                             ("nvfp4_mx_moe", _MOE + [_vp]), ("nvfp4_sequence_add_mx_moe", [_vp] + _MOE),
@@ -134,34 +136,53 @@ class MxEpilogue:
     gate_bias: "object" = None
     residual: "object" = None
 
-    def _marshal(self, b, out, args: tuple):
+    def _marshal(self, b, out, args: tuple, at: int):
         """(C arguments, tensors) for a product of B = b into out whose
-        arguments without an epilogue are `args`."""
-        shape = (b.rows,) if not hasattr(b, "groups") else (b.groups, b.rows)
-        bias, kind = _bias("bias", self.bias, shape)
-        gate_bias, gate_kind = _bias("gate_bias", self.gate_bias, shape)
-        g, r = self.gate, self.residual
-        if g is None:
-            if gate_bias is not None:
-                raise ValueError("gate_bias needs a gate")
-        else:
-            _kind(g, "gate", type(b))
-            if (g.rows, g.K) != (b.rows, b.K) or getattr(g, "groups", 0) != getattr(b, "groups", 0):
-                raise ValueError("the gate must have the sizes of b")
-            g.check("gate")
+        arguments without an epilogue are `args`, the epilogue's place among them
+        `at`."""
+        groups, g, r = getattr(b, "groups", None), self.gate, self.residual
+        bias = gate_bias = gate_codes = gate_scales = kind = gate_kind = residual = None
+        ld, tensors = 0, (self.bias, self.gate_bias, r)
+        if self.bias is not None or self.gate_bias is not None:
+            shape = (b.rows,) if groups is None else (groups, b.rows)
+            bias, kind = _bias("bias", self.bias, shape)
+            gate_bias, gate_kind = _bias("gate_bias", self.gate_bias, shape)
             if None not in (kind, gate_kind) and kind != gate_kind:
                 raise ValueError("bias and gate_bias must be of one type")
-        if r is not None and (r.shape != out.shape or r.dtype != out.dtype or (r.stride(1) != 1 and r.shape[1] != 1)):
-            raise ValueError(f"residual must be a tensor of shape {tuple(out.shape)} and type {out.dtype} with unit "
-                             "stride along its rows")
-        e = _EpilogueT(_activation(self.activation), None if g is None else g.codes.data_ptr(),
-                       None if g is None else g.scales.data_ptr(), bias, gate_bias,
-                       (gate_kind or 0) if kind is None else kind, None if r is None else r.data_ptr(),
-                       0 if r is None else r.stride(0))
-        tensors = (self.bias, self.gate_bias, r) + (() if g is None else (g.codes, g.scales))
-        # (alpha is the one float among the arguments)
-        at = next(i for i, a in enumerate(args) if type(a) is float) + 1
+        if g is not None:
+            _kind(g, "gate", type(b))
+            if g.rows != b.rows or g.K != b.K or getattr(g, "groups", None) != groups:
+                raise ValueError("the gate must have the sizes of b")
+            g.check("gate")
+            gate_codes, gate_scales = g.codes.data_ptr(), g.scales.data_ptr()
+            tensors += (g.codes, g.scales)
+        elif gate_bias is not None:
+            raise ValueError("gate_bias needs a gate")
+        if r is not None:
+            if r.shape != out.shape or r.dtype is not out.dtype or (r.stride(1) != 1 and r.shape[1] != 1):
+                raise ValueError(f"residual must be a tensor of shape {tuple(out.shape)} and type {out.dtype} with unit "
+                                 "stride along its rows")
+            residual, ld = r.data_ptr(), r.stride(0)
+        e = _EpilogueT(_activation(self.activation), gate_codes, gate_scales, bias, gate_bias,
+                       (gate_kind or 0) if kind is None else kind, residual, ld)
         return args[:at] + (e,) + args[at:], tensors
+
+
+#: The place of an epilogue among the arguments of a product, behind alpha.
+_EPILOGUE_AT = {"nvfp4_mx_gemm": 5, "nvfp4_mx_gemm_quantized": 6, "nvfp4_mx_grouped_gemm": 9}
+
+
+def _linear(x, b, alpha, out, dtype, epilogue):
+    """mx_linear of a 2-D x with an epilogue: one call (nvfp4_mx_linear_fused)."""
+    out, args = _gemm_quantized_args(x, b, alpha, out, dtype)
+    args, more = epilogue._marshal(b, out, args, 6)
+    work, size = None, 0
+    if x.shape[0] > MX_QUANT_ROWS or b.K > 8192:   # (below that the call takes no workspace)
+        size = sum(_packed(x.shape[0], b.K))
+        work = x.new_empty(size, dtype=torch.uint8)
+    _run(layer_lib().nvfp4_mx_linear_fused, args + (None if work is None else work.data_ptr(), size),
+         (x, b.codes, b.scales, out, work) + more)
+    return out
 
 
 # ---- a whole layer of experts --------------------------------------------------

@@ -330,7 +330,7 @@ def _product(name: str, b, out, args: tuple, tensors: tuple, epilogue) -> None:
     if epilogue is None:
         return _run(getattr(mx_lib(), name), args, tensors)
     from . import layer
-    args, more = epilogue._marshal(b, out, args)
+    args, more = epilogue._marshal(b, out, args, layer._EPILOGUE_AT[name])
     _run(getattr(layer.layer_lib(), name + "_fused"), args, tensors + more)
 
 
@@ -406,15 +406,18 @@ def mx_linear(x, b: MxOperand, alpha: float = 1.0, out=None, dtype=None, stream=
         c = mx_linear(x.flatten(0, -2), b, alpha, None if out is None else out.flatten(0, -2), dtype,
                       epilogue=epilogue)
         return c.view(shape) if out is None else out
+    if epilogue is not None:
+        from . import layer
+        return layer._linear(x, b, alpha, out, dtype, epilogue)
     # (one launch: 16 x 65536 x 8192 52 us, 57 + 2.7 in two; 1 x 6144 x 6144 6.9, 6.4
     # + 2.7.  Behind K = 8192 every 16 columns quantise the rows again, which takes
     # about N K (6 + rows) / 2e8 us: worth it up to the 2.7 us and part of the
     # other call's 8.)
     if x.dim() == 2 and x.shape[0] <= MX_QUANT_ROWS and (
             b.K <= 8192 or b.rows * b.K * (6 + x.shape[0]) <= 800_000_000):
-        return mx_gemm_quantized(x, b, alpha, out, dtype, epilogue=epilogue)
+        return mx_gemm_quantized(x, b, alpha, out, dtype)
     _kind(b, "b", MxOperand)
-    return mx_gemm(mx_quantize(x), b, alpha, out, dtype, epilogue=epilogue)
+    return mx_gemm(mx_quantize(x), b, alpha, out, dtype)
 
 
 def _grouped_args(a, b, row_offsets, alpha, rows, out, dtype):

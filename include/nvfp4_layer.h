@@ -64,7 +64,17 @@ int nvfp4_mx_grouped_gemm_fused(const void* a_packed, const void* a_scales, int6
                                 const nvfp4_mx_epilogue* epilogue, void* out, int out_type,
                                 int64_t M, int64_t N, int64_t K, void* stream);
 
-/* The same calls recorded into a sequence (nvfp4.h, "Recorded sequences"). */
+/* nvfp4_mx_quantize and nvfp4_mx_gemm_fused in one call, or nvfp4_mx_gemm_quantized_fused
+ * where that is faster (up to 16 rows, but for very wide and deep B); the same bits.
+ *   workspace : DEVICE, 16-byte aligned, for the packed rows: the code and scale bytes that
+ *               nvfp4_mx_packed_size(M, K) says, added up; not used (and may be NULL) in the
+ *               one-launch form.  Free again when the call's work is done. */
+int nvfp4_mx_linear_fused(const void* x, int x_type, int64_t ldx, const void* b_packed,
+                          const void* b_scales, float alpha, const nvfp4_mx_epilogue* epilogue,
+                          void* out, int out_type, int64_t M, int64_t N, int64_t K,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* The products recorded into a sequence (nvfp4.h, "Recorded sequences"). */
 int nvfp4_sequence_add_mx_gemm_fused(nvfp4_sequence_t seq, const void* a_packed,
                                      const void* a_scales, const void* b_packed,
                                      const void* b_scales, float alpha,
@@ -96,10 +106,10 @@ int nvfp4_sequence_add_mx_grouped_gemm_fused(nvfp4_sequence_t seq, const void* a
  *
  * For few tokens (up to 4, with rows that fit a workgroup's LDS when they are
  * quantised) the layer runs in two launches, bound by reading the chosen
- * experts' weights once.  Above that it is nvfp4_moe_sort, nvfp4_mx_quantize,
- * nvfp4_mx_grouped_gemm_fused, and the same two again with nvfp4_moe_combine
- * behind them, in one call; each choice's result is then also rounded to the
- * output's type before the sum.  Deterministic either way. */
+ * experts' weights once.  Above that the steps are those of nvfp4_moe_sort,
+ * nvfp4_mx_quantize, nvfp4_mx_grouped_gemm_fused twice and nvfp4_moe_combine, in
+ * four to six launches, each choice's result in fp32 until the sum.
+ * Deterministic either way. */
 typedef struct nvfp4_mx_experts {
     int64_t experts;         /* 1 to 2048 */
     int64_t hidden, inner;   /* row lengths of x and out, and of h: multiples of 32 */

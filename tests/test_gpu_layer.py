@@ -278,3 +278,30 @@ def test_recorded_and_captured():
 def nv_sequence():
     import contextlib
     return contextlib.closing(nv.Sequence())
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 48, 64), (16, 40, 8192), (16, 33, 8224), (16, 4500, 8224), (17, 64, 96), (100, 257, 544),
+                                   (0, 8, 64)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_linear_in_one_call(M, N, K, dtype):
+    """nvfp4_mx_linear_fused: the bits of the two calls it is made of, in its workspace, eager and captured."""
+    say(f"linear {M}x{N}x{K} {dtype}")
+    g = torch.Generator(device=DEV).manual_seed(M + N)
+    x = torch.randn(M, K + 16, device=DEV, generator=g).to(DT[dtype])[:, 8:K + 8]
+    w, v = (nv.mx_quantize(torch.randn(N, K, device=DEV, generator=g)) for _ in range(2))
+    e = nv.MxEpilogue("silu", torch.randn(N, device=DEV, generator=g), v, None,
+                      torch.randn(M, N, device=DEV, generator=g).to(torch.bfloat16))
+    want = nv.mx_gemm(nv.mx_quantize(x), w, 0.5, epilogue=e) if M else x.new_empty(0, N, dtype=torch.bfloat16)
+    out = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device=DEV)
+    assert nv.mx_linear(x, w, 0.5, out, epilogue=e) is out and torch.equal(out, want)
+    if M == 0:
+        return
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = nv.mx_linear(x, w, 0.5, epilogue=e)
+    for seed in range(3):
+        x.copy_(torch.randn(M, K, device=DEV, generator=g))
+        want = nv.mx_gemm(nv.mx_quantize(x), w, 0.5, epilogue=e)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)

@@ -113,12 +113,12 @@ def experts(g, E, F, H, gate, bias, exact, dtype=torch.float32):
 SIZES = [(1, 8, 256, 256, 6144), (1, 1, 1, 32, 32), (3, 2, 5, 96, 160), (4, 8, 64, 256, 544), (2, 128, 300, 64, 96),
          (3, 4, 8, 1056, 2080), (4, 1, 2, 2048, 32), (1, 100, 7, 64, 64), (2, 3, 4, 96, 30016), (16, 8, 64, 256, 544), (17, 4, 8, 160, 2080),
          (33, 3, 2, 64, 4192), (64, 8, 16, 512, 256), (64, 1, 3, 2048, 96), (5, 100, 7, 64, 64), (64, 8, 300, 32, 1024),
-         (65, 2, 4, 96, 160), (20, 30, 9, 64, 96), (130, 8, 32, 288, 544)]
-
-
-def few(T, k, F, H):
-    """Whether the layer runs in two launches: its quantised rows fit 48 KB of LDS."""
-    return T <= 4 and T * k <= 512 and all(rows * -(-K // 512) * 272 <= 48 << 10 for rows, K in ((T, H), (T * k, F)))
+         (65, 2, 4, 96, 160), (20, 30, 9, 64, 96), (130, 8, 32, 288, 544),
+         # choices sorted beside the quantisation and not, short products of up to 16 rows an expert
+         (128, 2, 16, 352, 128), (257, 1, 20, 416, 160), (20, 12, 15, 480, 96), (20, 12, 14, 512, 96),
+         # h packed by the products of 64 x 256, 128 x 128 and 128 x 256 tiles, with broken steps behind the last block
+         (100, 8, 256, 288, 256), (90, 9, 200, 160, 64), (100, 8, 640, 32, 64), (100, 8, 700, 64, 96), (4096, 8, 16, 160, 64),
+         (2500, 4, 9, 544, 96)]
 
 
 @pytest.mark.parametrize("T,k,E,F,H", SIZES)
@@ -135,9 +135,8 @@ def test_exact_sums(T, k, E, F, H, gate, act):
         out = nv.mx_moe(x, ids.to(idt), p, up, down, activation=act, dtype=DT[odt], **more)
         want, mag = expected(x, ids, p, up, down, act, **more)
         # (sums of h's values, which have up to 2^24 times their smallest step, round: a bound as of any
-        # product; the form for many tokens rounds each choice's result too)
-        each = 0.0 if few(T, k, F, H) else torch.finfo(DT[odt]).eps
-        ref.check(out, want, ((F / 64 + 20 + k) * 4 * ref.U + each) * mag, f"{T} {E}")
+        # product)
+        ref.check(out, want, (F / 64 + 20 + k) * 4 * ref.U * mag, f"{T} {E}")
 
 
 @pytest.mark.parametrize("T,k,E,F,H", SIZES)
@@ -162,7 +161,7 @@ def test_random(T, k, E, F, H, act):
 
 def test_both_forms_agree():
     """Four tokens in two launches and the same tokens among 65 by the general form: the same h, so the results differ by
-    the general form's rounding of each choice and fp32 sums only, but for steps of h as above."""
+    fp32 sums only, but for steps of h as above."""
     g = gen(3)
     up, down, more = experts(g, 16, 256, 512, True, True, True)
     x = torch.randint(-2, 3, (65, 512), device=DEV, generator=g).to(torch.bfloat16)

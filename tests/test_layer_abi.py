@@ -82,6 +82,23 @@ def test_epilogue_refusals(record):
     L.nvfp4_sequence_destroy(h)
 
 
+def test_linear_refusals():
+    L = nv.layer.layer_lib()
+
+    def call(e, x=P, kind=1, ld=64, b=P, M=40, N=4, K=64, ws=P, n=1 << 30, out=P):
+        return L.nvfp4_mx_linear_fused(x, kind, ld, b, P, 1.0, e, out, 1, M, N, K, ws, n, None)
+
+    for e in (epi(), None):
+        for bad in (dict(x=None), dict(kind=2), dict(ld=60), dict(b=None), dict(M=-1), dict(N=0), dict(K=48), dict(ws=None),
+                    dict(n=sum(nv.mx_packed_size(40, 64)) - 1), dict(out=None)):
+            assert call(e, **bad) == INV, bad
+        for bad in (dict(x=P + 8), dict(ws=P + 8), dict(out=P + 2), dict(M=3, x=P + 8)):
+            assert call(e, **bad) == MIS, bad
+        assert call(e, M=3, K=48) == INV and call(e, M=3, ld=60) == INV
+    for bad in BAD_EPILOGUES:
+        assert call(epi(**bad)) == INV and call(epi(**bad), M=3, ws=None) == INV, bad
+
+
 def test_epilogue_binding_refuses():
     a, w, off = operand(), groups(), torch.zeros(3, dtype=torch.int32)
     x = torch.zeros(4, 64)
@@ -119,7 +136,8 @@ def test_epilogue_binding_refuses():
 def test_epilogue_arguments(monkeypatch):
     """What reaches the C function: every part, for each product, and the leading dimensions of a linear layer."""
     calls = []
-    monkeypatch.setattr(nv.mx, "_run", lambda fn, args, tensors: calls.append((fn.__name__, args, tensors)))
+    for module in (nv.mx, nv.layer):
+        monkeypatch.setattr(module, "_run", lambda fn, args, tensors: calls.append((fn.__name__, args, tensors)))
     b, g = operand(7), operand(7)
     for lead in ((3,), (2, 3), (4, 100)):
         n = int(torch.tensor(lead).prod())
@@ -127,9 +145,12 @@ def test_epilogue_arguments(monkeypatch):
         e = nv.MxEpilogue("silu", torch.zeros(7), g, torch.ones(7), r)
         nv.mx_linear(torch.zeros(*lead, 64), b, epilogue=e)
         name, args, tensors = calls[-1]
-        assert name == ("nvfp4_mx_gemm_quantized_fused" if n <= 16 else "nvfp4_mx_gemm_fused")
+        assert name == "nvfp4_mx_linear_fused"
         s = next(a for a in args if isinstance(a, nv.layer._EpilogueT))
-        assert args[-3:] == (n, 7, 64) and args[args.index(s) - 1] == 1.0
+        work = tensors[4]
+        size = sum(nv.mx_packed_size(n, 64)) if n > 16 else 0
+        assert (work is None) == (size == 0) and args[args.index(s) - 1] == 1.0
+        assert args[-5:] == (n, 7, 64, work.data_ptr() if size else None, size)
         assert (s.activation, s.gate_packed, s.gate_scales, s.bias, s.gate_bias, s.bias_type, s.residual, s.ld_residual) == \
             (2, g.codes.data_ptr(), g.scales.data_ptr(), e.bias.data_ptr(), e.gate_bias.data_ptr(), 0, r.data_ptr(), 7)
         assert all(any(t is u for u in tensors) for t in (e.bias, e.gate_bias, g.codes, g.scales))

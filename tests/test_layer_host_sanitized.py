@@ -20,6 +20,7 @@ hipError_t launch_mx_gated(const MxGemmArgs&, const MxEpilogueArgs&, hipStream_t
 hipError_t launch_mx_short(const MxGemmArgs&, const MxEpilogueArgs&, hipStream_t) { return hipErrorInvalidValue; }
 bool mx_fused_packs(const MxGemmArgs&) { return true; }
 bool mx_gated_packs(const MxGemmArgs&) { return false; }
+hipError_t launch_moe_combine_narrow(const MoeArgs&, hipStream_t) { return hipErrorInvalidValue; }
 hipError_t launch_moe_route(const MoeArgs&, const MxQuantArgs&, hipStream_t) { return hipErrorInvalidValue; }
 bool mx_fused_fits(const MxGemmArgs&) { return true; }
 bool mx_gated_fits(const MxGemmArgs&) { return true; }
