@@ -778,7 +778,7 @@ class Sequence:
 
     def add_norm(self, y, residual, h, n=None, **how) -> None:
         """Records add_norm(y, residual, h=h, n=n, **how); h None: not kept (as rms_norm).  n is an MxOperand with
-        quantize=True."""
+        quantize=True.  Rows of y, residual and gate follow each other at one stride."""
         from . import layer
         pre = how.setdefault("pre", True)
         if pre and n is None or not pre and h is None:
@@ -786,6 +786,10 @@ class Sequence:
         how = {"post_weight": None, "gate": None, "pre_weight": None, "scale": 1.0, "residual_scale": 1.0, "eps": 1e-6,
                "post": None, "quantize": False, **how}
         _, _, args, tensors = layer._norm_args(y, residual, h=h, n=n, keep=h is not None, **how)
+        gate = how["gate"]
+        for name, given, read in (("y", y, tensors[0]), ("residual", residual, tensors[1]), ("gate", gate, tensors[-1])):
+            if given is not None and given.data_ptr() != read.data_ptr():   # (a copy of what it holds now)
+                raise ValueError(f"recorded rows must follow each other at one stride: {name} does not")
         self._record(layer.layer_lib().nvfp4_sequence_add_norm, args, tensors, list(tensors))
 
     def finalize(self) -> None:

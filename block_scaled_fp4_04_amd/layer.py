@@ -30,8 +30,8 @@ from dataclasses import dataclass
 import torch
 
 from . import Nvfp4Error, _i64, _vp, lib
-from .mx import (MX_BLOCK, MX_QUANT_ROWS, _GEMM, _GEMM_Q, _GROUPED, _KINDS, MxGroups, MxOperand, _gemm_quantized_args, _kind, _on, _out,
-                 _packed, _rows_2d, _run, _type_of)
+from .mx import (MX_BLOCK, MX_QUANT_ROWS, _GEMM, _GEMM_Q, _GROUPED, _KINDS, MxGroups, MxOperand,
+                 _gemm_quantized_args, _kind, _on, _out, _packed, _rows_2d, _run, _type_of)
 
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}   # NVFP4_ACT_*
 
@@ -221,12 +221,14 @@ def _moe_args(x, ids, weights, up, down, gate, activation, up_bias, gate_bias, d
         raise ValueError("expert_ids must be a contiguous [tokens, topk] int32 or int64 tensor")
     if weights is not None and (weights.dtype != torch.float32 or weights.shape != ids.shape or not weights.is_contiguous()):
         raise ValueError(f"weights must be a contiguous float32 tensor of shape {tuple(ids.shape)}")
-    bg, kg = _bias("gate_bias", gate_bias, (E, F))
-    bu, ku = _bias("up_bias", up_bias, (E, F))
-    bd, kd = _bias("down_bias", down_bias, (E, H))
-    bias_type = kg if kg is not None else ku if ku is not None else kd
-    if not (kg in (None, bias_type) and ku in (None, bias_type) and kd in (None, bias_type)):
-        raise ValueError("the biases must be of one type")
+    bg = bu = bd = bias_type = None
+    if not (gate_bias is up_bias is down_bias is None):
+        bg, kg = _bias("gate_bias", gate_bias, (E, F))
+        bu, ku = _bias("up_bias", up_bias, (E, F))
+        bd, kd = _bias("down_bias", down_bias, (E, H))
+        bias_type = kg if kg is not None else ku if ku is not None else kd
+        if not (kg in (None, bias_type) and ku in (None, bias_type) and kd in (None, bias_type)):
+            raise ValueError("the biases must be of one type")
     out, out_kind = _out(out, dtype, T, H, x)
     spec = _ExpertsT(E, H, F, _activation(activation), None if gate is None else gate.codes.data_ptr(),
                      None if gate is None else gate.scales.data_ptr(), up.codes.data_ptr(), up.scales.data_ptr(),
@@ -273,7 +275,10 @@ def _rows_of(name: str, t, shape, dtype):
         return None
     if t.shape != shape or t.dtype is not dtype:
         raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)}")
-    H = shape[-1]
+    return _strided(t, shape[-1])
+
+
+def _strided(t, H: int):
     if t.dim() != 2:
         t = t.reshape(-1, H)
     ld, unit = t.stride()
@@ -301,13 +306,14 @@ def _spec(y, post_weight, gate, pre_weight, scale, residual_scale, eps, post: bo
     weight_type = None
     for name, w in (("post_weight", post_weight), ("pre_weight", pre_weight), ("gate", channel)):
         if w is not None:
-            if w.numel() != H or w.dim() != 1 or not w.is_contiguous() or w.dtype not in _KINDS:
+            of = _KINDS.get(w.dtype)
+            if of is None or w.numel() != H or w.dim() != 1 or not w.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous float32 or bfloat16 tensor of shape ({H},)"
                                  + (f" or {tuple(shape)}" if w is channel else ""))
-            if weight_type not in (None, w.dtype):
+            if weight_type not in (None, of):
                 raise ValueError("the weights (and a gate for each channel) must be of one type")
-            weight_type = w.dtype
-    spec = _NormT(kind, 0 if weight_type is None else _KINDS[weight_type], y.numel() // H, H, post, pre,
+            weight_type = of
+    spec = _NormT(kind, weight_type or 0, y.numel() // H, H, post, pre,
                   None if post_weight is None else post_weight.data_ptr(),
                   None if pre_weight is None else pre_weight.data_ptr(), mode, None if at is None else at.data_ptr(),
                   ld, scale, residual_scale, eps)
@@ -320,8 +326,8 @@ def _at(t):
 
 def _given(name: str, out, like):
     """`out`, made like `like` if it is None, checked otherwise."""
-    if out is None:
-        return like.new_empty((*like.shape,))  # (of a plain tuple: three times as fast)
+    if out is None:   # (of a plain tuple: three times as fast as of a torch.Size)
+        return torch.empty_like(like) if like.is_contiguous() else like.new_empty((*like.shape,))
     if out.shape != like.shape or out.dtype != like.dtype or not out.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {like.dtype} tensor of shape {tuple(like.shape)}")
     return out
@@ -330,7 +336,7 @@ def _given(name: str, out, like):
 def _norm_args(y, residual, post_weight, gate, pre_weight, scale, residual_scale, eps, post, pre, quantize, h, n, keep):
     post = post_weight is not None if post is None else bool(post)
     spec, named = _spec(y, post_weight, gate, pre_weight, scale, residual_scale, eps, post, bool(pre))
-    rows = _rows_of("y", y, y.shape, y.dtype)
+    rows = _strided(y, y.shape[-1])
     res = _rows_of("residual", residual, y.shape, y.dtype)
     h = _given("h", h, y) if keep else None
     codes = scales = None

@@ -290,3 +290,23 @@ def test_a_whole_layer(T):
         for a, b in ((sf, f), (sy, y), (sh1, h1), (sn1, n1), (sm, m), (sh2, h2), (sn2, n2)):
             assert torch.equal(a, b)
     seq.close()
+
+
+@pytest.mark.parametrize("T,k,E,F,H", SIZES)
+@pytest.mark.parametrize("gated", [True, False])
+def test_whatever_the_workspace_holds(T, k, E, F, H, gated):
+    """The same bits from a workspace full of NaN scales (0xFF) as from one of zeros: all that counts is written."""
+    say(f"moe workspace {T}x{k} of {E}, {F} x {H}")
+    g = gen(T + E)
+    up, down, more = experts(g, E, F, H, gated, True, False)
+    x, ids = randn(g, T, H, dtype=torch.bfloat16), choices(g, T, k, E)
+    outs = []
+    for fill in (0, 255):
+        out, args, tensors = nv.layer._moe_args(x, ids, None, up, down, more.get("gate"), "silu", more["up_bias"],
+                                                more.get("gate_bias"), more["down_bias"], None, None)
+        work = tensors[4]
+        assert work.dtype == torch.uint8 and args[-2:] == (work.data_ptr(), work.numel())
+        work.fill_(fill)
+        nv.mx._run(nv.layer.layer_lib().nvfp4_mx_moe, args, tensors)
+        outs.append(out)
+    assert outs[0].isfinite().all() and torch.equal(*outs)

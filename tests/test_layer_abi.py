@@ -337,3 +337,16 @@ def test_moe_binding_refuses():
     with pytest.raises(ValueError, match="out"):
         seq.add_mx_moe(x, ids, p, up, down, None)
     assert seq.calls == 0
+
+
+def test_recorded_rows_are_not_copies():
+    """Eager calls copy rows that do not follow each other at one stride; a recorded call would keep what they held."""
+    seq, rows, wide = nv.Sequence(), torch.zeros(4, 8), torch.zeros(8, 4).t()
+    for y, r, gate, match in ((wide, rows, None, "y does"), (rows, rows[:1].expand(4, 8), None, "residual does"),
+                              (rows, wide, None, "residual does"), (rows, None, wide, "gate does"),
+                              (torch.zeros(4, 2, 8)[:, :1].expand(4, 2, 8), None, None, "y does")):
+        with pytest.raises(ValueError, match=match):
+            seq.add_norm(y, r, torch.zeros(*y.shape), torch.zeros(*y.shape), gate=gate)
+    with pytest.raises(ValueError, match="GPU"):
+        seq.add_norm(torch.zeros(4, 2, 9)[..., 1:], torch.zeros(4, 2, 8), torch.zeros(4, 2, 8), torch.zeros(4, 2, 8), gate=torch.ones(8))
+    assert seq.calls == 0
