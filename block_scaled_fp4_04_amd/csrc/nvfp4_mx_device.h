@@ -181,7 +181,8 @@ __device__ __forceinline__ float mx_widen(uint32_t w, int high) {
 // gelu takes 1 - erf(x) of x >= 0 as exp(-x^2) times a polynomial in 1 / (1 + p
 // x) (Abramowitz and Stegun 7.1.26), off by 1.5e-7 at most, and so by 0.75e-7
 // |z|: a wave has the epilogue to itself, and with the library's erf, whose two
-// ranges a wave runs both, 1237 x 2056 x 6112 with gelu took several us more.
+// ranges a wave runs both, 1237 x 2056 x 6112 with gelu took 29.0 us, 24.2 so
+// (of another form of the epilogue).
 __device__ __forceinline__ float mx_logistic(float z) {  // 1 / (1 + exp(-z))
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * z));
 }

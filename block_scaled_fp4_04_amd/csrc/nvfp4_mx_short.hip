@@ -8,10 +8,9 @@
 // wave works by itself on a run of the units (16 rows of one group, 32
 // columns) in the groups' order: the rows stay in its registers from unit to
 // unit, and the weights of the two units behind are on their way while one is
-// multiplied.  256 experts x (6144 x 256), us with tiles and here: 8 choices 5.6
-// and 5, 128 choices 26.4 and 17.6, 512 choices 52.5 and 36 (138 MB of weights).
-// With two scale words to a row (K up to 1024) it was no faster than tiles: 32 x
-// (2048 x 1024), 183 choices 9.3 and 12.5.
+// multiplied.  256 experts x (6144 x 256), us with tiles and here: 128
+// choices 26.4 and 17.6, 512 choices 52.5 and 36 (138 MB of weights).  With two
+// scale words to a row (K up to 1024) it was slower than tiles.
 #include "nvfp4_mx_parts.h"
 
 #include <algorithm>

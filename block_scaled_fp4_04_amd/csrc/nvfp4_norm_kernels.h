@@ -22,6 +22,10 @@
 //   v          = scale * D * gate * w_post        (without post: dy = scale * D * gate)
 //   dw_post   += scale * D * gate * y * ry
 //   dy         = ry * v - y * ry^3 * mean(v * y)
+// 8192 x 2048 bfloat16 with all parts 50 us and 5 for the sums' second launch,
+// 3.6 TB/s: 16 waves a CU at 128 registers.  The next row's loads ahead of the
+// sums spilled (78 us); pieces of 8 bytes at twice the waves spilled (106);
+// two workgroups of 8 waves a CU 55.6.
 // Sums over rows: a workgroup keeps those of its rows in registers, adds its
 // teams' through LDS and leaves them in the workspace, and a second launch
 // adds the workgroups' in order: no atomics, the same bits every time.
