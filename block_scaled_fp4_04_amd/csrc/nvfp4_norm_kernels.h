@@ -132,6 +132,25 @@ __device__ __forceinline__ void team_sum(float (&x)[N], float (*part)[16][N], in
     turn ^= 1;
 }
 
+// What is the same in every lane, in a scalar register.
+__device__ __forceinline__ float uniform(float x) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, x)));
+}
+// Squares are added as x^2 2^-k over a row, 2^k above its length: the sum then
+// passes fp32's range where the mean does, not before, and no other bit changes.
+// Squares that become too small for that do not count beside an eps of 1e-30;
+// with a smaller one k is 0, and small rows keep their bits.  (In scalar registers:
+// 16384 x 6144 bfloat16 with all parts 189 us, 206 in vector ones.)
+struct Squares {
+    float down, mean;  // 2^-k; 2^k / hidden
+    __device__ __forceinline__ Squares(int hidden, float eps) {
+        const int k = eps >= 1e-30f ? 32 - __builtin_clz(hidden) : 0;
+        down = uniform(__builtin_bit_cast(float, (127 - k) << 23));
+        mean = uniform(1.0f / (float)hidden * __builtin_bit_cast(float, (127 + k) << 23));
+    }
+    __device__ __forceinline__ float of(float x) const { return x * down * x; }
+};
+
 // ---- forward ------------------------------------------------------------------
 
 // A workgroup takes a row at a time; or, if one wave holds a row, four.
@@ -146,7 +165,7 @@ __global__ void __launch_bounds__(1024, P == 1 ? 6 : 4) norm_kernel(NormArgs a, 
     const int teams = waves == 1 ? 4 : 1, threads = waves * 64;
     const int tid = waves == 1 ? lane : (int)threadIdx.x;
     const Columns<V, P, ODD> c(a.hidden, threads, tid);
-    const float mean = 1.0f / (float)a.hidden;
+    const Squares sq(a.hidden, a.eps);
     const int steps = (a.hidden + kMxStep - 1) / kMxStep, words = (steps + 3) / 4;
     // (a team of one wave may leave before the others: it meets no barrier)
     for (int64_t row = (int64_t)blockIdx.x * teams + (waves == 1 ? threadIdx.x >> 6 : 0); row < rows_out;
@@ -187,9 +206,9 @@ __global__ void __launch_bounds__(1024, P == 1 ? 6 : 4) norm_kernel(NormArgs a, 
 #pragma unroll
             for (int p = 0; p < P; ++p)
 #pragma unroll
-                for (int i = 0; i < V; ++i) sum[0] += widen(y[p].v[i]) * widen(y[p].v[i]);
+                for (int i = 0; i < V; ++i) sum[0] += sq.of(widen(y[p].v[i]));
             team_sum<1>(sum, part, turn, 0, waves);
-            ry = rsqrtf(sum[0] * mean + a.eps);
+            ry = rsqrtf(sum[0] * sq.mean + a.eps);
         }
         float sum[1] = {0.0f};  // h^2
 #pragma unroll
@@ -200,14 +219,14 @@ __global__ void __launch_bounds__(1024, P == 1 ? 6 : 4) norm_kernel(NormArgs a, 
                 if constexpr (POST) u *= ry * wpost[p][i];
                 u *= ELEMENT ? widen(gate[p].v[i]) : wgate[p][i];
                 narrow(a.residual_scale * widen(res[p].v[i]) + a.scale * u, y[p].v[i]);  // now h
-                const float h = widen(y[p].v[i]);
-                sum[0] += (ODD ? i >= c.skip[p] : c.skip[p] == 0) ? h * h : 0.0f;
+                const float h2 = sq.of(widen(y[p].v[i]));
+                sum[0] += (ODD ? i >= c.skip[p] : c.skip[p] == 0) ? h2 : 0.0f;
             }
             if (a.h) c.store(static_cast<T*>(a.h) + row * a.hidden, p, y[p]);
         }
         if (!a.pre) continue;
         team_sum<1>(sum, part, turn, 0, waves);
-        const float rh = rsqrtf(sum[0] * mean + a.eps);
+        const float rh = rsqrtf(sum[0] * sq.mean + a.eps);
 #pragma unroll
         for (int p = 0; p < P; ++p) {
 #pragma unroll
@@ -257,9 +276,13 @@ __global__ void __launch_bounds__(kGradWaves * 64) norm_grad_kernel(NormArgs a, 
     __shared__ float sums[P == 1 ? kGradWaves * 64 * V : 1];
     int turn = 0;
     const int threads = waves * 64, teams = (int)blockDim.x / threads;
-    const int tid = threadIdx.x % threads, team = threadIdx.x / threads, first_wave = team * waves;
+    // (the team in a scalar register, and with it the rows' addresses: 8192 x 2048
+    // bfloat16 54.6 us, 58.9 otherwise; rows of several pieces to a lane have one
+    // team, and 2053 x 5003 fp32 took 79.4 so, 78.4 otherwise)
+    const int tid = threadIdx.x % threads, team = P > 1 ? (int)threadIdx.x / threads : __builtin_amdgcn_readfirstlane((int)threadIdx.x / threads), first_wave = team * waves;
     const Columns<V, P, ODD> c(a.hidden, threads, tid);
-    const float mean = 1.0f / (float)a.hidden;
+    const float mean = uniform(1.0f / (float)a.hidden);
+    const Squares sq(a.hidden, a.eps);
     float dpre[P][V], dpost[P][V], dgate[P][V];  // sums over the team's rows
     Weights<V, WB> wpre[P], wpost[P], wgate[P];
 #pragma unroll
@@ -291,16 +314,16 @@ __global__ void __launch_bounds__(kGradWaves * 64) norm_grad_kernel(NormArgs a, 
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const float x = widen(h[p].v[i]);
-                sum[0] += x * x;
+                sum[0] += sq.of(x);
                 sum[1] += widen(n[p].v[i]) * wpre[p][i] * x;
-                if constexpr (POST) sum[2] += widen(y[p].v[i]) * widen(y[p].v[i]);
+                if constexpr (POST) sum[2] += sq.of(widen(y[p].v[i]));
             }
         if (POST || a.pre) team_sum(sum, part, turn, first_wave, waves);
         // (no norm or no row: nothing but zeros, also with an eps of 0)
-        const float rh = live && a.pre ? rsqrtf(sum[0] * mean + a.eps) : 0.0f;
+        const float rh = live && a.pre ? rsqrtf(sum[0] * sq.mean + a.eps) : 0.0f;
         const float back = rh * rh * rh * (sum[1] * mean);
         float ry = 0.0f;
-        if constexpr (POST) ry = live ? rsqrtf(sum[2] * mean + a.eps) : 0.0f;
+        if constexpr (POST) ry = live ? rsqrtf(sum[2] * sq.mean + a.eps) : 0.0f;
         float dot[1] = {0.0f}, d[P][V];
 #pragma unroll
         for (int p = 0; p < P; ++p) {

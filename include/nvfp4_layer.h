@@ -154,7 +154,9 @@ int nvfp4_sequence_add_mx_moe(nvfp4_sequence_t seq, const nvfp4_mx_experts* laye
  * by rows, in fp32; h is rounded to its type once, and n is the norm of the
  * rounded h, rounded once: the same as that norm of the stored h in a call of
  * its own.  A mean of squares past fp32's range is an infinity (values of 2^64
- * and more; such a row's norm is zeros, NaN where an infinity stood). */
+ * and more; such a row's norm is zeros, NaN where an infinity stood).  With an
+ * eps below 1e-30, beside which small squares count, their sum has that limit
+ * (values of 2^64 / sqrt(hidden)), and values below 2^-63 lose bits. */
 enum { NVFP4_GATE_NONE = 0, NVFP4_GATE_CHANNEL = 1, NVFP4_GATE_ELEMENT = 2 };
 #define NVFP4_NORM_MAX_HIDDEN 16384
 

@@ -290,3 +290,48 @@ def test_streams_graphs_and_sequences():
         assert torch.equal(sh, want[0]) and torch.equal(sq.codes, q.codes) and torch.equal(sq.scales, q.scales)
         assert torch.equal(n1, nv.rms_norm(y, how["pre_weight"]))
     seq.close()
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("H", [3, 64, 201, 2048, 2050, 4100, 6144, 9000, 16384])
+def test_rows_up_to_the_largest_mean_of_squares(H, dtype):
+    """Rows whose sum of squares passes fp32's range while its mean does not, side by side with others: the limit is the
+    mean's, 2^128, from which on rows are zeros."""
+    say(f"rows of {H} up to 2^64 {dtype}")
+    g = gen(H)
+    rows = 45
+    size = torch.exp2(torch.randint(-20, 63, (rows, 1), device=DEV, generator=g).float())
+    size[::3] = 2.0 ** 62.5
+    size[5:8] = 1.0
+    sign = lambda: torch.where(torch.rand(rows, H, device=DEV, generator=g) < 0.5, -1.0, 1.0)  # noqa: E731
+    x = (size * sign() * (1 + 0.25 * torch.rand(rows, H, device=DEV, generator=g))).to(DT[dtype])    # (the mean stays below 2^126)
+    wide = dict(scale=0.75, residual_scale=1.25, eps=1e-6)
+    for post, pre in ((False, True), (True, False)):
+        w = randn(g, H, scale=0.3, shift=1.0)
+        how = dict(wide, post=post, post_weight=w if post else None, pre_weight=w if pre else None, gate=randn(g, H) if post else None)
+        # the norm before the next block of large rows h, and the norm behind a block of large rows y
+        y, res = (x, (sign() * 2.0 ** -3).to(x.dtype)) if post else ((sign() * 2.0 ** -3).to(x.dtype), (x * 0.5).to(x.dtype))
+        h, n = nv.add_norm(y, res, pre=pre, **how)
+        check_forward(y, res, how, pre, h, n, f"{H} {post}")
+        # what the weights' gradients add of these rows
+        dh, dn = randn(g, rows, H, dtype=x.dtype), None
+        if pre:
+            dh, dn = None, randn(g, rows, H, dtype=x.dtype)
+        gr = nv.add_norm_grad(dh, dn, y, h, **how)
+        want = ref.norm_grads(dbl(dh), dbl(dn), dbl(y), dbl(h), post, dbl(how["post_weight"]), dbl(how["gate"]), dbl(how["pre_weight"]),
+                              0.75, 1.25, 1e-6, channel=True)
+        for name in ("gate", "post_weight") if post else ("pre_weight",):
+            ref.check(getattr(gr, name), *want[name], f"{H} d{name}")
+    # and past it
+    x[4], x[9] = 2.0 ** 64.5, -(2.0 ** 90)
+    n = nv.rms_norm(x)
+    assert (n[4] == 0).all() and (n[9] == 0).all()
+    keep = [r for r in range(rows) if r not in (4, 9)]
+    ref.check(n[keep], *ref.norm_n(x[keep].double(), None, 1e-6))
+    # an eps beside which small squares count
+    x = torch.ones(4, H, device=DEV, dtype=DT[dtype])
+    x[0], x[1], x[2] = 2.0 ** -61, 2.0 ** 63 / H ** 0.5, 2.0 ** 60
+    n = nv.rms_norm(x, eps=0.0)
+    past = H > 256
+    ref.check(n[[0, 1, 3] if past else [0, 1, 2, 3]], *ref.norm_n(x[[0, 1, 3] if past else [0, 1, 2, 3]].double(), None, 0.0))
+    assert not past or (n[2] == 0).all()
