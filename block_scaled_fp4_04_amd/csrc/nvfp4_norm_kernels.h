@@ -16,12 +16,14 @@
 //
 // Gradients, with t = dn * w_pre and by rows:
 //   dw_pre    += dn * h * rh
-//   D          = dh + rh * t - h * rh^3 * mean(t * h)
+//   D          = dh + rh * (t - h * rh * mean(t * h * rh))
 //   dresidual  = residual_scale * D
 //   dgate      = scale * D * u                    (a CHANNEL gate's: summed)
 //   v          = scale * D * gate * w_post        (without post: dy = scale * D * gate)
 //   dw_post   += scale * D * gate * y * ry
-//   dy         = ry * v - y * ry^3 * mean(v * y)
+//   dy         = ry * (v - y * ry * mean(v * y * ry))
+// (rh goes with h and ry with y: their cubes leave fp32's normal range from an
+// rms of 2^42 on, and below 2^-42)
 // 8192 x 2048 bfloat16 with all parts 50 us and 5 for the sums' second launch,
 // 3.6 TB/s: 16 waves a CU at 128 registers.  The next row's loads ahead of the
 // sums spilled (78 us); pieces of 8 bytes at twice the waves spilled (106);
@@ -321,7 +323,7 @@ __global__ void __launch_bounds__(kGradWaves * 64) norm_grad_kernel(NormArgs a, 
         if (POST || a.pre) team_sum(sum, part, turn, first_wave, waves);
         // (no norm or no row: nothing but zeros, also with an eps of 0)
         const float rh = live && a.pre ? rsqrtf(sum[0] * sq.mean + a.eps) : 0.0f;
-        const float back = rh * rh * rh * (sum[1] * mean);
+        const float back = sum[1] * mean * rh;  // mean(t h) / rms
         float ry = 0.0f;
         if constexpr (POST) ry = live ? rsqrtf(sum[2] * sq.mean + a.eps) : 0.0f;
         float dot[1] = {0.0f}, d[P][V];
@@ -330,8 +332,8 @@ __global__ void __launch_bounds__(kGradWaves * 64) norm_grad_kernel(NormArgs a, 
             Piece<T, V> dres, dg;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float x = widen(h[p].v[i]), g = widen(n[p].v[i]) * rh;
-                float v = widen(dh[p].v[i]) + (g * wpre[p][i] - back * x);
+                const float x = widen(h[p].v[i]) * rh, g = widen(n[p].v[i]);
+                float v = widen(dh[p].v[i]) + rh * (g * wpre[p][i] - back * x);
                 dpre[p][i] += g * x;
                 narrow(a.residual_scale * v, dres.v[i]);
                 v *= a.scale;
@@ -346,8 +348,8 @@ __global__ void __launch_bounds__(kGradWaves * 64) norm_grad_kernel(NormArgs a, 
                     }
                 }
                 if constexpr (POST) {
-                    const float z = widen(y[p].v[i]);
-                    dpost[p][i] += v * (z * ry);
+                    const float z = widen(y[p].v[i]) * ry;
+                    dpost[p][i] += v * z;
                     v *= wpost[p][i];
                     dot[0] += v * z;
                 }
@@ -358,11 +360,11 @@ __global__ void __launch_bounds__(kGradWaves * 64) norm_grad_kernel(NormArgs a, 
         }
         if constexpr (POST) {
             team_sum<1>(dot, part_dot, turn, first_wave, waves);
-            const float along = ry * ry * ry * (dot[0] * mean);
+            const float along = dot[0] * mean;
 #pragma unroll
             for (int p = 0; p < P; ++p)
 #pragma unroll
-                for (int i = 0; i < V; ++i) d[p][i] = ry * d[p][i] - along * widen(y[p].v[i]);
+                for (int i = 0; i < V; ++i) d[p][i] = ry * (d[p][i] - along * (widen(y[p].v[i]) * ry));
         }
         if (a.dy && live) c.store(static_cast<T*>(a.dy) + row * a.hidden, d);
     }

@@ -335,3 +335,46 @@ def test_rows_up_to_the_largest_mean_of_squares(H, dtype):
     past = H > 256
     ref.check(n[[0, 1, 3] if past else [0, 1, 2, 3]], *ref.norm_n(x[[0, 1, 3] if past else [0, 1, 2, 3]].double(), None, 0.0))
     assert not past or (n[2] == 0).all()
+
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("size,eps", [(1e-15, 0.0), (1e12, 1e-6), (1e15, 1e-6), (1e17, 0.0), (1e17, 1e-6)])
+@pytest.mark.parametrize("H", [40, 96, 2048, 6001])
+def test_gradients_of_rows_far_from_one(H, size, eps, dtype):
+    """The part of a gradient along the row: of a size with the rest whatever the row's."""
+    if H * (3 * size) ** 2 > 2.0 ** 128 and eps < 1e-30:
+        pytest.skip("values of 3e17 are past the header's limit for such an eps, 2^64 / sqrt(6001) = 2.4e17")
+    say(f"gradients of rows of {H}, {size} {dtype}")
+    g = gen(H)
+    for post, pre in ((False, True), (True, False), (True, True)):
+        y, res, how = make(g, 9, H, DT[dtype], torch.float32, post, "channel", pre)
+        y, res, how = (y * size).to(y.dtype), (res * size).to(y.dtype), dict(how, eps=eps)
+        h, n = nv.add_norm(y, res, pre=pre, **how)
+        check_forward(y, res, how, pre, h, n, f"{H} {size}")
+        # gradients that point along the rows, beside what does not
+        dh, dn = (randn(g, 9, H) + 2 * y.float() / size).to(y.dtype), None
+        if pre:
+            dh, dn = None, (randn(g, 9, H) + 2 * h.float() / h.float().square().mean(1, keepdim=True).sqrt()).to(y.dtype)
+        check_grads(dh, dn, y, h, how, nv.add_norm_grad(dh, dn, y, h, **how), f"{H} {size} {post} {pre}")
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("H", [3, 64, 201, 2048, 2050, 4100, 6144, 9000, 16384])
+def test_gradients_up_to_the_largest_mean_of_squares(H, dtype):
+    """Rows of 2^-20 to 2^62.5 side by side."""
+    say(f"gradients of rows of {H} up to 2^64 {dtype}")
+    g = gen(H + 1)
+    rows = 45
+    size = torch.exp2(torch.randint(-20, 63, (rows, 1), device=DEV, generator=g).float())
+    size[::3] = 2.0 ** 62.5
+    sign = lambda: torch.where(torch.rand(rows, H, device=DEV, generator=g) < 0.5, -1.0, 1.0)  # noqa: E731
+    x = (size * sign() * (1 + 0.25 * torch.rand(rows, H, device=DEV, generator=g))).to(DT[dtype])
+    w = randn(g, H, scale=0.3, shift=1.0)
+    along = (randn(g, rows, H) + x.float() / size).to(x.dtype)
+    for post, pre in ((False, True), (True, False)):
+        how = dict(post=post, post_weight=w if post else None, pre_weight=w if pre else None, gate=randn(g, H) if post else None,
+                   scale=0.75, residual_scale=1.25, eps=1e-6)
+        y, h = (x, randn(g, rows, H, dtype=x.dtype)) if post else (randn(g, rows, H, dtype=x.dtype), x)
+        dh, dn = (None, along) if pre else (along, None)
+        check_grads(dh, dn, y, h, how, nv.add_norm_grad(dh, dn, y, h, **how), f"{H} {post}")
