@@ -271,7 +271,7 @@ int check_norm(const nvfp4_norm* f, NormArgs* a) {
     a->rows = f->rows;
     a->post_weight = post_weight;
     a->pre_weight = pre_weight;
-    a->gate = f->gate;
+    a->gate = element || channel ? f->gate : nullptr;  // (the forward kernel takes any other one for a channel's)
     a->scale = f->scale;
     a->residual_scale = f->residual_scale;
     a->eps = f->eps;

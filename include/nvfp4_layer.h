@@ -169,7 +169,7 @@ typedef struct nvfp4_norm {
     const void* pre_weight;
     int gate_mode;           /* NVFP4_GATE_* */
     const void* gate;        /* DEVICE; CHANNEL: [hidden], the same for every row; ELEMENT: rows x hidden
-                                of `type`, row stride ld_gate */
+                                of `type`, row stride ld_gate; NONE: not looked at */
     int64_t ld_gate;
     float scale, residual_scale, eps;   /* eps >= 0 */
 } nvfp4_norm;

@@ -378,3 +378,22 @@ def test_gradients_up_to_the_largest_mean_of_squares(H, dtype):
         y, h = (x, randn(g, rows, H, dtype=x.dtype)) if post else (randn(g, rows, H, dtype=x.dtype), x)
         dh, dn = (None, along) if pre else (along, None)
         check_grads(dh, dn, y, h, how, nv.add_norm_grad(dh, dn, y, h, **how), f"{H} {post}")
+
+
+def test_a_gate_of_mode_none_is_not_read():
+    """A description used again with NVFP4_GATE_NONE may still name the gate of another call."""
+    import ctypes
+    L = nv.layer.layer_lib()
+    for dtype in DT.values():
+        for post in (False, True):
+            g = gen(5)
+            y, res, how = make(g, 6, 200, dtype, torch.float32, post, "none", True)
+            want_h, want_n = nv.add_norm(y, res, **how)
+            left = randn(g, 200)
+            spec = nv.layer._NormT(0 if dtype is torch.float32 else 1, 0, 6, 200, post, 1,
+                                   how["post_weight"].data_ptr() if post else None, how["pre_weight"].data_ptr(), 0, left.data_ptr(),
+                                   200, how["scale"], how["residual_scale"], how["eps"])
+            h, n = torch.empty_like(y), torch.empty_like(y)
+            args = (ctypes.byref(spec), y.data_ptr(), 200, res.data_ptr(), 200, h.data_ptr(), n.data_ptr(), None, None)
+            assert L.nvfp4_add_norm(*args, torch.cuda.current_stream().cuda_stream) == nv.OK
+            assert torch.equal(h, want_h) and torch.equal(n, want_n)
