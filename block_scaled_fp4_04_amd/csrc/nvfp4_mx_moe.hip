@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kUpWaves * 64) moe_up_few_kernel(MxMoeArgs a) 
                 const int64_t b = (int64_t)e * a.inner + col;
                 mx_f4 z = sum_of(GATED ? lane + 32 : lane) + mx_row4(a.up_bias, a.bias_bf16, b, col, a.inner), gate = z;
                 if constexpr (GATED) gate = sum_of(lane) + mx_row4(a.gate_bias, a.bias_bf16, b, col, a.inner);
-                mx_by_act(a.act, [&](auto ACT) {
+                mx_by_act(a.act, true, [&](auto ACT) {
 #pragma unroll
                     for (int v = 0; v < 4; ++v) z[v] = GATED ? mx_act<ACT.value>(gate[v]) * z[v] : mx_act<ACT.value>(z[v]);
                 });

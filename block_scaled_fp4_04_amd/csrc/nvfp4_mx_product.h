@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(1024) mx_skinny_kernel(MxGemmArgs a, MxEpi<EPI
                     const mx_f4 bias = mx_row4(e.bias, e.bias_bf16, at, col, a.N);
                     const mx_f4 gate_bias = mx_row4(e.gate_bias, e.bias_bf16, at, col, a.N);
                     mx_f4 z = mx_row4(e.residual, a.out_bf16, row * e.ldr + col, col, a.N);
-                    mx_by_act(e.act, [&](auto ACT) {
+                    mx_by_act(e.act, a.out_bf16, [&](auto ACT) {
 #pragma unroll
                         for (int v = 0; v < 4; ++v)
                             z[v] += mx_epilogue<EPI, ACT.value>(a.alpha, sum[v], gate[v], bias[v], gate_bias[v]);
@@ -767,7 +767,7 @@ __global__ void __launch_bounds__(KS * 256, KS > 1 || BM * BN > 128 * 256 ? KS :
                 }
             });
         };
-        mx_by_act(e.act, rows);
+        mx_by_act(e.act, a.out_bf16, rows);
         // packed rows are filled up to whole steps and scale words
         if (e.q_codes && tn == tiles_n - 1 && wn == 0) {
             const int Qn = (a.N + 4 * kMxStep - 1) / (4 * kMxStep), more = Qn * 16 - a.N / kMxBlock;

@@ -19,7 +19,11 @@ extern "C" {
 /* Activations, in fp32:
  *   SILU       z / (1 + exp(-z))
  *   GELU       z * (1 + erf(z / sqrt(2))) / 2
- *   GELU_TANH  z * (1 + tanh(sqrt(2 / pi) * (z + 0.044715 z^3))) / 2 */
+ *   GELU_TANH  z * (1 + tanh(sqrt(2 / pi) * (z + 0.044715 z^3))) / 2
+ * with the GPU's power of two and reciprocal.  Relative errors, with u = 2^-24: SILU
+ * up to 2 (|z| + 8) u, GELU_TANH up to 8 (|x| + 8) u of its exponent x = 1.6 z (1 +
+ * 0.045 z^2), GELU up to (1.5 z^2 + 48) u: measured 1.3e-7 for z > -0.5 (7.5e-7 before
+ * a result is rounded to bfloat16), 6e-7 at -2, 1.7e-6 at -5. */
 enum {
     NVFP4_ACT_NONE = 0,
     NVFP4_ACT_RELU = 1,

@@ -305,3 +305,18 @@ def test_linear_in_one_call(M, N, K, dtype):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("M", [3, 70])
+def test_gelu_by_its_own_size(M):
+    """gelu keeps its digits where it is small: z comes as it is from the bias of a product of zeros.  With u = 2^-24,
+    erfc's factor adds 9 terms of at most 2.2 times their sum and its argument's 3 roundings at a slope below 2.8: 48 u;
+    the exponent z^2 / 2 is rounded three times: 1.5 z^2 u."""
+    N = 4096
+    z = torch.cat([torch.linspace(-12, 12, N - 200, device=DEV), torch.linspace(-1e-3, 1e-3, 200, device=DEV)])
+    a, b = nv.mx_quantize(torch.zeros(M, 32, device=DEV)), nv.mx_quantize(torch.zeros(N, 32, device=DEV))
+    want = ref.act("gelu", z.double())
+    for dtype in DT.values():
+        out = nv.mx_gemm(a, b, dtype=dtype, epilogue=nv.MxEpilogue("gelu", bias=z))
+        assert torch.equal(out, out[:1].expand_as(out))
+        ref.check(out[0], want, (48 + 1.5 * z.double() ** 2) * ref.U * want.abs())
