@@ -24,6 +24,7 @@ recorded by autograd, and results carry no history.
 from __future__ import annotations
 
 import ctypes
+import dataclasses
 import functools
 from dataclasses import dataclass
 
@@ -175,6 +176,9 @@ _EPILOGUE_AT = {"nvfp4_mx_gemm": 5, "nvfp4_mx_gemm_quantized": 6, "nvfp4_mx_grou
 def _linear(x, b, alpha, out, dtype, epilogue):
     """mx_linear of a 2-D x with an epilogue: one call (nvfp4_mx_linear_fused)."""
     out, args = _gemm_quantized_args(x, b, alpha, out, dtype)
+    r = epilogue.residual
+    if r is not None and r.dim() == 2 and r.shape[0] > 1 and r.stride(0) < r.shape[1] and 1 in (r.stride(1), r.shape[1]):
+        epilogue = dataclasses.replace(epilogue, residual=r.contiguous())   # (one row for all of them, say)
     args, more = epilogue._marshal(b, out, args, 6)
     work, size = None, 0
     if x.shape[0] > MX_QUANT_ROWS or b.K > 8192:   # (below that the call takes no workspace)

@@ -391,7 +391,7 @@ def mx_linear(x, b: MxOperand, alpha: float = 1.0, out=None, dtype=None, stream=
     mx_quantize and mx_gemm.  Both give the same bits.  Dimensions in front of
     K (batch x sequence x K) are rows, and C has them in front of N; an x whose
     rows do not follow each other at one stride is copied first, and so is such a
-    residual of the ``epilogue``."""
+    residual of the ``epilogue``, or one whose rows overlap (broadcast ones)."""
     if stream is not None:
         with _on(stream, x):
             return mx_linear(x, b, alpha, out, dtype, epilogue=epilogue)

@@ -320,3 +320,14 @@ def test_gelu_by_its_own_size(M):
         out = nv.mx_gemm(a, b, dtype=dtype, epilogue=nv.MxEpilogue("gelu", bias=z))
         assert torch.equal(out, out[:1].expand_as(out))
         ref.check(out[0], want, (48 + 1.5 * z.double() ** 2) * ref.U * want.abs())
+
+
+def test_broadcast_residuals():
+    """One row of a residual for all rows of a linear layer, with and without leading dimensions."""
+    g = gen(12)
+    b = nv.mx_quantize(randn(g, 40, 64))
+    for lead in ((5,), (30,), (2, 3), (3, 20)):
+        x, row = randn(g, *lead, 64), randn(g, 40, dtype=torch.bfloat16)
+        for r in (row.expand(*lead, 40), randn(g, *lead, 40, dtype=torch.bfloat16)[..., :1, :].expand(*lead, 40)):
+            want = nv.mx_linear(x, b, epilogue=nv.MxEpilogue("silu", residual=r.contiguous()))
+            assert torch.equal(nv.mx_linear(x, b, epilogue=nv.MxEpilogue("silu", residual=r)), want)

@@ -350,3 +350,28 @@ def test_recorded_rows_are_not_copies():
     with pytest.raises(ValueError, match="GPU"):
         seq.add_norm(torch.zeros(4, 2, 9)[..., 1:], torch.zeros(4, 2, 8), torch.zeros(4, 2, 8), torch.zeros(4, 2, 8), gate=torch.ones(8))
     assert seq.calls == 0
+
+
+def test_broadcast_residuals_of_a_linear_layer_are_copied(monkeypatch):
+    """Rows of a residual that overlap (one row for all of them) reach the call as rows of their own."""
+    calls = []
+    monkeypatch.setattr(nv.layer, "_run", lambda fn, args, tensors: calls.append((args, tensors)))
+    b, row = operand(7), torch.arange(7, dtype=torch.bfloat16)
+    for lead in ((6,), (2, 3), (40,), (4, 2, 5)):
+        n = int(torch.tensor(lead).prod())
+        whole = torch.arange(n * 7, dtype=torch.bfloat16).view(*lead, 7)
+        wide = torch.zeros(*lead, 9, dtype=torch.bfloat16)[..., :7]
+        some = [row.expand(*lead, 7), whole] + [whole[..., :1, :].expand(*lead, 7)] * (len(lead) > 1)
+        for r in some + [wide]:
+            nv.mx_linear(torch.zeros(*lead, 64), b, epilogue=nv.MxEpilogue(residual=r))
+            args, tensors = calls[-1]
+            s = next(a for a in args if isinstance(a, nv.layer._EpilogueT))
+            read = next(t for t in tensors if t is not None and t.data_ptr() == s.residual and t.shape == (n, 7))
+            assert s.ld_residual == read.stride(0) >= 7 and torch.equal(read.reshape(*lead, 7), r)
+            assert (s.residual == r.data_ptr()) == (r is whole or r is wide)
+    one = nv.MxEpilogue(residual=torch.zeros(5, 1, dtype=torch.bfloat16)[:1].expand(5, 1))
+    nv.mx_linear(torch.zeros(5, 64), operand(1), epilogue=one)
+    assert next(a for a in calls[-1][0] if isinstance(a, nv.layer._EpilogueT)).ld_residual == 1
+    out = torch.zeros(3, 7, dtype=torch.bfloat16)
+    nv.mx_linear(torch.zeros(3, 64), b, out=out, epilogue=nv.MxEpilogue(residual=out))      # (in place: never a copy)
+    assert next(a for a in calls[-1][0] if isinstance(a, nv.layer._EpilogueT)).residual == out.data_ptr()
