@@ -462,7 +462,7 @@ int nvfp4_mx_linear_fused(const void* x, int x_type, int64_t ldx, const void* b_
                           void* workspace, size_t workspace_bytes, void* stream) {
     // (one launch: 16 x 65536 x 8192 52 us, 57 + 2.7 in two.  Behind K = 8192 every
     // 16 columns quantise the rows again, about N K (6 + M) / 2e8 us)
-    if (M <= kMxQuantRows && (K <= 8192 || (double)N * K * (6 + M) <= 8e8))
+    if (M == 0 || (M <= kMxQuantRows && (K <= 8192 || (double)N * K * (6 + M) <= 8e8)))
         return nvfp4_mx_gemm_quantized_fused(x, x_type, ldx, b_packed, b_scales, alpha, epilogue, out, out_type,
                                              M, N, K, stream);
     size_t codes = 0, scales = 0;

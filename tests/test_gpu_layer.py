@@ -331,3 +331,14 @@ def test_broadcast_residuals():
         for r in (row.expand(*lead, 40), randn(g, *lead, 40, dtype=torch.bfloat16)[..., :1, :].expand(*lead, 40)):
             want = nv.mx_linear(x, b, epilogue=nv.MxEpilogue("silu", residual=r.contiguous()))
             assert torch.equal(nv.mx_linear(x, b, epilogue=nv.MxEpilogue("silu", residual=r)), want)
+
+
+@pytest.mark.parametrize("N,K", [(40, 64), (9000, 16384)])
+def test_linear_without_rows(N, K):
+    """An empty batch, also by a weight that more rows would take in two launches."""
+    g = gen(13)
+    w = nv.mx_quantize(randn(g, N, K, scale=0.06))
+    for lead in ((0,), (2, 0)):
+        x = torch.empty(*lead, K, dtype=torch.bfloat16, device=DEV)
+        out = nv.mx_linear(x, w, epilogue=nv.MxEpilogue("silu", bias=randn(g, N), gate=w))
+        assert out.shape == (*lead, N) and torch.equal(out, nv.mx_linear(x, w))

@@ -375,3 +375,14 @@ def test_broadcast_residuals_of_a_linear_layer_are_copied(monkeypatch):
     out = torch.zeros(3, 7, dtype=torch.bfloat16)
     nv.mx_linear(torch.zeros(3, 64), b, out=out, epilogue=nv.MxEpilogue(residual=out))      # (in place: never a copy)
     assert next(a for a in calls[-1][0] if isinstance(a, nv.layer._EpilogueT)).residual == out.data_ptr()
+
+
+def test_linear_without_rows():
+    """No rows: nothing to do and no workspace to do it in, whatever the weight's size (without a GPU the call comes as
+    far as looking for one)."""
+    L = nv.layer.layer_lib()
+    for N, K in ((4, 64), (9000, 16384), (131072, 8192)):
+        for e in (None, epi(2, P, P, P, P, 1, P, N)):
+            st = L.nvfp4_mx_linear_fused(None, 1, K, P, P, 1.0, e, None, 1, 0, N, K, None, 0, None)
+            assert st in (nv.OK, nv.ERR_HIP), (N, K)
+            assert L.nvfp4_mx_linear_fused(None, 1, K, P, P, 1.0, e, None, 1, 0, N, K - 16, None, 0, None) == INV
