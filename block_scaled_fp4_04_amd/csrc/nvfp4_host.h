@@ -92,8 +92,11 @@ hipError_t launch_job(const Job& job, int device, const WorkspacePtrs& ws, hipSt
 // Runs a prepared job eagerly on `stream` with that stream's workspace.
 int run_job(const Job& job, void* stream);
 
-// Appends a prepared job to a sequence (status: of its preparation, returned
-// if it is an error).
-int sequence_add(nvfp4_sequence* seq, int status, const Job& job);
+// Appends the prepared jobs of a call to a sequence, all or none (status: of their
+// preparation, returned if it is an error).
+int sequence_add(nvfp4_sequence* seq, int status, const Job* jobs, int count);
+inline int sequence_add(nvfp4_sequence* seq, int status, const Job& job) {
+    return sequence_add(seq, status, &job, 1);
+}
 
 }  // namespace nvfp4

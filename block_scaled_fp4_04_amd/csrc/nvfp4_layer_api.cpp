@@ -347,16 +347,15 @@ int nvfp4_sequence_add_mx_moe(nvfp4_sequence_t seq, const nvfp4_mx_experts* laye
                               int out_type, void* workspace, size_t workspace_bytes) {
     Job jobs[kMoeJobs];
     int count;
-    int st = prepare_mx_moe(layer, x, x_type, ldx, expert_ids, id_type, weights, tokens, topk, out, out_type,
-                            workspace, workspace_bytes, jobs, &count);
+    const int st = prepare_mx_moe(layer, x, x_type, ldx, expert_ids, id_type, weights, tokens, topk, out, out_type,
+                                  workspace, workspace_bytes, jobs, &count);
     if (count == 0) {  // refused, or no tokens: a call that does nothing
         jobs[0] = Job{};
         jobs[0].kind = JOB_LAUNCH;
         jobs[0].empty = true;
-        return sequence_add(seq, st, jobs[0]);
+        count = 1;
     }
-    for (int i = 0; i < count && st == NVFP4_OK; ++i) st = sequence_add(seq, st, jobs[i]);
-    return st;
+    return sequence_add(seq, st, jobs, count);
 }
 
 int nvfp4_add_norm(const nvfp4_norm* norm, const void* y, int64_t ld_y, const void* residual,

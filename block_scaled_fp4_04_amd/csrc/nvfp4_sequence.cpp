@@ -76,11 +76,13 @@ int capture(nvfp4_sequence* seq) {
 
 namespace nvfp4 {
 
-int sequence_add(nvfp4_sequence* seq, int status, const Job& job) {
+int sequence_add(nvfp4_sequence* seq, int status, const Job* jobs, int count) {
     if (!seq) return NVFP4_ERR_INVALID_VALUE;
     if (seq->finalized) return NVFP4_ERR_STATE;
+    if (status != NVFP4_OK) return status;
     try {
-        return add_job(seq, status, job);
+        seq->jobs.insert(seq->jobs.end(), jobs, jobs + count);  // (all or, without memory, none)
+        return NVFP4_OK;
     } catch (const std::bad_alloc&) {
         return NVFP4_ERR_ALLOC;
     }
