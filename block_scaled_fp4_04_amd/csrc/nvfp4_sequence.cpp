@@ -30,12 +30,6 @@ struct nvfp4_sequence {
 
 namespace {
 
-int add_job(nvfp4_sequence* seq, int status, const Job& job) {
-    if (status != NVFP4_OK) return status;
-    seq->jobs.push_back(job);
-    return NVFP4_OK;
-}
-
 void release(nvfp4_sequence* seq) {
     if (seq->exec) (void)hipGraphExecDestroy(seq->exec);
     if (seq->ws.partials) (void)hipFree(seq->ws.partials);
@@ -106,7 +100,7 @@ int nvfp4_sequence_add_gemm(nvfp4_sequence_t seq, const void* a_packed, const vo
     Job job;
     const int st = prepare_gemm(a_packed, a_scales, b_packed, b_scales, alpha, out, M, N, K,
                                 NVFP4_PATH_AUTO, 0, 0, &job);
-    return add_job(seq, st, job);
+    return sequence_add(seq, st, job);
 }
 
 int nvfp4_sequence_add_grouped_gemm(nvfp4_sequence_t seq, const void* a_packed,
@@ -119,7 +113,7 @@ int nvfp4_sequence_add_grouped_gemm(nvfp4_sequence_t seq, const void* a_packed,
     Job job;
     const int st = prepare_grouped(a_packed, a_scales, b_packed, b_scales, row_offsets, groups,
                                    alpha, out, M, N, K, NVFP4_PATH_AUTO, &job);
-    return add_job(seq, st, job);
+    return sequence_add(seq, st, job);
 }
 
 int nvfp4_sequence_add_quantize(nvfp4_sequence_t seq, const float* x, int64_t rows, int64_t K,
@@ -128,7 +122,7 @@ int nvfp4_sequence_add_quantize(nvfp4_sequence_t seq, const float* x, int64_t ro
     if (seq->finalized) return NVFP4_ERR_STATE;
     Job job;
     const int st = prepare_quantize(x, false, rows, K, ld, packed_codes, packed_scales, &job);
-    return add_job(seq, st, job);
+    return sequence_add(seq, st, job);
 }
 
 int nvfp4_sequence_add_gemm_quantized(nvfp4_sequence_t seq, const void* x, int x_type,
@@ -139,7 +133,7 @@ int nvfp4_sequence_add_gemm_quantized(nvfp4_sequence_t seq, const void* x, int x
     Job job;
     const int st = prepare_gemm_quantized(x, x_type, ldx, b_packed, b_scales, alpha, out, M, N, K,
                                           &job);
-    return add_job(seq, st, job);
+    return sequence_add(seq, st, job);
 }
 
 int nvfp4_sequence_add_quantize_bf16(nvfp4_sequence_t seq, const void* x, int64_t rows, int64_t K,
@@ -148,7 +142,7 @@ int nvfp4_sequence_add_quantize_bf16(nvfp4_sequence_t seq, const void* x, int64_
     if (seq->finalized) return NVFP4_ERR_STATE;
     Job job;
     const int st = prepare_quantize(x, true, rows, K, ld, packed_codes, packed_scales, &job);
-    return add_job(seq, st, job);
+    return sequence_add(seq, st, job);
 }
 
 int nvfp4_sequence_finalize(nvfp4_sequence_t seq) {

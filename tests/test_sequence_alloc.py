@@ -78,3 +78,28 @@ def build_and_run(tmp_path, main):
 
 def test_a_layer_of_experts_is_recorded_whole_or_not_at_all(tmp_path):
     build_and_run(tmp_path, MAIN)
+
+
+def test_recording_without_memory_is_an_error(tmp_path):
+    """Every call that records reports it: no exception leaves the library."""
+    body = r"""
+    for (int which = 0; which < 6; ++which) {
+        nvfp4_sequence_t s = nullptr;
+        CHECK(nvfp4_sequence_create(&s) == NVFP4_OK);
+        countdown = 0;
+        const int32_t* const off = static_cast<const int32_t*>(P);
+        const int st = which == 0 ? nvfp4_sequence_add_gemm(s, P, P, P, P, 1.0f, P, 16, 64, 128)
+                     : which == 1 ? nvfp4_sequence_add_grouped_gemm(s, P, P, P, P, off, 2, 1.0f, P, 16, 64, 128)
+                     : which == 2 ? nvfp4_sequence_add_quantize(s, static_cast<const float*>(P), 16, 128, 128, P, P)
+                     : which == 3 ? nvfp4_sequence_add_gemm_quantized(s, P, 1, 128, P, P, 1.0f, P, 1, 64, 128)
+                     : which == 4 ? nvfp4_sequence_add_quantize_bf16(s, P, 16, 128, 128, P, P) : moe(s, 4);
+        countdown = -1;
+        CHECK(st == NVFP4_ERR_ALLOC);
+        CHECK(nvfp4_sequence_finalize(s) == NVFP4_ERR_INVALID_VALUE);
+        CHECK(nvfp4_sequence_destroy(s) == NVFP4_OK);
+    }
+    std::printf("ok\n");
+    return 0;
+}
+"""
+    build_and_run(tmp_path, MAIN[:MAIN.index("    int failed = 0;")] + body)
