@@ -459,18 +459,32 @@ int nvfp4_mx_linear_fused(const void* x, int x_type, int64_t ldx, const void* b_
                           const void* b_scales, float alpha, const nvfp4_mx_epilogue* epilogue,
                           void* out, int out_type, int64_t M, int64_t N, int64_t K,
                           void* workspace, size_t workspace_bytes, void* stream) {
-    // (one launch: 16 x 65536 x 8192 52 us, 57 + 2.7 in two.  Behind K = 8192 every
-    // 16 columns quantise the rows again, about N K (6 + M) / 2e8 us)
-    if (M == 0 || (M <= kMxQuantRows && (K <= 8192 || (double)N * K * (6 + M) <= 8e8)))
+    size_t codes = 0, scales = 0;
+    const int st0 = nvfp4_mx_packed_size(M, K, &codes, &scales);
+    if (st0 != NVFP4_OK) return st0;
+    const bool room = workspace && workspace_bytes >= codes + scales;
+    // One launch where quantising again costs less than a launch of its own, 2.7 us.
+    // Up to K = 8192 each of the 256 workgroups quantises the rows once (16 x 65536 x
+    // 8192 52 us, 57 + 2.7 in two); behind it for every row block of B, and again of a
+    // gate, that it walks: 2e-5 us for each of the values.  One launch and two, us:
+    //                           K = 9984      16384         28672
+    //    1 row,  768 columns    4.9   7.1    5.9   8.2    7.6   9.8
+    //      with a gate          7.5   9.1    9.7  11.2   13.2  14.7
+    //    4 rows                 5.3   7.4    6.8   8.6    9.0  10.6
+    //      with a gate          8.2   9.5   11.0  11.9   15.8  16.2
+    //   16 rows                 8.6   7.9   12.0   9.3   18.2  12.2
+    //      with a gate         15.5  10.9   21.9  13.6   34.4  19.6
+    //    4 rows, 4608 columns   8.6  11.3   13.3  15.2   20.5  21.7
+    //      with a gate         17.3  17.7   24.3  24.5   36.3  35.3
+    const bool gate = epilogue && epilogue->gate_packed;
+    const double again = 2e-5 * (gate ? 2 : 1) * (double)M * K * (double)((mx_row_blocks(N) + 255) / 256);
+    if (M <= kMxQuantRows && (!room || K <= 8192 || again <= 2.7))
         return nvfp4_mx_gemm_quantized_fused(x, x_type, ldx, b_packed, b_scales, alpha, epilogue, out, out_type,
                                              M, N, K, stream);
-    size_t codes = 0, scales = 0;
-    int st = nvfp4_mx_packed_size(M, K, &codes, &scales);
-    if (st != NVFP4_OK) return st;
-    if (!workspace || workspace_bytes < codes + scales) return NVFP4_ERR_INVALID_VALUE;
+    if (!room) return NVFP4_ERR_INVALID_VALUE;
     uint8_t* const w = static_cast<uint8_t*>(workspace);
     Job quantize, product;
-    st = prepare_mx_quantize(false, x, x_type, 1, 0, M, K, ldx, w, w + codes, &quantize);
+    int st = prepare_mx_quantize(false, x, x_type, 1, 0, M, K, ldx, w, w + codes, &quantize);
     if (st == NVFP4_OK)
         st = prepare_gemm_fused(w, w + codes, b_packed, b_scales, alpha, epilogue, out, out_type, M, N, K, &product);
     if (st == NVFP4_OK) st = run_job(quantize, stream);

@@ -69,10 +69,10 @@ int nvfp4_mx_grouped_gemm_fused(const void* a_packed, const void* a_scales, int6
                                 int64_t M, int64_t N, int64_t K, void* stream);
 
 /* nvfp4_mx_quantize and nvfp4_mx_gemm_fused in one call, or nvfp4_mx_gemm_quantized_fused
- * where that is faster (up to 16 rows, but for very wide and deep B); the same bits.
+ * where that is faster (up to 16 rows, but for many of them by deep B); the same bits.
  *   workspace : DEVICE, 16-byte aligned, for the packed rows: the code and scale bytes that
- *               nvfp4_mx_packed_size(M, K) says, added up; not used (and may be NULL) in the
- *               one-launch form.  Free again when the call's work is done. */
+ *               nvfp4_mx_packed_size(M, K) says, added up.  Free again when the call's work is
+ *               done.  Up to 16 rows it may be NULL or smaller: they then take one launch. */
 int nvfp4_mx_linear_fused(const void* x, int x_type, int64_t ldx, const void* b_packed,
                           const void* b_scales, float alpha, const nvfp4_mx_epilogue* epilogue,
                           void* out, int out_type, int64_t M, int64_t N, int64_t K,

@@ -342,3 +342,25 @@ def test_linear_without_rows(N, K):
         x = torch.empty(*lead, K, dtype=torch.bfloat16, device=DEV)
         out = nv.mx_linear(x, w, epilogue=nv.MxEpilogue("silu", bias=randn(g, N), gate=w))
         assert out.shape == (*lead, N) and torch.equal(out, nv.mx_linear(x, w))
+
+
+@pytest.mark.parametrize("M,K,gate,two", [(1, 9984, True, False), (4, 9984, True, False), (16, 8192, True, False), (16, 9984, True, True),
+                                          (8, 9984, False, False), (8, 9984, True, True), (1, 28672, True, False), (4, 28672, True, True)])
+def test_linear_of_few_deep_rows(M, K, gate, two):
+    """Rows that one launch would quantise often, twice as often with a gate, are quantised once, in the workspace; the
+    same bits, and without a workspace too."""
+    import ctypes
+    N, g = 768, gen(K + M)
+    x = randn(g, M, K, dtype=torch.bfloat16)
+    w, v = nv.mx_quantize(randn(g, N, K, scale=0.06)), nv.mx_quantize(randn(g, N, K, scale=0.06))
+    want = nv.mx_gemm(nv.mx_quantize(x), w, epilogue=nv.MxEpilogue("silu", gate=v if gate else None))
+    e = nv.layer._EpilogueT(2, v.codes.data_ptr() if gate else None, v.scales.data_ptr() if gate else None)
+    size = sum(nv.mx_packed_size(M, K))
+    work = torch.full((size,), 0xAA, dtype=torch.uint8, device=DEV)
+    for ws, n in ((work.data_ptr(), size), (None, 0)):
+        out = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device=DEV)
+        st = nv.layer.layer_lib().nvfp4_mx_linear_fused(x.data_ptr(), 1, K, w.codes.data_ptr(), w.scales.data_ptr(), 1.0,
+                                                        ctypes.byref(e), out.data_ptr(), 1, M, N, K, ws, n,
+                                                        torch.cuda.current_stream().cuda_stream)
+        assert st == nv.OK and torch.equal(out, want)
+    assert bool((work != 0xAA).any()) == two

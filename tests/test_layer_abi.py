@@ -386,3 +386,15 @@ def test_linear_without_rows():
             st = L.nvfp4_mx_linear_fused(None, 1, K, P, P, 1.0, e, None, 1, 0, N, K, None, 0, None)
             assert st in (nv.OK, nv.ERR_HIP), (N, K)
             assert L.nvfp4_mx_linear_fused(None, 1, K, P, P, 1.0, e, None, 1, 0, N, K - 16, None, 0, None) == INV
+
+
+def test_linear_of_few_rows_needs_no_workspace():
+    """Up to 16 rows run without one, whatever the weight's size (without a GPU the call comes as far as looking for one)."""
+    L = nv.layer.layer_lib()
+    for M, N, K in ((1, 4, 64), (16, 9000, 16384), (16, 768, 9984), (5, 131072, 8224)):
+        for e in (None, epi(2, P, P, P, P, 1, P, N)):
+            for ws, n in ((None, 0), (P, sum(nv.mx_packed_size(M, K)) - 1)):
+                if torch.cuda.is_available():
+                    continue    # (the addresses stand for nothing)
+                assert L.nvfp4_mx_linear_fused(P, 1, K, P, P, 1.0, e, P, 1, M, N, K, ws, n, None) == nv.ERR_HIP, (M, N, K)
+    assert L.nvfp4_mx_linear_fused(P, 1, 64, P, P, 1.0, None, P, 1, 17, 4, 64, None, 0, None) == INV
