@@ -893,6 +893,7 @@ void run_small_tiles(Launch<EPI>& l) {
 
 template <int EPI>
 void choose(Launch<EPI>& l) {
+    constexpr bool GATED = EPI == EPI_GATED;
     const MxGemmArgs& a = l.a;
     const int64_t M = a.M, N = (int64_t)a.N * l.kWeights, G = a.groups;
     const int64_t row_blocks = (int64_t)a.RBb * l.kWeights;
@@ -936,8 +937,10 @@ void choose(Launch<EPI>& l) {
         return weights > kStreamBytes ? run_skinny<1, A_PACKED, false, true>(l) : run_skinny<1, A_PACKED, false>(l);
     }
     // Up to 64 rows while its workgroups fit the GPU at once (64 x 768: 5.3
-    // against 7.4 us; 64 x 6144: 14.0 against 8.8).
-    if ((M <= 64 && (M + 31) / 32 * row_blocks <= 256) || a.C > kMxTileSteps) return run_skinny<2, A_PACKED, false>(l);
+    // against 7.4 us; 64 x 6144: 14.0 against 8.8).  With a gate it would walk K
+    // twice: 64 x 768 4.9 us with 64 x 64 tiles, 5.5 so (K = 2048), 7.5 and 8.3 (6144), 13.6
+    // and 15.6 (16384).
+    if ((!GATED && M <= 64 && (M + 31) / 32 * row_blocks <= 256) || a.C > kMxTileSteps) return run_skinny<2, A_PACKED, false>(l);
     // The smallest tiles that one round of the 256 CUs holds (256 x 4096 x 4096,
     // 256 tiles of 64 x 64: 7.9 us, 9.6 with 64 x 128; 400 x 4096 x 4096, 224 of
     // 64 x 128: 9.0, 10.3 with 64 x 64, 10.6 with 128 x 128).
@@ -948,7 +951,11 @@ void choose(Launch<EPI>& l) {
     // 71 and 67), unless they would be half empty (128 x 65536 x 8192: 71, 61 with
     // 128 x 128).
     const int64_t large = tiles(256, 256);
-    if (M > 128 && large >= 256 && (a.C > 32 || large >= 1024)) return run_tile<256, 256, 4, 2, 1, false>(l);
+    // With a gate 128 x 256 up to K = 8192, two to a CU, so that one's epilogue runs
+    // beside the other's products (us with 256 x 256 and so: 8192 x 4096 x 2048 99 and 80,
+    // 3000 x 3000 x 6144 84 and 67, 8192 x 8192 x 4096 292 and 259, 16384 x 4096 x 8192
+    // 489 and 480; 8192 x 4096 x 12288 344 and 350).
+    if (M > 128 && large >= 256 && (GATED ? a.C > 64 : a.C > 32 || large >= 1024)) return run_tile<256, 256, 4, 2, 1, false>(l);
     // 128 x 256, two to a CU, unless a few of them need a second round (256 x
     // 32768 x 8192, 256 tiles: 44 us, 49 with 128 x 128; 2048 x 6144 x 6144, 384: 44
     // and 46; 3000 x 3000 x 6144, 288: 39 and 37; 1237 x 2056 x 6112, 90: 21 and 15).

@@ -364,3 +364,19 @@ def test_linear_of_few_deep_rows(M, K, gate, two):
                                                         torch.cuda.current_stream().cuda_stream)
         assert st == nv.OK and torch.equal(out, want)
     assert bool((work != 0xAA).any()) == two
+
+
+@pytest.mark.parametrize("M,N,K", [(17, 40, 160), (64, 768, 2080), (33, 300, 9024),      # 64 x 64, with one and two teams
+                                   (1500, 2051, 224), (4100, 2051, 8192),                # 128 x 256
+                                   (4100, 2051, 8224)])                                  # 256 x 256
+def test_gated_product_by_size(M, N, K):
+    """The sizes at which a gated product takes another kernel than the plain one."""
+    say(f"gated {M}x{N}x{K}")
+    g = gen(M + K)
+    for dtype in DT.values():
+        a, b = nv.mx_quantize(randn(g, M, K)), nv.mx_quantize(randn(g, N, K, scale=0.06))
+        p = parts(g, M, N, dtype, True, True, True, K=K)
+        out = nv.mx_gemm(a, b, 0.75, dtype=dtype, epilogue=nv.MxEpilogue("silu", **p))
+        want, d = expected(values(a), values(b), p, "silu", 0.75)
+        r = p["residual"].double()
+        ref.check(out, want + r, d + 2 * ref.U * ((want + r).abs() + d), f"{M}x{N}x{K}")
