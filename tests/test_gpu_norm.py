@@ -397,3 +397,16 @@ def test_a_gate_of_mode_none_is_not_read():
             args = (ctypes.byref(spec), y.data_ptr(), 200, res.data_ptr(), 200, h.data_ptr(), n.data_ptr(), None, None)
             assert L.nvfp4_add_norm(*args, torch.cuda.current_stream().cuda_stream) == nv.OK
             assert torch.equal(h, want_h) and torch.equal(n, want_n)
+
+
+@pytest.mark.parametrize("H", [7, 640, 16384])
+@pytest.mark.parametrize("eps", [0.0, 0.9e-30, 1e-30, 1e-29])
+def test_small_rows_beside_a_small_eps(eps, H):
+    """Squares that the scale makes subnormal do not count beside the eps that they are scaled for."""
+    g = gen(H)
+    x = randn(g, 40, H) * torch.exp2(torch.linspace(-58, -40, 40, device=DEV))[:, None]
+    dn = randn(g, 40, H)
+    n = nv.rms_norm(x, eps=eps)
+    ref.check(n, *ref.norm_n(x.double(), None, eps), f"{H} {eps}")
+    how = dict(post=False, post_weight=None, gate=None, pre_weight=torch.ones(H, device=DEV), scale=1.0, residual_scale=1.0, eps=eps)
+    check_grads(None, dn, x, x, how, nv.add_norm_grad(None, dn, x, x, **how), f"{H} {eps}")
