@@ -12,8 +12,9 @@
 // the one that is multiplied, also past the end of a task.
 // x, and in the second launch h, are quantised by every workgroup into an
 // image in its LDS, while its first weights are on their way.  256 experts x
-// 256 x 6144, top 8, both launches: 1 token 12.5 us (30 from the calls for more
-// tokens), 2 tokens 16.2 (33), 4 tokens 23.1 (39): 70 MB of weights, 3.0 TB/s.
+// 256 x 6144, top 8, both launches, weights from the last-level cache: 1 token 11 us
+// (14.4 from memory, 20 MB), 2 tokens 15, 4 tokens 24 (75 MB, 3.2 TB/s); 5 tokens by the
+// calls for more 39.
 #include "nvfp4_mx_parts.h"
 
 #include <algorithm>

@@ -24,10 +24,11 @@
 //   dy         = ry * (v - y * ry * mean(v * y * ry))
 // (rh goes with h and ry with y: their cubes leave fp32's normal range from an
 // rms of 2^42 on, and below 2^-42)
-// 8192 x 2048 bfloat16 with all parts 50 us and 5 for the sums' second launch,
-// 3.6 TB/s: 16 waves a CU at 128 registers.  The next row's loads ahead of the
-// sums spilled (78 us); pieces of 8 bytes at twice the waves spilled (106);
-// two workgroups of 8 waves a CU 55.6.
+// 8192 x 2048 bfloat16 with all parts 49 us, 4.1 TB/s, and 5 for the sums' second
+// launch: 16 waves a CU at 128 registers.  (Of a form that took 50: the next row's
+// loads ahead of the sums spilled, 78 us; pieces of 8 bytes at twice the waves
+// spilled, 106; two workgroups of 8 waves a CU 55.6.)  Rows of more than 8192 elements
+// spill: 4096 x 9000 bfloat16 584 us.
 // Sums over rows: a workgroup keeps those of its rows in registers, adds its
 // teams' through LDS and leaves them in the workspace, and a second launch
 // adds the workgroups' in order: no atomics, the same bits every time.
@@ -158,7 +159,7 @@ struct Squares {
 // A workgroup takes a row at a time; or, if one wave holds a row, four.
 // ELEMENT: a gate for every element; else one for every channel (ones).  The
 // bound on registers lets two workgroups of 12 waves share a CU (six waves a
-// SIMD: 263 -> 206 us for the call above, the rate of a copy).
+// SIMD: 263 -> 206 us for the call above, now 189, 5.3 TB/s).
 template <typename T, int V, int P, bool ODD, bool POST, bool ELEMENT, bool WB>
 __global__ void __launch_bounds__(1024, P == 1 ? 6 : 4) norm_kernel(NormArgs a, int64_t rows_out, int waves) {
     __shared__ float part[2][16][1];
