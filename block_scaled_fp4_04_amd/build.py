@@ -21,7 +21,8 @@ SOURCES = [os.path.join(CSRC, "nvfp4_api.cpp"), os.path.join(CSRC, "nvfp4_plan.c
            os.path.join(CSRC, "nvfp4_mx_quantize.hip"), os.path.join(CSRC, "nvfp4_mx_gemm.hip"),
            os.path.join(CSRC, "nvfp4_moe.hip")]
 # the operators around the products of a layer (include/nvfp4_layer.h)
-LAYER_SOURCES = [os.path.join(CSRC, f) for f in ("nvfp4_layer_api.cpp", "nvfp4_mx_fused.hip", "nvfp4_mx_gated.hip",
+LAYER_SOURCES = [os.path.join(CSRC, f) for f in ("nvfp4_layer_api.cpp", "nvfp4_mx_fused.hip",
+                                                 "nvfp4_mx_fused_grouped.hip", "nvfp4_mx_gated.hip",
                                                  "nvfp4_mx_moe.hip", "nvfp4_mx_short.hip", "nvfp4_norm.hip",
                                                  "nvfp4_norm_bf16.hip", "nvfp4_norm_f32.hip",
                                                  "nvfp4_norm_grad_bf16.hip", "nvfp4_norm_grad_f32.hip")]

@@ -96,12 +96,14 @@ hipError_t launch_mx_gemm(const MxGemmArgs& a, hipStream_t stream);
 bool mx_gemm_fits(const MxGemmArgs& a);
 // The same with an epilogue.
 hipError_t launch_mx_fused(const MxGemmArgs& a, const MxEpilogueArgs& e, hipStream_t stream);
+hipError_t launch_mx_fused_grouped(const MxGemmArgs& a, const MxEpilogueArgs& e, hipStream_t stream);  // its part for groups
 hipError_t launch_mx_gated(const MxGemmArgs& a, const MxEpilogueArgs& e, hipStream_t stream);
 // Grouped, rows of A in order, up to four steps and kMoeMaxExperts groups, a bias at most.
 hipError_t launch_mx_short(const MxGemmArgs& a, const MxEpilogueArgs& e, hipStream_t stream);
 bool mx_fused_fits(const MxGemmArgs& a);
+bool mx_fused_grouped_fits(const MxGemmArgs& a);
 bool mx_gated_fits(const MxGemmArgs& a);
-// Whether the kernel that the sizes choose writes C packed.
+// Whether the kernel that the sizes of a grouped product choose writes C packed.
 bool mx_fused_packs(const MxGemmArgs& a);
 bool mx_gated_packs(const MxGemmArgs& a);
 

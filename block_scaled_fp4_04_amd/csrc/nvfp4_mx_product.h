@@ -891,39 +891,47 @@ void run_small_tiles(Launch<EPI>& l) {
     return run_tile<64, 64, 4, 2, 2, GROUPED>(l);
 }
 
+// (A bound on the) tiles of rows x cols.
 template <int EPI>
-void choose(Launch<EPI>& l) {
-    constexpr bool GATED = EPI == EPI_GATED;
+int64_t tiles_of(const Launch<EPI>& l, int64_t rows, int64_t cols) {
+    const int64_t M = l.a.M, N = (int64_t)l.a.N * l.kWeights;
+    return ((M + rows - 1) / rows + std::min<int64_t>(l.a.groups, M)) * ((N + cols - 1) / cols);
+}
+
+template <int EPI>
+void choose_grouped(Launch<EPI>& l) {
     const MxGemmArgs& a = l.a;
     const int64_t M = a.M, N = (int64_t)a.N * l.kWeights, G = a.groups;
-    const int64_t row_blocks = (int64_t)a.RBb * l.kWeights;
-    // (a bound on the) tiles of rows x cols
-    auto tiles = [&](int64_t rows, int64_t cols) {
-        return ((M + rows - 1) / rows + std::min(G, M)) * ((N + cols - 1) / cols);
-    };
-    if (G > 0) {
-        // the tile kernel addresses A with 32-bit offsets and numbers row blocks in 32 bits
-        if (a.C > kMxTileSteps || M >= 1 << 28 || (int64_t)a.RBa * a.C * kMxFrag >= (int64_t)1 << 31)
-            return run_skinny<2, A_PACKED, true>(l);
-        // Few tiles, so that one tile's time counts (8 experts x 2048 columns,
-        // 16 rows each: 13.4 us, 18.1 with 64 x 256 tiles); about even at 64
-        // experts x 512 x K 2048 with 16 rows (640 tiles).
-        if (tiles(64, 64) <= 640) return run_small_tiles<true>(l);
-        // From 128 rows each (dropped ones among them), larger tiles read the
-        // weights less often (256 experts x 256 columns, 128 rows: 73 us, 77 with
-        // one token less and 64 x 256 tiles, in three runs; 16 x 2048 x K 2048,
-        // 1024 rows: 56 against 64), if they are enough to fill the GPU or the
-        // weights come from memory (8 x 2048, 256 rows: 27 against 33; but 4 x
-        // 768, 1024 rows: 25 against 20).
-        const int64_t weights = G * row_blocks * a.C * kMxFrag;
-        if (M >= 128 * G && (tiles(128, 256) >= 256 || weights >= 32 << 20))
-            return run_tile<128, 256, 3, 2, 1, true>(l);
-        // 64 x 256 tiles stream the weights of small groups at the memory's
-        // rate (256 experts x 256 columns, 16 rows: 39 us, 49 with 128 x 128);
-        // narrow weights would leave them half empty.
-        if (N <= 128) return run_tile<128, 128, 4, 2, 1, true>(l);
-        return run_tile<64, 256, 3, 1, 1, true>(l);
-    }
+    auto tiles = [&](int64_t rows, int64_t cols) { return tiles_of(l, rows, cols); };
+    // the tile kernel addresses A with 32-bit offsets and numbers row blocks in 32 bits
+    if (a.C > kMxTileSteps || M >= 1 << 28 || (int64_t)a.RBa * a.C * kMxFrag >= (int64_t)1 << 31)
+        return run_skinny<2, A_PACKED, true>(l);
+    // Few tiles, so that one tile's time counts (8 experts x 2048 columns,
+    // 16 rows each: 13.4 us, 18.1 with 64 x 256 tiles); about even at 64
+    // experts x 512 x K 2048 with 16 rows (640 tiles).
+    if (tiles(64, 64) <= 640) return run_small_tiles<true>(l);
+    // From 128 rows each (dropped ones among them), larger tiles read the
+    // weights less often (256 experts x 256 columns, 128 rows: 73 us, 77 with
+    // one token less and 64 x 256 tiles, in three runs; 16 x 2048 x K 2048,
+    // 1024 rows: 56 against 64), if they are enough to fill the GPU or the
+    // weights come from memory (8 x 2048, 256 rows: 27 against 33; but 4 x
+    // 768, 1024 rows: 25 against 20).
+    const int64_t weights = G * a.RBb * l.kWeights * a.C * kMxFrag;
+    if (M >= 128 * G && (tiles(128, 256) >= 256 || weights >= 32 << 20))
+        return run_tile<128, 256, 3, 2, 1, true>(l);
+    // 64 x 256 tiles stream the weights of small groups at the memory's
+    // rate (256 experts x 256 columns, 16 rows: 39 us, 49 with 128 x 128);
+    // narrow weights would leave them half empty.
+    if (N <= 128) return run_tile<128, 128, 4, 2, 1, true>(l);
+    return run_tile<64, 256, 3, 1, 1, true>(l);
+}
+
+template <int EPI>
+void choose_single(Launch<EPI>& l) {
+    constexpr bool GATED = EPI == EPI_GATED;
+    const MxGemmArgs& a = l.a;
+    const int64_t M = a.M, row_blocks = (int64_t)a.RBb * l.kWeights;
+    auto tiles = [&](int64_t rows, int64_t cols) { return tiles_of(l, rows, cols); };
     const int64_t weights = row_blocks * ((int64_t)a.C * kMxFrag + (a.C + 3) / 4 * kMxScaleFrag);
     if (!a.a_codes) {  // (1 x 131072 x 8192: 98 -> 87 us with the weights non-temporal)
         if (weights > kStreamBytes) return a.x_bf16 ? run_skinny<1, A_BF16, false, true>(l) : run_skinny<1, A_F32, false, true>(l);
@@ -962,6 +970,14 @@ void choose(Launch<EPI>& l) {
     const int64_t wide = tiles(128, 256);
     if (wide >= 360 || (wide >= 180 && wide <= 256)) return run_tile<128, 256, 3, 2, 1, false>(l);
     run_tile<128, 128, 4, 2, 1, false>(l);
+}
+
+template <int EPI>
+void choose(Launch<EPI>& l) {
+    if (l.a.groups > 0)
+        choose_grouped(l);
+    else
+        choose_single(l);
 }
 
 }  // namespace
